@@ -532,6 +532,135 @@ int zero_checkpoint_save(const zero_plan_t* plan, int32_t rank, const char* path
 int zero_checkpoint_load(const zero_plan_t* plan, int32_t rank, const char* path, int32_t state_layout,
                          float* master, float* m, float* v, zero_ckpt_meta_t* meta, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The model's input layer: embedding, its gradient, dropout (device)         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Dropout from a counter-based generator; the mask is never stored.  Whether
+ * element (row, col) of a [rows, cols] matrix is kept is a function of its
+ * place alone, so the backward pass, a recomputed forward pass and any split
+ * of a batch over micro-batches or ranks draw the same mask:
+ *   (w0, w1, w2, w3) = Philox4x32-10 (Salmon et al., "Parallel random numbers:
+ *       as easy as 1, 2, 3", SC'11) with key = (seed & 0xffffffff, seed >> 32) and
+ *       counter = (col / 8, row0 + row, step & 0xffffffff, site);
+ *   u = the 16-bit half (col % 2) of word (col % 8) / 2, low half first;
+ *   kept  <=>  u >= D,  D = p * 65536 rounded to the nearest integer (ties to even).
+ * A kept value is multiplied by 65536 / (65536 - D) (the exact inverse of the
+ * share kept, rounded once to fp32), a dropped one becomes 0 whatever it was
+ * (an infinity or NaN there does not reach the result).  D = 0 (p < 2^-17)
+ * keeps everything; D = 65536 (p = 1) drops everything.
+ *
+ * step_dev: the step number is read from this device int64 (8-byte aligned) at
+ * run time instead of `step`, so that a captured graph draws a new mask on
+ * every replay; &ctl->step of a zero_step_ctl_t counts the steps applied.
+ */
+typedef struct zero_drop {
+  double p;                /* 0 <= p <= 1                                        */
+  uint64_t seed;
+  uint32_t site;           /* tells the model's dropouts of one step apart       */
+  uint32_t reserved;       /* 0                                                  */
+  int64_t step;            /* 0 <= step < 2^32, unused with step_dev             */
+  const int64_t* step_dev; /* or NULL                                            */
+  int64_t row0;            /* place of row 0 in the whole batch; row0 + rows <= 2^32 */
+} zero_drop_t;
+
+/*
+ * out = kept ? x * ks : 0, plus the residual if there is one (element by element, in
+ * fp32, rounded once to out_dtype).  The backward pass is the same call on the
+ * output's gradient, without a residual.
+ *
+ * x [rows, cols] of x_dtype, out and residual (or NULL) [rows, cols] of
+ * out_dtype; rows ld_x, ld_out, ld_res elements apart, columns adjacent.  Element
+ * alignment suffices.  out may be x itself (same address, stride and type) or
+ * the residual itself; any other overlap is refused.  1 <= cols < 2^31.
+ * drop == NULL: nothing is dropped.  rows == 0: nothing to do.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
+ */
+int zero_dropout(const void* x, int64_t ld_x, zero_dtype_t x_dtype, const void* residual, int64_t ld_res,
+                 void* out, int64_t ld_out, zero_dtype_t out_dtype, int64_t rows, int64_t cols,
+                 const zero_drop_t* drop, void* stream);
+
+/* Arguments of zero_embed_lookup (host struct; pointers are device addresses). */
+typedef struct zero_embed_args {
+  const void* table;       /* row of id i at table + (i - id0) * ld_table elements */
+  int64_t ld_table;
+  int64_t rows;            /* rows of the table held here; may be 0                */
+  int64_t id0;             /* id of its first row                                  */
+  zero_dtype_t table_dtype;
+  int32_t id_bytes;        /* 4 or 8: ids and pos are int32 or int64               */
+  const void* ids;         /* [n_ids]                                              */
+  int64_t n_ids;
+  int64_t dim;             /* 1 <= dim < 2^31                                      */
+  float scale;
+  /* optional second table, added unscaled: row pos[t], or t % pos_period where
+   * pos is NULL (1 <= pos_period); type table_dtype                               */
+  const void* pos_table;
+  int64_t ld_pos;
+  int64_t pos_rows;
+  const void* pos;
+  int64_t pos_period;
+  void* out;               /* [n_ids, dim], rows ld_out elements apart             */
+  int64_t ld_out;
+  zero_dtype_t out_dtype;
+  const zero_drop_t* drop; /* or NULL; row = t, col = the column                   */
+} zero_embed_args_t;
+
+/*
+ * out[t, :] = dropout(scale * table[ids[t] - id0, :] + pos_table[pos[t], :]),
+ * in fp32 and rounded once to out_dtype.  An id outside [id0, id0 + rows) adds
+ * a row of zeros (padding ids; the rows of the other ranks where a table is split by
+ * rows, whose outputs then add up), and so does a position outside [0, pos_rows).
+ * The tables may sit anywhere in the gather buffer: element alignment suffices.
+ * out must not overlap an input.  n_ids == 0: nothing to do.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
+ */
+int zero_embed_lookup(const zero_embed_args_t* args, void* stream);
+
+/* Arguments of zero_embed_grad (host struct; pointers are device addresses). */
+typedef struct zero_embed_grad_args {
+  const void* dy;          /* [n_ids, dim], rows ld_dy elements apart              */
+  int64_t ld_dy;
+  zero_dtype_t dy_dtype;
+  int32_t id_bytes;        /* 4 or 8: int32 or int64 ids                           */
+  const void* ids;         /* [n_ids]; NULL: id of t = t % period                  */
+  int64_t period;          /* >= 1 where ids is NULL                               */
+  int64_t n_ids;           /* < 2^31                                               */
+  int64_t dim;             /* 1 <= dim < 2^31                                      */
+  int64_t id0;             /* id of the gradient's first row                       */
+  int64_t rows;            /* rows of the gradient, < 2^31                         */
+  float scale;
+  zero_dtype_t grad_dtype;
+  void* grad;              /* [rows, dim], rows ld_grad elements apart             */
+  int64_t ld_grad;
+  int32_t accumulate;      /* nonzero: add to what grad holds                      */
+  const zero_drop_t* drop; /* the drop of the lookup, or NULL                      */
+  void* ws;                /* zero_embed_grad_ws_bytes() bytes, 16-byte aligned    */
+  int64_t ws_bytes;
+} zero_embed_grad_args_t;
+
+/*
+ * The gradient of zero_embed_lookup in its table: row v gets
+ *   scale * sum over t with ids[t] == id0 + v of dropout'(dy[t, :]),
+ * where dropout' keeps and scales the elements that the lookup kept.  Sums are fp32
+ * in an order that depends on the arguments' sizes and the ids alone (no
+ * floating-point atomics: the same call gives the same bits), rounded once.
+ * accumulate == 0: every row is written, rows without an id with zeros.
+ * accumulate != 0: rows without an id are neither read nor written; the others
+ * add the sum to what they hold (in fp32, rounded once), as for an output head
+ * that shares the table.  Ids outside [id0, id0 + rows) are left out.
+ * ids == NULL is the gradient of a table of positions (pos == NULL in the lookup).
+ *
+ * The gradient's place is a tensor of a flat gradient buffer, such as the step reads
+ * with ZERO_GRAD_FULL: element alignment suffices.  ws needs no initial content
+ * and must not be shared by calls that overlap in time.  grad and ws must not overlap
+ * an input or each other.
+ * zero_embed_grad_ws_bytes: the bytes ws needs; 0 if an argument is out of range.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
+ */
+int64_t zero_embed_grad_ws_bytes(int64_t n_ids, int64_t rows, int64_t dim);
+int zero_embed_grad(const zero_embed_grad_args_t* args, void* stream);
+
 /*
  * A plain streaming copy of `bytes` bytes from src to dst (device pointers,
  * both 16-byte aligned, bytes a multiple of 16, no overlap), with the step's

@@ -13,7 +13,8 @@ from ._abi import (DTYPE_BYTES, DTYPE_CODES, EXPORTS, ZERO_BF16, ZERO_EALIGN, ZE
                    zero_checkpoint_load, zero_checkpoint_save, zero_ckpt_meta_t, zero_last_error,
                    zero_plan_hash, zero_reduce_shard, zero_scaler_t, zero_shard_norm, zero_step_ctl_t,
                    zero_stream_copy, zero_version, ZERO_NOALLOC_SCRATCH_BYTES, zero_noalloc_max_shard,
-                   zero_reduce_norm_noalloc)
+                   zero_reduce_norm_noalloc, zero_drop_t, zero_dropout, zero_embed_args_t, zero_embed_grad,
+                   zero_embed_grad_args_t, zero_embed_grad_ws_bytes, zero_embed_lookup)
 
 __all__ = [
     "DTYPE_BYTES", "DTYPE_CODES", "EXPORTS", "ZERO_BF16", "ZERO_EALIGN", "ZERO_EHIP", "ZERO_EINVAL",
@@ -23,4 +24,6 @@ __all__ = [
     "zero_checkpoint_save", "zero_ckpt_meta_t", "zero_last_error", "zero_plan_hash",
     "zero_reduce_shard", "zero_scaler_t", "zero_shard_norm", "zero_step_ctl_t", "zero_stream_copy",
     "zero_version", "ZERO_NOALLOC_SCRATCH_BYTES", "zero_noalloc_max_shard", "zero_reduce_norm_noalloc",
+    "zero_drop_t", "zero_dropout", "zero_embed_args_t", "zero_embed_grad", "zero_embed_grad_args_t",
+    "zero_embed_grad_ws_bytes", "zero_embed_lookup",
 ]

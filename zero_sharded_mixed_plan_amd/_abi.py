@@ -31,6 +31,7 @@ EXPORTS = [
     "zero_reduce_shard", "zero_shard_norm", "zero_noalloc_max_shard", "zero_reduce_norm_noalloc",
     "zero_adam_step", "zero_scaler_init", "zero_scaler_update", "zero_scaler_inv_scale", "zero_plan_hash",
     "zero_checkpoint_save", "zero_checkpoint_load", "zero_stream_copy", "zero_last_error", "zero_version",
+    "zero_dropout", "zero_embed_lookup", "zero_embed_grad", "zero_embed_grad_ws_bytes",
 ]
 
 
@@ -100,6 +101,65 @@ class zero_ckpt_meta_t(ctypes.Structure):
     _fields_ = [("step", ctypes.c_int64), ("scaler", zero_scaler_t)]
 
 
+class zero_drop_t(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_double),
+        ("seed", ctypes.c_uint64),
+        ("site", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+        ("step", ctypes.c_int64),
+        ("step_dev", ctypes.c_void_p),
+        ("row0", ctypes.c_int64),
+    ]
+
+
+class zero_embed_args_t(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("id0", ctypes.c_int64),
+        ("table_dtype", ctypes.c_int),
+        ("id_bytes", ctypes.c_int32),
+        ("ids", ctypes.c_void_p),
+        ("n_ids", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("pos_table", ctypes.c_void_p),
+        ("ld_pos", ctypes.c_int64),
+        ("pos_rows", ctypes.c_int64),
+        ("pos", ctypes.c_void_p),
+        ("pos_period", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int),
+        ("drop", ctypes.c_void_p),
+    ]
+
+
+class zero_embed_grad_args_t(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("ld_dy", ctypes.c_int64),
+        ("dy_dtype", ctypes.c_int),
+        ("id_bytes", ctypes.c_int32),
+        ("ids", ctypes.c_void_p),
+        ("period", ctypes.c_int64),
+        ("n_ids", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("id0", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("grad_dtype", ctypes.c_int),
+        ("grad", ctypes.c_void_p),
+        ("ld_grad", ctypes.c_int64),
+        ("accumulate", ctypes.c_int32),
+        ("drop", ctypes.c_void_p),
+        ("ws", ctypes.c_void_p),
+        ("ws_bytes", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -156,6 +216,10 @@ def load(path: str, required: bool = True) -> ctypes.CDLL:
         "zero_checkpoint_load": (ctypes.c_int, [vp, i32, ctypes.c_char_p, i32, vp, vp, vp,
                                                 ctypes.POINTER(zero_ckpt_meta_t), vp]),
         "zero_stream_copy": (ctypes.c_int, [vp, vp, i64, vp]),
+        "zero_dropout": (ctypes.c_int, [vp, i64, ctypes.c_int, vp, i64, vp, i64, ctypes.c_int, i64, i64, vp, vp]),
+        "zero_embed_lookup": (ctypes.c_int, [vp, vp]),
+        "zero_embed_grad": (ctypes.c_int, [vp, vp]),
+        "zero_embed_grad_ws_bytes": (i64, [i64, i64, i64]),
         "zero_last_error": (ctypes.c_char_p, []),
         "zero_version": (ctypes.c_char_p, []),
     }
@@ -405,6 +469,30 @@ def zero_checkpoint_load(plan: Plan, rank: int, path: str, state_layout: int, ma
 
 def zero_stream_copy(dst: int, src: int, nbytes: int, stream: int = 0) -> None:
     _check(lib().zero_stream_copy(dst, src, int(nbytes), stream or None))
+
+
+# ---------------------------------------------------------------------------
+# the model's input layer
+# ---------------------------------------------------------------------------
+
+def zero_dropout(x: int, ld_x: int, x_dtype: int, residual: int, ld_res: int, out: int, ld_out: int,
+                 out_dtype: int, rows: int, cols: int, drop: "zero_drop_t | None", stream: int = 0) -> None:
+    """residual 0: none; drop None: nothing is dropped."""
+    _check(lib().zero_dropout(x or None, ld_x, x_dtype, residual or None, ld_res, out or None, ld_out, out_dtype,
+                              rows, cols, ctypes.addressof(drop) if drop is not None else None, stream or None))
+
+
+def zero_embed_lookup(args: zero_embed_args_t, stream: int = 0) -> None:
+    _check(lib().zero_embed_lookup(ctypes.addressof(args), stream or None))
+
+
+def zero_embed_grad_ws_bytes(n_ids: int, rows: int, dim: int) -> int:
+    """Workspace bytes of zero_embed_grad; 0 for sizes out of range."""
+    return int(lib().zero_embed_grad_ws_bytes(n_ids, rows, dim))
+
+
+def zero_embed_grad(args: zero_embed_grad_args_t, stream: int = 0) -> None:
+    _check(lib().zero_embed_grad(ctypes.addressof(args), stream or None))
 
 
 def adam_args(**kw) -> zero_adam_args_t:

@@ -1,0 +1,115 @@
+// Declarations shared by the input layer's C ABI (input_abi.cpp) and its kernels
+// (input.hip): embedding lookup, embedding gradient, dropout.
+#pragma once
+
+#include <cstdint>
+
+#include "zero_internal.h"
+
+namespace zk {
+
+// q = n / d for 0 <= n < 2^31: (n * m) >> sh with m = ceil(2^sh / d) and
+// sh = 31 + ceil(log2 d).  The error of m, below 1, adds n / 2^sh < 1 / d to the
+// quotient, which cannot carry it past the next integer; m fits 32 bits because
+// d > 2^(sh - 32).
+struct FastDiv {
+  uint32_t d, m, sh;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t lg = 0;
+  while (lg < 31 && (uint32_t(1) << lg) < d) ++lg;
+  const uint32_t sh = 31 + lg;
+  return FastDiv{d, (uint32_t)(((uint64_t(1) << sh) + d - 1) / d), sh};
+}
+
+// One launch's dropout.  thr == 0: none.
+struct DropK {
+  uint32_t key0, key1, step, site;
+  const int64_t* step_dev;
+  uint32_t row0;
+  uint32_t thr;  // kept <=> 16-bit number >= thr
+  float ks;      // multiplier of the kept
+};
+
+constexpr int kInThreads = 256;      // threads per workgroup of the streaming kernels here
+constexpr int kGroup = 8;            // columns per lane and row: one generator call, 16 bytes of a 16-bit type
+constexpr int64_t kMaxUnits = (int64_t(1) << 31) - 1;  // (row, 8-column group) units of one launch
+
+struct DropoutLaunch {
+  const char* x;
+  const char* res;  // or null
+  char* out;
+  int64_t ld_x, ld_res, ld_out;  // bytes
+  uint32_t rows, cols;
+  uint32_t units;   // rows * ceil(cols / 8)
+  FastDiv groups;   // ceil(cols / 8)
+  DropK drop;
+};
+
+struct LookupLaunch {
+  const char* table;
+  const char* pos_table;  // or null
+  const void* ids;        // already advanced to row t0
+  const void* pos;        // or null; advanced to row t0
+  char* out;              // likewise
+  int64_t ld_table, ld_pos, ld_out;  // bytes
+  int64_t rows, id0, pos_rows;
+  int32_t id64;
+  uint32_t n, dim, units;
+  FastDiv groups;
+  uint32_t t0;            // position of this launch's first row in the call
+  FastDiv period;         // of the positions, where pos is null
+  float scale;
+  DropK drop;
+};
+
+// --- gradient ---------------------------------------------------------------
+constexpr int kSortThreads = 1024;   // 16 waves, one workgroup per class of ids
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortKeys = 896;       // rows of one class at most: 17 counters each fit 64 KiB of LDS
+constexpr int kSortMinClasses = 256; // one workgroup per CU
+constexpr int kJoinThreads = 256;
+
+struct GradLaunch {
+  const char* dy;
+  const void* ids;        // null: id of t is t mod period
+  char* grad;
+  int64_t ld_dy, ld_grad; // bytes
+  int64_t id0, rows;
+  int32_t id64;
+  int32_t accumulate;
+  uint32_t n;             // ids
+  uint32_t dim;
+  float factor;           // scale * ks
+  DropK drop;
+  // ids given
+  uint32_t lg_classes;
+  uint32_t keys;          // rows of the largest class
+  uint32_t* n_valid;
+  uint32_t* perm;
+  uint32_t* skey;
+  // ids == null: sorted position -> (id, occurrence) by arithmetic.  Ids below
+  // long_ids occur occ + 1 times, the others occ times.
+  uint32_t row_lo, row_hi;  // rows [row_lo, row_hi) have occurrences (row = id - id0)
+  uint32_t start_lo;        // sorted position of row_lo's first among all ids
+  uint32_t long_ids;
+  uint32_t split;           // long_ids * (occ + 1)
+  uint32_t total;           // positions of rows [row_lo, row_hi)
+  uint32_t period;
+  FastDiv div_long, div_short;  // by occ + 1, by occ
+  // tiles of the sorted positions
+  uint32_t tile;          // positions per tile
+  uint32_t n_tiles;
+  float* partial;         // [n_tiles][2][ld_partial]
+  uint32_t ld_partial;
+};
+
+// sizes of the gradient's tiles: a rule on the sizes alone, shared by the
+// workspace size and the launches
+uint32_t grad_tile(int64_t n_ids, int64_t dim);
+
+int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, void* stream);
+int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void* stream);
+int launch_embed_grad(const GradLaunch& a, zero_dtype_t dt, zero_dtype_t gt, void* stream);
+
+}  // namespace zk

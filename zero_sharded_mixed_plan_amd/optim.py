@@ -134,6 +134,7 @@ class ZeroAdam:
             self.plan = _abi.Plan(numels, world, bucket_cap)
         else:
             raise ValueError("layout must be 'flat' or 'dim0'")
+        self._shapes = [tuple(int(x) for x in n) if layout == "dim0" else (int(n),) for n in numels]
         self.world, self.rank = int(world), int(rank)
         self._lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.grad_dtype, self.param_dtype = grad_dtype, param_dtype
@@ -231,6 +232,38 @@ class ZeroAdam:
 
     def segments(self):
         return self.plan.segments(self.rank)
+
+    # -- the model's tensors in the flat buffers --------------------------------
+    def param(self, i: int, shape: Optional[Sequence[int]] = None) -> torch.Tensor:
+        """Tensor i as a view of the gather buffer (`shape`: default its size,
+        or with layout "dim0" its shape).  An embedding table is used in place:
+        input_layer.embedding(ids, opt.param(i, (rows, dim)), ...)."""
+        return self._tensor(self.gather, i, shape)
+
+    def grad_view(self, grads: torch.Tensor, i: int, shape: Optional[Sequence[int]] = None) -> torch.Tensor:
+        """Tensor i as a view of one flat gradient in the gather layout (a row
+        of what step(..., full=True) takes), for input_layer.embedding_grad."""
+        if grads.dim() != 1 or grads.numel() < self.plan.padded_numel or grads.stride(0) != 1:
+            raise ValueError(f"grads must be one flat gradient of at least {self.plan.padded_numel} elements")
+        return self._tensor(grads, i, shape)
+
+    def _tensor(self, flat: torch.Tensor, i: int, shape) -> torch.Tensor:
+        own = self._shapes[i]
+        n = 1
+        for x in own:
+            n *= x
+        shape = own if shape is None else tuple(int(x) for x in shape)
+        off = self.plan.tensor(i)[1]
+        return flat[off:off + n].view(shape)
+
+    def dropout(self, p: float, seed: int = 0, site: int = 0, row0: int = 0):
+        """The input_layer.Dropout of the coming step: its step number is the
+        number of steps applied so far, read on the device with device control."""
+        from .input_layer import Dropout
+        if self.ctl:
+            o = _abi.zero_step_ctl_t.step.offset
+            return Dropout(p, seed, site, self.ctl.buf[o:o + 8].view(torch.int64), row0)
+        return Dropout(p, seed, site, self._t, row0)
 
     # -- sharded checkpoint ----------------------------------------------------
     def _ptrs(self):
