@@ -576,3 +576,38 @@ def test_step_views():
     with pytest.raises(ValueError, match="flat gradient"):
         opt.grad_view(g[1:], 0)
     assert opt.dropout(0.1).p == 0.1
+
+
+@pytest.mark.parametrize("n,dim", [(1, 1), (1, 7), (1, 8), (1, 9), (2, 3), (3, 3), (7, 1), (8, 1), (9, 1), (4, 2),
+                                   (40, 3), (5, 15), (33, 12)])
+@pytest.mark.parametrize("dt,gt", [("bf16", "bf16"), ("f32", "f32"), ("f16", "f32")])
+def test_tensors_of_a_few_elements_at_the_end_of_memory(n, dim, dt, gt):
+    """The vector accesses near the ends of the smallest tensors: every operator at the
+    end of its own allocation's used part, with NaN right behind every tensor."""
+    rng = np.random.default_rng(n * 100 + dim)
+    d = drop_of(0.3, rows_at=2)
+    x = Mat(n, dim, dt, 3, dim, rng.normal(size=(n, dim)), fill=float("nan"))
+    r = Mat(n, dim, gt, 1, dim, rng.normal(size=(n, dim)), fill=float("nan"))
+    y = L.dropout(x.v, L_drop(d), residual=r.v)
+    close(y, OI.dropout(x.f64(), d, r.f64()), np.abs(x.f64()) * OI.keep_scale(0.3) + np.abs(r.f64()), 5)
+    ids = rng.integers(-1, n + 1, size=19)
+    ti = torch.from_numpy(ids).cuda()
+    y = L.embedding(ti, x.v, scale=2.0, pos_table=x.v, pos_period=4, drop=L_drop(d), out_dtype=T[gt])
+    kw = dict(scale=2.0, pos_period=4)
+    close(y, OI.lookup(ids, x.f64(), pos_table=x.f64(), drop=d, **kw),
+          OI.lookup(ids, np.abs(x.f64()), pos_table=np.abs(x.f64()), **kw) * OI.keep_scale(0.3), 5)
+    ids = rng.integers(-1, 4, size=n)
+    for it in (torch.int32, torch.int64):
+        for accumulate in (False, True):
+            grad = Mat(3, dim, gt, 1, dim, rng.normal(size=(3, dim)))
+            old = grad.f64() if accumulate else np.zeros((3, dim))
+            L.embedding_grad(x.v, torch.from_numpy(ids).to(it).cuda(), grad.v, scale=0.5, drop=L_drop(d),
+                             accumulate=accumulate)
+            want, cnt, mag = OI.lookup_grad(x.f64(), ids, 3, scale=0.5, drop=d)
+            close(grad.v, want + old, mag + np.abs(old), (cnt + 4)[:, None])
+            grad.check()
+    grad = Mat(4, dim, gt, 1, dim)
+    L.embedding_grad(x.v, None, grad.v, period=3, drop=L_drop(d))
+    want, cnt, mag = OI.lookup_grad(x.f64(), None, 4, period=3, drop=d)
+    close(grad.v, want, mag, (cnt + 4)[:, None])
+    grad.check()

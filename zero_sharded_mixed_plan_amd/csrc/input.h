@@ -2,6 +2,8 @@
 // (input.hip): embedding lookup, embedding gradient, dropout.
 #pragma once
 
+#include <hip/hip_runtime.h>
+
 #include <cstdint>
 
 #include "zero_internal.h"
@@ -39,6 +41,8 @@ struct DropoutLaunch {
   const char* x;
   const char* res;  // or null
   char* out;
+  const char* x_end;    // ends of what the tensors span, for the accesses near them
+  const char* res_end;
   int64_t ld_x, ld_res, ld_out;  // bytes
   uint32_t rows, cols;
   uint32_t units;   // rows * ceil(cols / 8)
@@ -49,6 +53,8 @@ struct DropoutLaunch {
 struct LookupLaunch {
   const char* table;
   const char* pos_table;  // or null
+  const char* table_end;
+  const char* pos_end;
   const void* ids;        // already advanced to row t0
   const void* pos;        // or null; advanced to row t0
   char* out;              // likewise
@@ -66,12 +72,18 @@ struct LookupLaunch {
 // --- gradient ---------------------------------------------------------------
 constexpr int kSortThreads = 1024;   // 16 waves, one workgroup per class of ids
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortKeys = 896;       // rows of one class at most: 17 counters each fit 64 KiB of LDS
 constexpr int kSortMinClasses = 256; // one workgroup per CU
-constexpr int kJoinThreads = 256;
+constexpr int kSortList = 256;       // own positions a wave keeps in LDS between its two passes
+constexpr int kSortAhead = 8;        // loads of 64 ids in flight per wave
+// rows of one class at most: 18 counters each beside the lists fit 64 KiB of LDS
+constexpr int kSortKeys = 560;
+constexpr int kChunk = 32;           // places of a run summed by one wave
+constexpr int kWindow = 16;          // places whose chunks one wave sums; kWindow + kChunk <= 64
+constexpr int kJoinThreads = 512;
 
 struct GradLaunch {
   const char* dy;
+  const char* dy_end;
   const void* ids;        // null: id of t is t mod period
   char* grad;
   int64_t ld_dy, ld_grad; // bytes
@@ -82,31 +94,30 @@ struct GradLaunch {
   uint32_t dim;
   float factor;           // scale * ks
   DropK drop;
-  // ids given
+  // ids given: written by the sort
   uint32_t lg_classes;
   uint32_t keys;          // rows of the largest class
-  uint32_t* n_valid;
-  uint32_t* perm;
-  uint32_t* skey;
-  // ids == null: sorted position -> (id, occurrence) by arithmetic.  Ids below
-  // long_ids occur occ + 1 times, the others occ times.
+  uint32_t* n_valid;      // ids that have a row
+  uint4* order;           // [n_valid] (t, row, index within the row's run, length of the run)
+  uint8_t* has;           // [rows] whether the row has an id
+  // ids == null: the same by arithmetic.  Ids below long_ids occur
+  // div_long.d times, the others div_short.d times.
   uint32_t row_lo, row_hi;  // rows [row_lo, row_hi) have occurrences (row = id - id0)
-  uint32_t start_lo;        // sorted position of row_lo's first among all ids
+  uint32_t start_lo;        // place of row_lo's first among all ids
   uint32_t long_ids;
-  uint32_t split;           // long_ids * (occ + 1)
-  uint32_t total;           // positions of rows [row_lo, row_hi)
+  uint32_t split;           // long_ids * div_long.d
+  uint32_t total;           // places of rows [row_lo, row_hi)
   uint32_t period;
-  FastDiv div_long, div_short;  // by occ + 1, by occ
-  // tiles of the sorted positions
-  uint32_t tile;          // positions per tile
-  uint32_t n_tiles;
-  float* partial;         // [n_tiles][2][ld_partial]
-  uint32_t ld_partial;
+  FastDiv div_long, div_short;
+  // division of the work
+  uint32_t places;        // upper bound of the order's length
+  uint32_t longest;       // upper bound of a run's length
+  uint32_t window, windows;
+  uint32_t slabs;         // ceil(dim / 512)
+  uint32_t sum_groups;    // workgroups that sum; the others zero fill_rows rows each
+  uint32_t fill_rows;
+  float* partial;         // [2 * ceil(places / kChunk)][slabs][512], in lane order
 };
-
-// sizes of the gradient's tiles: a rule on the sizes alone, shared by the
-// workspace size and the launches
-uint32_t grad_tile(int64_t n_ids, int64_t dim);
 
 int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, void* stream);
 int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void* stream);

@@ -29,59 +29,107 @@ struct BF16 { static constexpr int bytes = 2; };
 struct F16 { static constexpr int bytes = 2; };
 
 typedef u32 vec4 __attribute__((ext_vector_type(4)));
-typedef vec4 vec4_any __attribute__((aligned(2)));  // 16 bytes at an element-aligned address
+typedef u32 vec2 __attribute__((ext_vector_type(2)));
+typedef vec4 vec4_any __attribute__((aligned(2)));  // at an element-aligned address
+typedef vec2 vec2_any __attribute__((aligned(2)));
 
-// 8 elements, raw
-template <class T>
-struct Raw8 {
-  vec4 q[T::bytes / 2];
+// How the 64 lanes of a wave share 64 consecutive 8-column groups.  Two 16-bit
+// tensors: lane l takes group l, 16 bytes.  With an fp32 tensor that would be 32
+// bytes a lane, of which each 16-byte access of the wave touches every second half of a cache
+// line; there lane l takes 4 columns, half l % 2 of group l / 2, and the same of
+// group 32 + l / 2: every access of the wave is contiguous again.
+template <class A, class B>
+constexpr int kWidth = (A::bytes == 4 || B::bytes == 4) ? 4 : 8;  // columns of one piece; 8 / kWidth pieces
+template <int W>
+__device__ __forceinline__ u32 piece_group(u32 lane, int piece) {
+  return W == 8 ? lane : (lane >> 1) + 32 * piece;
+}
+// of a value per piece, the one of the piece whose group the lane draws numbers for
+template <int P>
+__device__ __forceinline__ u32 own_piece(u32 lane, const u32 (&v)[P]) {
+  const u32 first = v[0], last = v[P - 1];
+  return P == 2 && (lane & 1) ? last : first;
+}
+template <int W>
+__device__ __forceinline__ u32 piece_col(u32 lane) {  // first column within the group
+  return W == 8 ? 0 : (lane & 1) * 4;
+}
+
+// W consecutive elements, raw
+template <class T, int W>
+struct Raw {
+  u32 w[W * T::bytes / 4];
 };
 
-template <class T>
-__device__ __forceinline__ Raw8<T> load8(const char* p) {
-  Raw8<T> r;
+// Loads W elements at p, or, where they would pass `end`, the end of the tensor,
+// the W before `end`.  A row's last group reads on into what follows the row, at
+// the cost of no further instruction; only the last row's begins early, by the returned
+// number of elements, and move_down() puts it right.  The tensor has at least W
+// elements (the launches see to it).
+template <class T, int W>
+__device__ __forceinline__ u32 load_w(const char* p, const char* end, Raw<T, W>& r) {
+  constexpr int N = W * T::bytes / 4;
+  static_assert(N == 2 || N == 4, "8 or 16 bytes");
+  const int64_t past = p + W * T::bytes - end;
+  const u32 d = past > 0 ? (u32)past / T::bytes : 0;
+  p -= d * T::bytes;
+  if constexpr (N == 2) {
+    const vec2 q = *reinterpret_cast<const vec2_any*>(p);
+    r.w[0] = q.x;
+    r.w[1] = q.y;
+  } else {
+    const vec4 q = *reinterpret_cast<const vec4_any*>(p);
 #pragma unroll
-  for (int i = 0; i < T::bytes / 2; ++i) r.q[i] = *reinterpret_cast<const vec4_any*>(p + 16 * i);
-  return r;
-}
-
-// the first n < 8 elements, zeros behind them
-template <class T>
-__device__ __forceinline__ Raw8<T> load_some(const char* p, u32 n) {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < T::bytes / 2; ++i) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      u32 v = 0;
-      if constexpr (T::bytes == 4) {
-        const u32 e = 4 * i + w;
-        if (e < n) v = reinterpret_cast<const u32*>(p)[e];
-      } else {
-        const u32 e = 2 * w;
-        if (e < n) v = reinterpret_cast<const uint16_t*>(p)[e];
-        if (e + 1 < n) v |= (u32) reinterpret_cast<const uint16_t*>(p)[e + 1] << 16;
-      }
-      r.q[i][w] = v;
-    }
+    for (int j = 0; j < 4; ++j) r.w[j] = q[j];
   }
-  return r;
+  return d;
 }
 
-template <class T>
-__device__ __forceinline__ void widen8(const Raw8<T>& r, float o[8]) {
+// Moves the elements down by the bits K, K / 2 .. 1 of d; behind the moved ones anything.
+template <class T, int W, int K>
+__device__ __forceinline__ void move_bits(Raw<T, W>& r, u32 d) {
+  constexpr int N = W * T::bytes / 4, M = K * T::bytes / 4;
+  const bool on = d & K;
+  const Raw<T, W> old = r;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int i = 0; i < N; ++i) {
+    const u32 next = i + 1 < N ? old.w[(i + 1) % N] : 0;
+    const u32 from = M > 0 ? (i + M < N ? old.w[(i + M) % N] : old.w[i]) : (old.w[i] >> 16 | next << 16);
+    const u32 stay = old.w[i];
+    r.w[i] = on ? from : stay;
+  }
+  if constexpr (K > 1) move_bits<T, W, K / 2>(r, d);
+}
+// ... by d < W.  The empty asm keeps d's bits from being held as lane masks across
+// an unrolled loop, whose scalar registers they would use up.
+template <class T, int W>
+__device__ __forceinline__ void move_down(Raw<T, W>& r, u32 d) {
+  if (d == 0) return;
+  asm volatile("" : "+v"(d));
+  move_bits<T, W, W / 2>(r, d);
+}
+
+template <class T, int W>
+__device__ __forceinline__ void widen(const Raw<T, W>& r, float* o) {
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
     if constexpr (T::bytes == 4) {
-      o[j] = __uint_as_float(r.q[j / 4][j % 4]);
+      o[j] = __uint_as_float(r.w[j]);
     } else {
-      const u32 w = r.q[0][j / 2];
+      const u32 w = r.w[j / 2];
       if constexpr (std::is_same<T, BF16>::value)
         o[j] = __uint_as_float(j % 2 ? (w & 0xffff0000u) : (w << 16));
       else
         o[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(j % 2 ? w >> 16 : w));
     }
   }
+}
+
+// one element, of a type known when the kernel runs
+__device__ __forceinline__ float load_one(const char* p, int type) {
+  if (type == ZERO_F32) return *reinterpret_cast<const float*>(p);
+  const u32 h = *reinterpret_cast<const uint16_t*>(p);
+  return type == ZERO_BF16 ? __uint_as_float(h << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
 }
 
 template <class T>
@@ -91,38 +139,37 @@ __device__ __forceinline__ u32 bits_of(float v) {
   else return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-template <class T>
-__device__ __forceinline__ void store8(char* p, const float v[8]) {
+__device__ __forceinline__ void store_one(char* p, int type, float v) {
+  if (type == ZERO_F32) *reinterpret_cast<float*>(p) = v;
+  else *reinterpret_cast<uint16_t*>(p) = (uint16_t)(type == ZERO_BF16 ? bits_of<BF16>(v) : bits_of<F16>(v));
+}
+__device__ __forceinline__ int one_bytes(int type) { return type == ZERO_F32 ? 4 : 2; }
+
+template <class T, int W>
+__device__ __forceinline__ void store_n(char* p, const float* v, u32 n) {
+  constexpr int N = W * T::bytes / 4;
+  if (n >= W) {
+    u32 x[N];
 #pragma unroll
-  for (int i = 0; i < T::bytes / 2; ++i) {
-    vec4 x;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if constexpr (T::bytes == 4) x[w] = bits_of<T>(v[4 * i + w]);
-      else x[w] = bits_of<T>(v[2 * w]) | bits_of<T>(v[2 * w + 1]) << 16;
+    for (int i = 0; i < N; ++i) {
+      if constexpr (T::bytes == 4) x[i] = bits_of<T>(v[i]);
+      else x[i] = bits_of<T>(v[2 * i]) | bits_of<T>(v[2 * i + 1]) << 16;
     }
-    *reinterpret_cast<vec4_any*>(p + 16 * i) = x;
-  }
-}
-
-template <class T>
-__device__ __forceinline__ void store_some(char* p, const float v[8], u32 n) {
+    if constexpr (N == 2) {
+      const vec2 q = {x[0], x[1]};
+      __builtin_nontemporal_store(q, reinterpret_cast<vec2_any*>(p));
+    } else {
+      const vec4 q = {x[0], x[1], x[2], x[3]};
+      __builtin_nontemporal_store(q, reinterpret_cast<vec4_any*>(p));
+    }
+  } else {
 #pragma unroll
-  for (u32 j = 0; j < 8; ++j) {
-    if (j >= n) continue;
-    if constexpr (T::bytes == 4) reinterpret_cast<float*>(p)[j] = v[j];
-    else reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)bits_of<T>(v[j]);
+    for (u32 j = 0; j < W; ++j) {
+      if (j >= n) continue;
+      if constexpr (T::bytes == 4) reinterpret_cast<float*>(p)[j] = v[j];
+      else reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)bits_of<T>(v[j]);
+    }
   }
-}
-
-template <class T>
-__device__ __forceinline__ Raw8<T> load_n(const char* p, u32 n) {
-  return n >= 8 ? load8<T>(p) : load_some<T>(p, n);
-}
-template <class T>
-__device__ __forceinline__ void store_n(char* p, const float v[8], u32 n) {
-  if (n >= 8) store8<T>(p, v);
-  else store_some<T>(p, v, n);
 }
 
 __device__ __forceinline__ u32 quotient(u32 n, const FastDiv& f) { return (u32)(((u64)n * f.m) >> f.sh); }
@@ -130,6 +177,9 @@ __device__ __forceinline__ u32 quotient(u32 n, const FastDiv& f) { return (u32)(
 // ---------------------------------------------------------------------------
 // dropout's generator
 // ---------------------------------------------------------------------------
+
+// one instruction on gfx950 (truth table 0x96)
+__device__ __forceinline__ u32 xor3(u32 a, u32 b, u32 c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
 
 // Philox4x32-10: ten rounds of two 32 x 32 -> 64 bit products (constants and
 // round as published, Salmon et al., SC'11).  On CDNA a product with both halves is
@@ -140,8 +190,8 @@ __device__ __forceinline__ void philox(u32 c0, u32 c1, u32 c2, u32 c3, u32 k0, u
   for (int r = 0; r < 10; ++r) {
     const u64 a = (u64)c0 * 0xD2511F53u;
     const u64 b = (u64)c2 * 0xCD9E8D57u;
-    c0 = (u32)(b >> 32) ^ c1 ^ k0;
-    c2 = (u32)(a >> 32) ^ c3 ^ k1;
+    c0 = xor3((u32)(b >> 32), c1, k0);
+    c2 = xor3((u32)(a >> 32), c3, k1);
     c1 = (u32)b;
     c3 = (u32)a;
     k0 += 0x9E3779B9u;
@@ -154,7 +204,11 @@ __device__ __forceinline__ u32 drop_step(const DropK& d) {
   return d.step_dev ? (u32)*d.step_dev : d.step;
 }
 
-// zeroes the dropped of the 8 values of (row, group); the kept are not scaled
+// Zeroes the dropped among a lane's 8 values; the kept are not scaled.  (row, group)
+// is the group whose numbers this lane computes: its own (W = 8), or that of piece
+// lane % 2 (W = 4), where the two lanes of a pair hold half of each group and
+// exchange two words.  Every lane of the wave has to take part.
+template <int W>
 __device__ __forceinline__ void drop8(const DropK& d, u32 step, u32 row, u32 group, float v[8]) {
   // The empty asm keeps the compiler from holding all twenty round keys in scalar
   // registers across calls (the gradient's unrolled loop ran out of them); two
@@ -162,6 +216,19 @@ __device__ __forceinline__ void drop8(const DropK& d, u32 step, u32 row, u32 gro
   u32 k0 = d.key0, k1 = d.key1, w[4];
   asm volatile("" : "+s"(k0), "+s"(k1));
   philox(group, d.row0 + row, step, d.site, k0, k1, w);
+  if constexpr (W == 4) {
+    const bool odd = threadIdx.x & 1;
+    // to the other lane of the pair: quad_perm [1, 0, 3, 2]
+    const u32 a = __builtin_amdgcn_mov_dpp((int)(odd ? w[0] : w[2]), 0xB1, 0xF, 0xF, true);
+    const u32 b = __builtin_amdgcn_mov_dpp((int)(odd ? w[1] : w[3]), 0xB1, 0xF, 0xF, true);
+    if (odd) {
+      w[0] = a;
+      w[1] = b;
+    } else {
+      w[2] = a;
+      w[3] = b;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     v[2 * j] = (w[j] & 0xffffu) >= d.thr ? v[2 * j] : 0.0f;
@@ -169,47 +236,84 @@ __device__ __forceinline__ void drop8(const DropK& d, u32 step, u32 row, u32 gro
   }
 }
 
+// whether the one element (row, col) is kept
+__device__ __forceinline__ bool kept(const DropK& d, u32 row, u32 col) {
+  if (d.thr == 0) return true;
+  u32 w[4];
+  philox(col / kGroup, d.row0 + row, drop_step(d), d.site, d.key0, d.key1, w);
+  const u32 j = col % kGroup / 2, u = j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3];
+  return (col % 2 ? u >> 16 : u & 0xffffu) >= d.thr;
+}
+
+// Tensors of fewer than 8 elements are too short for the vector accesses of the
+// kernels below; one workgroup serves them element by element.
+
 // ---------------------------------------------------------------------------
 // dropout
 // ---------------------------------------------------------------------------
 
-// Unit u = (row u / groups, group u % groups); a workgroup takes U * 256
-// consecutive units, a lane U of them 256 apart, all loads before the arithmetic.
+__global__ void dropout_short_kernel(const DropoutLaunch a, int xt, int ot) {
+  for (u64 i = threadIdx.x; i < (u64)a.rows * a.cols; i += blockDim.x) {
+    const u32 r = (u32)(i / a.cols), c = (u32)(i % a.cols);
+    float v = load_one(a.x + r * a.ld_x + (int64_t)c * one_bytes(xt), xt) * a.drop.ks;
+    if (!kept(a.drop, r, c)) v = 0.0f;
+    if (a.res) v += load_one(a.res + r * a.ld_res + (int64_t)c * one_bytes(ot), ot);
+    store_one(a.out + r * a.ld_out + (int64_t)c * one_bytes(ot), ot, v);
+  }
+}
+
+// A unit is (row, 8-column group), numbered row by row.  A wave takes U times 64
+// consecutive units (256 apart within a workgroup), all loads before the arithmetic.
 template <class XT, class OT, int U, bool DROP>
 __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch a) {
-  const u32 base = blockIdx.x * (u32)(kInThreads * U) + threadIdx.x;
+  constexpr int W = kWidth<XT, OT>, P = 8 / W;
+  const u32 lane = threadIdx.x & 63;
+  const u32 base = blockIdx.x * (u32)(kInThreads * U) + (threadIdx.x & ~63u);
   const u32 step = DROP ? drop_step(a.drop) : 0;
-  u32 row[U], grp[U], n[U];
-  Raw8<XT> x[U];
-  Raw8<OT> r[U];
+  u32 row[U][P], grp[U][P], n[U][P], dx[U][P], dr[U][P];
+  Raw<XT, W> x[U][P];
+  Raw<OT, W> r[U][P];
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const u32 u = base + i * kInThreads + piece_group<W>(lane, q);
+      row[i][q] = quotient(u, a.groups);
+      grp[i][q] = u - row[i][q] * a.groups.d;
+      const u32 col = grp[i][q] * kGroup + piece_col<W>(lane);
+      n[i][q] = u < a.units && col < a.cols ? a.cols - col : 0;
+      dx[i][q] = dr[i][q] = 0;
+      if (n[i][q] == 0) continue;
+      dx[i][q] = load_w<XT, W>(a.x + (int64_t)row[i][q] * a.ld_x + (int64_t)col * XT::bytes, a.x_end, x[i][q]);
+      if (a.res)
+        dr[i][q] = load_w<OT, W>(a.res + (int64_t)row[i][q] * a.ld_res + (int64_t)col * OT::bytes, a.res_end, r[i][q]);
+    }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const u32 u = base + i * kInThreads;
-    n[i] = 0;
-    if (u >= a.units) continue;
-    row[i] = quotient(u, a.groups);
-    grp[i] = u - row[i] * a.groups.d;
-    n[i] = a.cols - grp[i] * kGroup;
-    x[i] = load_n<XT>(a.x + (int64_t)row[i] * a.ld_x + (int64_t)grp[i] * (kGroup * XT::bytes), n[i]);
-    if (a.res) r[i] = load_n<OT>(a.res + (int64_t)row[i] * a.ld_res + (int64_t)grp[i] * (kGroup * OT::bytes), n[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    if (n[i] == 0) continue;
     float v[8];
-    widen8<XT>(x[i], v);
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      move_down<XT, W>(x[i][q], dx[i][q]);
+      widen<XT, W>(x[i][q], v + q * W);
+    }
     if constexpr (DROP) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= a.drop.ks;
-      drop8(a.drop, step, row[i], grp[i], v);
+      drop8<W>(a.drop, step, own_piece<P>(lane, row[i]), own_piece<P>(lane, grp[i]), v);
     }
-    if (a.res) {
-      float o[8];
-      widen8<OT>(r[i], o);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += o[j];
+    for (int q = 0; q < P; ++q) {
+      if (n[i][q] == 0) continue;
+      if (a.res) {
+        float o[W];
+        move_down<OT, W>(r[i][q], dr[i][q]);
+        widen<OT, W>(r[i][q], o);
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[q * W + j] += o[j];
+      }
+      const u32 col = grp[i][q] * kGroup + piece_col<W>(lane);
+      store_n<OT, W>(a.out + (int64_t)row[i][q] * a.ld_out + (int64_t)col * OT::bytes, v + q * W, n[i][q]);
     }
-    store_n<OT>(a.out + (int64_t)row[i] * a.ld_out + (int64_t)grp[i] * (kGroup * OT::bytes), v, n[i]);
   }
 }
 
@@ -217,63 +321,105 @@ __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch
 // embedding lookup
 // ---------------------------------------------------------------------------
 
+// Without a branch on the id's width: its low word, and its high word or the low
+// one again, of which the sign is then the high word.
 __device__ __forceinline__ int64_t id_at(const void* ids, int32_t id64, u32 t) {
-  return id64 ? reinterpret_cast<const int64_t*>(ids)[t] : (int64_t) reinterpret_cast<const int32_t*>(ids)[t];
+  const u32* const p = reinterpret_cast<const u32*>(ids) + ((u64)t << id64);
+  const u32 lo = p[0], hi = p[id64];
+  return (int64_t)((u64)(id64 ? hi : (u32)((int32_t)hi >> 31)) << 32 | lo);
+}
+
+__device__ __forceinline__ int64_t pos_at(const LookupLaunch& a, u32 i) {
+  const u32 t = a.t0 + i;
+  return a.pos ? id_at(a.pos, a.id64, i) : (int64_t)(t - quotient(t, a.period) * a.period.d);
+}
+
+__global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
+  const u64 i = (u64)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (u64)a.n * a.dim) return;
+  const u32 t = (u32)(i / a.dim), c = (u32)(i % a.dim);
+  const u64 row = (u64)id_at(a.ids, a.id64, t) - (u64)a.id0;
+  const int64_t col = (int64_t)c * one_bytes(tt);
+  float v = row < (u64)a.rows ? load_one(a.table + (int64_t)row * a.ld_table + col, tt) * a.scale : 0.0f;
+  if (a.pos_table) {
+    const int64_t pos = pos_at(a, t);
+    if ((u64)pos < (u64)a.pos_rows) v += load_one(a.pos_table + pos * a.ld_pos + col, tt);
+  }
+  v *= a.drop.ks;
+  if (!kept(a.drop, a.t0 + t, c)) v = 0.0f;
+  store_one(a.out + t * a.ld_out + (int64_t)c * one_bytes(ot), ot, v);
 }
 
 template <class TT, class OT, int U, bool DROP>
 __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a) {
-  const u32 base = blockIdx.x * (u32)(kInThreads * U) + threadIdx.x;
+  constexpr int W = kWidth<TT, OT>, P = 8 / W;
+  const u32 lane = threadIdx.x & 63;
+  const u32 base = blockIdx.x * (u32)(kInThreads * U) + (threadIdx.x & ~63u);
   const u32 step = DROP ? drop_step(a.drop) : 0;
-  u32 row[U], grp[U], n[U];
-  int64_t tab[U], pos[U];
-  Raw8<TT> x[U], y[U];
+  u32 row[U][P], grp[U][P], n[U][P], dx[U][P], dy[U][P];
+  int64_t tab[U][P], pos[U][P];
+  Raw<TT, W> x[U][P], y[U][P];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const u32 u = base + i * kInThreads;
-    n[i] = 0;
-    tab[i] = pos[i] = -1;
-    if (u >= a.units) continue;
-    row[i] = quotient(u, a.groups);
-    grp[i] = u - row[i] * a.groups.d;
-    n[i] = a.dim - grp[i] * kGroup;
-    tab[i] = id_at(a.ids, a.id64, row[i]);
-    if (a.pos_table) {
-      const u32 t = a.t0 + row[i];
-      pos[i] = a.pos ? id_at(a.pos, a.id64, row[i]) : (int64_t)(t - quotient(t, a.period) * a.period.d);
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const u32 u = base + i * kInThreads + piece_group<W>(lane, q);
+      row[i][q] = quotient(u, a.groups);
+      grp[i][q] = u - row[i][q] * a.groups.d;
+      const u32 col = grp[i][q] * kGroup + piece_col<W>(lane);
+      n[i][q] = u < a.units && col < a.dim ? a.dim - col : 0;
+      // behind the last unit: the id of the last row, whose table row is not read
+      tab[i][q] = id_at(a.ids, a.id64, min(row[i][q], a.n - 1));
     }
+  if (a.pos_table) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int q = 0; q < P; ++q) pos[i][q] = pos_at(a, min(row[i][q], a.n - 1));
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    if (n[i] == 0) continue;
-    const int64_t col = (int64_t)grp[i] * (kGroup * TT::bytes);
-    // unsigned: an id below id0, or so far from it that the difference wraps, is outside too
-    const u64 v = (u64)tab[i] - (u64)a.id0;
-    const bool in_tab = v < (u64)a.rows, in_pos = a.pos_table && (u64)pos[i] < (u64)a.pos_rows;
-    x[i] = Raw8<TT>{};
-    y[i] = Raw8<TT>{};
-    if (in_tab) x[i] = load_n<TT>(a.table + (int64_t)v * a.ld_table + col, n[i]);
-    if (in_pos) y[i] = load_n<TT>(a.pos_table + pos[i] * a.ld_pos + col, n[i]);
-  }
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      x[i][q] = Raw<TT, W>{};
+      y[i][q] = Raw<TT, W>{};
+      dx[i][q] = dy[i][q] = 0;
+      const int64_t col = (int64_t)(grp[i][q] * kGroup + piece_col<W>(lane)) * TT::bytes;
+      // unsigned: an id below id0, or so far from it that the difference wraps, is outside too
+      const u64 v = (u64)tab[i][q] - (u64)a.id0;
+      if (n[i][q] != 0 && v < (u64)a.rows)
+        dx[i][q] = load_w<TT, W>(a.table + (int64_t)v * a.ld_table + col, a.table_end, x[i][q]);
+      if (a.pos_table && n[i][q] != 0 && (u64)pos[i][q] < (u64)a.pos_rows)
+        dy[i][q] = load_w<TT, W>(a.pos_table + pos[i][q] * a.ld_pos + col, a.pos_end, y[i][q]);
+    }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    if (n[i] == 0) continue;
     float v[8];
-    widen8<TT>(x[i], v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= a.scale;
-    if (a.pos_table) {
-      float o[8];
-      widen8<TT>(y[i], o);
+    for (int q = 0; q < P; ++q) {
+      move_down<TT, W>(x[i][q], dx[i][q]);
+      widen<TT, W>(x[i][q], v + q * W);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += o[j];
+      for (int j = 0; j < W; ++j) v[q * W + j] *= a.scale;
+      if (a.pos_table) {
+        float o[W];
+        move_down<TT, W>(y[i][q], dy[i][q]);
+        widen<TT, W>(y[i][q], o);
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[q * W + j] += o[j];
+      }
     }
     if constexpr (DROP) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= a.drop.ks;
-      drop8(a.drop, step, a.t0 + row[i], grp[i], v);
+      drop8<W>(a.drop, step, a.t0 + own_piece<P>(lane, row[i]), own_piece<P>(lane, grp[i]), v);
     }
-    store_n<OT>(a.out + (int64_t)row[i] * a.ld_out + (int64_t)grp[i] * (kGroup * OT::bytes), v, n[i]);
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      if (n[i][q] == 0) continue;
+      const u32 col = grp[i][q] * kGroup + piece_col<W>(lane);
+      store_n<OT, W>(a.out + (int64_t)row[i][q] * a.ld_out + (int64_t)col * OT::bytes, v + q * W, n[i][q]);
+    }
   }
 }
 
@@ -281,26 +427,38 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
 // embedding gradient
 // ---------------------------------------------------------------------------
 //
-// 1. sort_kernel orders the positions t by id (perm, and the row of each in
-//    skey), equal ids by ascending t, and zeroes the rows without an id.
-// 2. grad_sum_kernel cuts the order into tiles of equal length, so that a frequent
-//    id is shared by many waves, and sums each run of equal ids inside a tile; a run that
-//    crosses a tile border leaves an fp32 partial row instead of a result.
-// 3. grad_join_kernel adds the partial rows of each such run, in order.
+// 1. sort_kernel orders the positions t by row, equal rows by ascending t.  Each
+//    place of the order gets (t, row, its index within the row's run, the run's
+//    length); each row a flag that says whether it has any.
+// 2. grad_sum_kernel sums the runs in chunks of kChunk places, so that a frequent id
+//    is shared by many waves.  A run of one chunk gives its row of the gradient,
+//    the chunks of longer ones give fp32 partial rows.  Further workgroups of the
+//    same launch zero the rows without an id.
+// 3. grad_join_kernel adds the partial rows of each longer run, in order.
 // No floating-point atomics: the same call gives the same bits.
+
+// The row of position t's id, or kNoRow.
+constexpr u32 kNoRow = ~0u;
+__device__ __forceinline__ u32 row_of_id(const GradLaunch& a, u64 id) {
+  const u64 v = id - (u64)a.id0;
+  return v < (u64)a.rows ? (u32)v : kNoRow;
+}
 
 // One workgroup per class c = row mod classes (frequent ids are neighbours in
 // most vocabularies, so classes are interleaved).  Every workgroup reads all ids,
 // counts those of lower classes -- which is where its own begin in the order --
-// and places its own.  Nothing passes between workgroups.  Wave w owns a
+// and lists its own.  Nothing passes between workgroups.  Wave w owns a
 // contiguous range of positions; cnt[w][k] first counts its ids of the class's
 // row k, then holds the place of its next one.
-__global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a, int fill_bytes) {
-  extern __shared__ u32 cnt[];  // [kSortWaves][keys], then tot[keys]
+__global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) {
+  extern __shared__ u32 cnt[];  // [kSortWaves][keys], then start[keys], tot[keys]
+  __shared__ u32 list_t[kSortWaves][kSortList];
+  __shared__ uint16_t list_k[kSortWaves][kSortList];
   __shared__ u32 wave_sum[kSortWaves], lower_sum;
   const u32 cls = blockIdx.x, mask = (1u << a.lg_classes) - 1, keys = a.keys;
-  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  u32* const tot = cnt + kSortWaves * keys;
+  const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  u32* const start = cnt + kSortWaves * keys;
+  u32* const tot = start + keys;
   for (u32 i = threadIdx.x; i < kSortWaves * keys; i += kSortThreads) cnt[i] = 0;
   if (threadIdx.x == 0) lower_sum = 0;
   __syncthreads();
@@ -308,25 +466,57 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a, 
   const u32 chunk = ((a.n + kSortThreads - 1) / kSortThreads) * 64;  // positions per wave, a multiple of 64
   const u32 t_lo = min(a.n, wave * chunk), t_hi = min(a.n, t_lo + chunk);
   u32* const mine = cnt + wave * keys;
-  u32 lower = 0;
-  for (u32 t0 = t_lo; t0 < t_hi; t0 += 64) {
-    const u32 t = t0 + lane;
-    u64 v = ~(u64)0;
-    if (t < t_hi) v = (u64)id_at(a.ids, a.id64, t) - (u64)a.id0;
-    const bool in = v < (u64)a.rows;
-    const u32 c = (u32)v & mask;
-    lower += (in && c < cls) ? 1 : 0;
-    u64 own = __ballot(in && c == cls);
-    const u32 k = (u32)v >> a.lg_classes;
-    while (own) {  // one turn per distinct row
+
+  // calls f(t, row) for 64 positions at a time, kSortAhead loads ahead
+  auto scan = [&](auto&& f) {
+    for (u32 t0 = t_lo; t0 < t_hi; t0 += 64 * kSortAhead) {
+      u32 row[kSortAhead];
+      if (a.id64) {
+#pragma unroll
+        for (u32 j = 0; j < kSortAhead; ++j) {
+          const u32 t = t0 + 64 * j + lane;
+          row[j] = t < t_hi ? row_of_id(a, (u64) reinterpret_cast<const int64_t*>(a.ids)[t]) : kNoRow;
+        }
+      } else {
+#pragma unroll
+        for (u32 j = 0; j < kSortAhead; ++j) {
+          const u32 t = t0 + 64 * j + lane;
+          row[j] = t < t_hi ? row_of_id(a, (u64)(int64_t) reinterpret_cast<const int32_t*>(a.ids)[t]) : kNoRow;
+        }
+      }
+#pragma unroll
+      for (u32 j = 0; j < kSortAhead; ++j) f(t0 + 64 * j + lane, row[j]);
+    }
+  };
+  // calls f(leader lane, row k, its lanes) for each distinct k of the lanes in `own`
+  auto each_row = [&](u64 own, u32 k, auto&& f) {
+    while (own) {
       const int l = __builtin_ctzll(own);
       const u32 kk = __builtin_amdgcn_readlane(k, l);
       const u64 same = __ballot(k == kk) & own;
-      if ((int)lane == l) atomicAdd(&mine[kk], (u32)__popcll(same));
+      f(l, kk, same);
       own &= ~same;
     }
-  }
-  for (int o = 32; o; o >>= 1) lower += __shfl_xor(lower, o);
+  };
+  auto below = [&](u64 m) { return (u32)__popcll(m & (((u64)1 << lane) - 1)); };
+
+  u32 lower = 0, listed = 0;  // wave-uniform
+  scan([&](u32 t, u32 row) {
+    const u32 c = row & mask;
+    const bool in = row != kNoRow;
+    lower += (u32)__popcll(__ballot(in && c < cls));
+    const u64 own = __ballot(in && c == cls);
+    if (own == 0) return;
+    const u32 k = row >> a.lg_classes;
+    if (listed + (u32)__popcll(own) <= kSortList && (own >> lane & 1)) {
+      list_t[wave][listed + below(own)] = t;
+      list_k[wave][listed + below(own)] = (uint16_t)k;
+    }
+    listed += (u32)__popcll(own);
+    each_row(own, k, [&](int l, u32 kk, u64 same) {
+      if ((int)lane == l) atomicAdd(&mine[kk], (u32)__popcll(same));
+    });
+  });
   if (lane == 0) atomicAdd(&lower_sum, lower);
   __syncthreads();
 
@@ -348,225 +538,283 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a, 
   }
   if (threadIdx.x < keys) {
     u32 at = before + incl - sum;
+    start[threadIdx.x] = at;
+    tot[threadIdx.x] = sum;
     for (int w = 0; w < kSortWaves; ++w) {
       const u32 x = cnt[w * keys + threadIdx.x];
       cnt[w * keys + threadIdx.x] = at;
       at += x;
     }
-    tot[threadIdx.x] = sum;
+    const u64 row = ((u64)threadIdx.x << a.lg_classes) + cls;
+    if (row < (u64)a.rows) a.has[row] = sum != 0;
   }
   if (cls == mask && threadIdx.x == 0) *a.n_valid = all;
   __syncthreads();
 
-  for (u32 t0 = t_lo; t0 < t_hi; t0 += 64) {
-    const u32 t = t0 + lane;
-    u64 v = ~(u64)0;
-    if (t < t_hi) v = (u64)id_at(a.ids, a.id64, t) - (u64)a.id0;
-    u64 own = __ballot(v < (u64)a.rows && ((u32)v & mask) == cls);
-    const u32 k = (u32)v >> a.lg_classes;
-    while (own) {
-      const int l = __builtin_ctzll(own);
-      const u32 kk = __builtin_amdgcn_readlane(k, l);
-      const u64 same = __ballot(k == kk) & own;
+  auto place = [&](u64 own, u32 t, u32 k) {
+    each_row(own, k, [&](int l, u32 kk, u64 same) {
       u32 at = 0;
       if ((int)lane == l) at = atomicAdd(&mine[kk], (u32)__popcll(same));
-      at = __builtin_amdgcn_readlane(at, l);
-      if (same >> lane & 1) {
-        at += (u32)__popcll(same & (((u64)1 << lane) - 1));
-        a.perm[at] = t;
-        a.skey[at] = (u32)v;
-      }
-      own &= ~same;
+      at = __builtin_amdgcn_readlane(at, l) + below(same);
+      if (same >> lane & 1) a.order[at] = make_uint4(t, (kk << a.lg_classes) + cls, at - start[kk], tot[kk]);
+    });
+  };
+  if (listed <= kSortList) {
+    for (u32 i = 0; i < listed; i += 64) {
+      const bool in = i + lane < listed;
+      const u32 t = in ? list_t[wave][i + lane] : 0, k = in ? list_k[wave][i + lane] : 0;
+      place(__ballot(in), t, k);
     }
-  }
-
-  if (a.accumulate) return;
-  for (u32 k = wave; k < keys; k += kSortWaves) {
-    const u64 row = ((u64)k << a.lg_classes) + cls;
-    if (row >= (u64)a.rows || tot[k] != 0) continue;
-    char* const p = a.grad + (int64_t)row * a.ld_grad;
-    const float z[8] = {};
-    for (u32 c = lane * 8; c < a.dim; c += 512) {
-      if (fill_bytes == 4) store_n<F32>(p + (int64_t)c * 4, z, a.dim - c);
-      else store_n<BF16>(p + (int64_t)c * 2, z, a.dim - c);
-    }
+  } else {
+    scan([&](u32 t, u32 row) {
+      const u64 own = __ballot(row != kNoRow && (row & mask) == cls);
+      if (own) place(own, t, row >> a.lg_classes);
+    });
   }
 }
 
-// zeroes the rows outside [row_lo, row_hi): one wave per row
-__global__ __launch_bounds__(kInThreads) void fill_kernel(const GradLaunch a, int fill_bytes) {
-  const u32 i = blockIdx.x * (kInThreads / 64) + (threadIdx.x >> 6);
-  const u32 row = i < a.row_lo ? i : i - a.row_lo + a.row_hi;
-  if ((int64_t)row >= a.rows) return;
-  char* const p = a.grad + (int64_t)row * a.ld_grad;
-  const float z[8] = {};
-  for (u32 c = (threadIdx.x & 63) * 8; c < a.dim; c += 512) {
-    if (fill_bytes == 4) store_n<F32>(p + (int64_t)c * 4, z, a.dim - c);
-    else store_n<BF16>(p + (int64_t)c * 2, z, a.dim - c);
+// dy of fewer than 8 elements, and so fewer than 8 ids: a thread per element
+__global__ void grad_short_kernel(const GradLaunch a, int dt, int gt) {
+  const u64 i = (u64)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (u64)a.rows * a.dim) return;
+  const u32 row = (u32)(i / a.dim), c = (u32)(i % a.dim);
+  float sum = 0.0f;
+  bool any = false;
+  for (u32 t = 0; t < a.n; ++t) {
+    const u64 id = a.ids ? (u64)id_at(a.ids, a.id64, t) : t % a.period;
+    if (row_of_id(a, id) != row) continue;
+    any = true;
+    if (kept(a.drop, t, c)) sum += load_one(a.dy + t * a.ld_dy + (int64_t)c * one_bytes(dt), dt);
   }
+  char* const p = a.grad + (int64_t)row * a.ld_grad + (int64_t)c * one_bytes(gt);
+  sum *= a.factor;
+  if (a.accumulate) {
+    if (!any) return;
+    sum += load_one(p, gt);
+  }
+  store_one(p, gt, sum);
 }
 
-// position p of the order: its t and its row
+// place p of the order: (t, row, index within the run, length of the run)
 template <bool SORTED>
-__device__ __forceinline__ void order_at(const GradLaunch& a, u32 p, u32& t, u32& row) {
+__device__ __forceinline__ uint4 order_at(const GradLaunch& a, u32 p) {
   if constexpr (SORTED) {
-    t = a.perm[p];
-    row = a.skey[p];
+    return a.order[p];
   } else {
     p += a.start_lo;
-    u32 id, i;
+    u32 id, i, len = a.div_short.d;
     if (p < a.split) {
       id = quotient(p, a.div_long);
       i = p - id * a.div_long.d;
+      len = a.div_long.d;
     } else {
       p -= a.split;
       id = quotient(p, a.div_short);
       i = p - id * a.div_short.d;
       id += a.long_ids;
     }
-    t = id + i * a.period;
-    row = (u32)((int64_t)id - a.id0);
+    return make_uint4(id + i * a.period, (u32)((int64_t)id - a.id0), i, len);
   }
-}
-template <bool SORTED>
-__device__ __forceinline__ u32 row_at(const GradLaunch& a, u32 p) {
-  u32 t, row;
-  order_at<SORTED>(a, p, t, row);
-  return row;
 }
 
-template <class GT>
-__device__ __forceinline__ void write_row8(const GradLaunch& a, u32 row, u32 col, const float acc[8]) {
-  char* const p = a.grad + (int64_t)row * a.ld_grad + (int64_t)col * GT::bytes;
-  const u32 n = a.dim - col;
-  float v[8];
+// Where the partial row of the chunk that begins at place p lies: at most one
+// full chunk and the shorter tail of one other run begin in an aligned kChunk places.
+__device__ __forceinline__ u32 partial_slot(u32 p, bool tail) { return 2 * (p / kChunk) + (tail ? 1 : 0); }
+
+// Writes a lane's sums to its columns of a row.
+template <class GT, int W>
+__device__ __forceinline__ void write_row8(const GradLaunch& a, u32 row, u32 slab, u32 lane, const float acc[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = acc[j] * a.factor;
-  if (a.accumulate) {
-    float o[8];
-    widen8<GT>(load_n<GT>(p, n), o);
+  for (int q = 0; q < 8 / W; ++q) {
+    const u32 col = (slab * 64 + piece_group<W>(lane, q)) * kGroup + piece_col<W>(lane);
+    if (col >= a.dim) continue;
+    char* const p = a.grad + (int64_t)row * a.ld_grad + (int64_t)col * GT::bytes;
+    const u32 n = a.dim - col;
+    float v[W];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += o[j];
+    for (int j = 0; j < W; ++j) v[j] = acc[q * W + j] * a.factor;
+    if (a.accumulate) {
+      constexpr int type = std::is_same<GT, F32>::value ? ZERO_F32 : std::is_same<GT, BF16>::value ? ZERO_BF16 : ZERO_F16;
+      if (n >= W) {
+        Raw<GT, W> old;
+        float o[W];
+        load_w<GT, W>(p, p + W * GT::bytes, old);
+        widen<GT, W>(old, o);
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] += o[j];
+      } else {
+#pragma unroll
+        for (u32 j = 0; j < W; ++j)
+          if (j < n) v[j] += load_one(p + j * GT::bytes, type);
+      }
+    }
+    store_n<GT, W>(p, v, n);
   }
-  store_n<GT>(p, v, n);
+}
+
+// Zeroes up to a.fill_rows rows from row r0 on where they have no id.
+template <class GT, bool SORTED>
+__device__ __forceinline__ void fill_rows(const GradLaunch& a, u32 r0) {
+  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const u32 row = r0 + lane;
+  bool empty = lane < a.fill_rows && row < (u64)a.rows;
+  if (SORTED) empty = empty && a.has[row] == 0;
+  else empty = empty && (row < a.row_lo || row >= a.row_hi);
+  u64 todo = __ballot(empty);
+  const float z[8] = {};
+  constexpr u32 V = 16 / GT::bytes;
+  for (u32 i = 0; todo; ++i) {
+    const int l = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    if ((i & (kInThreads / 64 - 1)) != wave) continue;
+    char* const p = a.grad + (int64_t)(r0 + l) * a.ld_grad;
+    for (u32 c = lane * V; c < a.dim; c += 64 * V) store_n<GT, V>(p + (int64_t)c * GT::bytes, z, a.dim - c);
+  }
 }
 
 // rows of dy in flight per wave
 template <bool DROP> constexpr int kSumBatch = DROP ? 4 : 8;
 
-// One wave per (tile, 512 columns).
+// One wave per (window of a.window places, 512 columns): it sums the chunks that
+// begin in the window.  A chunk may end up to kChunk - 1 places behind it.
 template <class DT, class GT, bool SORTED, bool DROP>
-__global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a, u32 slabs) {
+__global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a) {
+  constexpr int W = kWidth<DT, GT>, P = 8 / W, B = kSumBatch<DROP>;
+  if (blockIdx.x >= a.sum_groups) {
+    fill_rows<GT, SORTED>(a, (blockIdx.x - a.sum_groups) * a.fill_rows);
+    return;
+  }
   const u32 lane = threadIdx.x & 63;
   const u32 w = __builtin_amdgcn_readfirstlane(blockIdx.x * (kInThreads / 64) + (threadIdx.x >> 6));
-  const u32 tile = w / slabs, slab = w - tile * slabs;
+  const u32 win = w / a.slabs, slab = w - win * a.slabs;
   const u32 total = SORTED ? *a.n_valid : a.total;
-  const u32 p0 = tile * a.tile;
-  if (tile >= a.n_tiles || p0 >= total) return;
-  const u32 n = min(a.tile, total - p0);
-  const u32 group = slab * 64 + lane, col = group * kGroup;
-  const u32 cols = col < a.dim ? a.dim - col : 0;
+  const u32 p0 = win * a.window;
+  if (win >= a.windows || p0 >= total) return;
+
+  uint4 e = make_uint4(0, 0, 1, 0);
+  if (p0 + lane < total) e = order_at<SORTED>(a, p0 + lane);
+  const u64 inside = a.window >= 64 ? ~(u64)0 : ((u64)1 << a.window) - 1;
+  const u64 heads = __ballot(p0 + lane < total && e.z % kChunk == 0) & inside;
+  if (heads == 0) return;
+  const u64 ends = __ballot(p0 + lane < total && (e.z % kChunk == kChunk - 1 || e.z + 1 == e.w));
+  const u32 lo = (u32)__builtin_ctzll(heads);
+  const u32 last = 63 - (u32)__builtin_clzll(heads);
+  const u32 hi = last + (u32)__builtin_ctzll(ends >> last) + 1;  // window + kChunk <= 64 places: the end is in sight
+
+  u32 col[P], n[P];
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    col[q] = (slab * 64 + piece_group<W>(lane, q)) * kGroup + piece_col<W>(lane);
+    n[q] = col[q] < a.dim ? a.dim - col[q] : 0;
+  }
+  const u32 drop_group = slab * 64 + piece_group<W>(lane, lane & (P - 1));
   const u32 step = DROP ? drop_step(a.drop) : 0;
 
-  u32 t = 0, row = 0;
-  if (lane < n) order_at<SORTED>(a, p0 + lane, t, row);
-  const u32 next = __shfl_down(row, 1);
-  const u64 ends = __ballot(lane + 1 == n || (lane + 1 < n && next != row));
-  // does the first run continue from the tile before, the last one into the next?
-  const u32 first_row = __builtin_amdgcn_readlane(row, 0), last_row = __builtin_amdgcn_readlane(row, n - 1);
-  const bool from_left = p0 > 0 && row_at<SORTED>(a, p0 - 1) == first_row;
-  const bool to_right = p0 + n < total && row_at<SORTED>(a, p0 + n) == last_row;
-
   float acc[8] = {};
-  u32 run = 0;  // first position of the current run
-  for (u32 i0 = 0; i0 < n; i0 += kSumBatch<DROP>) {
-    Raw8<DT> x[kSumBatch<DROP>];
+  u32 head = lo;  // of the current chunk
+  for (u32 i0 = lo; i0 < hi; i0 += B) {
+    Raw<DT, W> x[B][P];
 #pragma unroll
-    for (int b = 0; b < kSumBatch<DROP>; ++b) {
-      x[b] = Raw8<DT>{};
-      if (i0 + b < n && cols) {
-        const u32 tt = __builtin_amdgcn_readlane(t, i0 + b);
-        x[b] = load_n<DT>(a.dy + (int64_t)tt * a.ld_dy + (int64_t)col * DT::bytes, cols);
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int q = 0; q < P; ++q) {
+        x[b][q] = Raw<DT, W>{};
+        if (i0 + b < hi && n[q]) {
+          const u32 t = __builtin_amdgcn_readlane(e.x, i0 + b);
+          const u32 d = load_w<DT, W>(a.dy + (int64_t)t * a.ld_dy + (int64_t)col[q] * DT::bytes, a.dy_end, x[b][q]);
+          if (a.n - t <= kGroup) move_down<DT, W>(x[b][q], d);
+        }
       }
-    }
 #pragma unroll
-    for (int b = 0; b < kSumBatch<DROP>; ++b) {
+    for (int b = 0; b < B; ++b) {
       const u32 i = i0 + b;
-      if (i >= n) break;
+      if (i >= hi) break;
       float v[8];
-      widen8<DT>(x[b], v);
-      if constexpr (DROP) drop8(a.drop, step, __builtin_amdgcn_readlane(t, i), group, v);
+#pragma unroll
+      for (int q = 0; q < P; ++q) widen<DT, W>(x[b][q], v + q * W);
+      if constexpr (DROP) drop8<W>(a.drop, step, __builtin_amdgcn_readlane(e.x, i), drop_group, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += v[j];
       if (ends >> i & 1) {
-        const bool left = run == 0 && from_left, right = i + 1 == n && to_right;
-        if (cols) {
-          if (left || right) {
-            float* const q = a.partial + ((u64)tile * 2 + (left ? 0 : 1)) * a.ld_partial + col;
+        const u32 len = __builtin_amdgcn_readlane(e.w, i);
+        if (len <= kChunk) {
+          write_row8<GT, W>(a, __builtin_amdgcn_readlane(e.y, i), slab, lane, acc);
+        } else {
+          const bool tail = i + 1 - head < kChunk;
+          float* const q = a.partial + ((u64)partial_slot(p0 + head, tail) * a.slabs + slab) * 512 + lane * 8;
 #pragma unroll
-            for (int j = 0; j < 8; j += 4)
-              *reinterpret_cast<float4*>(q + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-          } else {
-            write_row8<GT>(a, __builtin_amdgcn_readlane(row, i), col, acc);
-          }
+          for (int j = 0; j < 8; j += 4)
+            *reinterpret_cast<float4*>(q + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-        run = i + 1;
+        head = i + 1;
       }
     }
   }
 }
 
-// One workgroup per (tile in which a crossing run begins, 512 columns): the
-// waves take consecutive parts of the run's tiles, wave 0 adds their sums.
-template <class GT, bool SORTED>
-__global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunch a, u32 slabs) {
-  constexpr u32 W = kJoinThreads / 64;
-  __shared__ float part[W][64][8];
-  const u32 tile = blockIdx.x / slabs, slab = blockIdx.x - tile * slabs;
-  const u32 total = SORTED ? *a.n_valid : a.total;
-  const u32 p1 = (tile + 1) * a.tile;
-  if (p1 >= total) return;
-  const u32 p0 = tile * a.tile;
-  const u32 row = row_at<SORTED>(a, p1);
-  if (row_at<SORTED>(a, p1 - 1) != row) return;
-  if (p0 > 0 && row_at<SORTED>(a, p0) == row && row_at<SORTED>(a, p0 - 1) == row) return;  // began earlier
-  // tiles (tile, last] begin with this row: a run is contiguous, so the first
-  // tile that does not ends the search (64 tiles a turn)
-  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const u32 n_tiles = (total + a.tile - 1) / a.tile;
-  u32 last = tile + 1;
-  for (u32 c0 = tile + 2;; c0 += 64) {
-    const u32 c = c0 + lane;
-    const u64 other = __ballot(!(c < n_tiles && row_at<SORTED>(a, min(c, n_tiles - 1) * a.tile) == row));
-    if (other) {
-      last = c0 + (u32)__builtin_ctzll(other) - 1;
-      break;
-    }
-  }
-  const u32 m = last - tile, each = (m + W - 1) / W;
-  const u32 lo = tile + 1 + min(m, wave * each), hi = min(last + 1, lo + each);
-  const u32 col = (slab * 64 + lane) * kGroup;
-  float acc[8] = {};
-  if (col < a.dim)
+// adds the partial rows [j_lo, j_hi) of the run of m chunks that begins at place p
+__device__ __forceinline__ void add_partials(const GradLaunch& a, u32 p, u32 len, u32 j_lo, u32 j_hi, u32 slab,
+                                             u32 lane, float acc[8]) {
+  const u32 m = (len + kChunk - 1) / kChunk;
 #pragma unroll 4
-    for (u32 c = lo; c < hi; ++c) {
-      const float* const q = a.partial + (u64)c * 2 * a.ld_partial + col;
+  for (u32 j = j_lo; j < j_hi; ++j) {
+    const u32 slot = partial_slot(p + j * kChunk, j + 1 == m && len % kChunk != 0);
+    const float* const q = a.partial + ((u64)slot * a.slabs + slab) * 512 + lane * 8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += q[j];
-    }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) part[wave][lane][j] = acc[j];
-  __syncthreads();
-  if (wave != 0 || col >= a.dim) return;
-  const float* const q = a.partial + ((u64)tile * 2 + 1) * a.ld_partial + col;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    acc[j] = q[j];
-    for (u32 w = 0; w < W; ++w) acc[j] += part[w][lane][j];
+    for (int c = 0; c < 8; ++c) acc[c] += q[c];
   }
-  write_row8<GT>(a, row, col, acc);
+}
+
+// One workgroup per (kJoinThreads places, 512 columns).  The runs of several chunks
+// that begin there: a wave takes one of few chunks by itself, all waves together
+// one of many, each a consecutive part of it.
+template <class GT, int W, bool SORTED>
+__global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunch a) {
+  constexpr u32 NW = kJoinThreads / 64;
+  __shared__ u32 runs[kJoinThreads / kChunk], n_runs;
+  __shared__ float part[NW][64][8];
+  const u32 block = blockIdx.x / a.slabs, slab = blockIdx.x - block * a.slabs;
+  const u32 total = SORTED ? *a.n_valid : a.total;
+  const u32 p0 = block * kJoinThreads;
+  if (p0 >= total) return;
+  if (threadIdx.x == 0) n_runs = 0;
+  __syncthreads();
+  const u32 p = p0 + threadIdx.x;
+  if (p < total) {
+    const uint4 e = order_at<SORTED>(a, p);
+    // heads of longer runs are more than kChunk places apart
+    if (e.z == 0 && e.w > kChunk) runs[atomicAdd(&n_runs, 1u)] = p;
+  }
+  __syncthreads();
+  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6, count = n_runs;
+  for (u32 r = wave; r < count; r += NW) {
+    const uint4 e = order_at<SORTED>(a, runs[r]);
+    const u32 m = (e.w + kChunk - 1) / kChunk;
+    if (m > NW) continue;
+    float acc[8] = {};
+    add_partials(a, runs[r], e.w, 0, m, slab, lane, acc);
+    write_row8<GT, W>(a, e.y, slab, lane, acc);
+  }
+  for (u32 r = 0; r < count; ++r) {
+    const uint4 e = order_at<SORTED>(a, runs[r]);
+    const u32 m = (e.w + kChunk - 1) / kChunk;
+    if (m <= NW) continue;
+    const u32 each = (m + NW - 1) / NW, lo = min(m, wave * each), hi = min(m, lo + each);
+    float acc[8] = {};
+    add_partials(a, runs[r], e.w, lo, hi, slab, lane, acc);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[wave][lane][j] = acc[j];
+    __syncthreads();
+    if (wave == 0) {
+      for (u32 w = 1; w < NW; ++w)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += part[w][lane][j];
+      write_row8<GT, W>(a, e.y, slab, lane, acc);
+    }
+    __syncthreads();
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -612,28 +860,29 @@ void lookup_as(const LookupLaunch& a, hipStream_t st) {
 }
 
 template <class DT, class GT, bool SORTED>
-int grad_as(const GradLaunch& a, hipStream_t st) {
-  const u32 slabs = (a.dim + 511) / 512;
-  const int fill_bytes = GT::bytes;
+int grad_as(GradLaunch a, hipStream_t st) {
   if constexpr (SORTED) {
-    const size_t lds = (size_t)(kSortWaves + 1) * a.keys * sizeof(u32);
-    hipLaunchKernelGGL(sort_kernel, dim3(1u << a.lg_classes), dim3(kSortThreads), lds, st, a, fill_bytes);
-  } else if (!a.accumulate) {
-    const int64_t rows = a.rows - (int64_t)(a.row_hi - a.row_lo);
-    if (rows > 0)
-      hipLaunchKernelGGL(fill_kernel, dim3((u32)((rows + 3) / 4)), dim3(kInThreads), 0, st, a, fill_bytes);
+    const size_t lds = (size_t)(kSortWaves + 2) * a.keys * sizeof(u32);
+    hipLaunchKernelGGL(sort_kernel, dim3(1u << a.lg_classes), dim3(kSortThreads), lds, st, a);
+    if (int rc = launched("embedding gradient (order)")) return rc;
   }
-  if (int rc = launched("embedding gradient")) return rc;
-  if (a.n_tiles == 0) return ZERO_OK;
-  const u64 waves = (u64)a.n_tiles * slabs;
-  const dim3 g((u32)((waves + 3) / 4)), b(kInThreads);
-  if (a.drop.thr) hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, true>), g, b, 0, st, a, slabs);
-  else hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, false>), g, b, 0, st, a, slabs);
-  if (int rc = launched("embedding gradient")) return rc;
-  if (a.n_tiles > 1)
-    hipLaunchKernelGGL((grad_join_kernel<GT, SORTED>), dim3((a.n_tiles - 1) * slabs), dim3(kJoinThreads), 0, st, a,
-                       slabs);
-  return launched("embedding gradient");
+  const u64 waves = (u64)a.windows * a.slabs;
+  a.sum_groups = (u32)((waves + 3) / 4);
+  // a workgroup zeroes about 64 KiB
+  a.fill_rows = (u32)std::max<int64_t>(1, std::min<int64_t>(64, 65536 / ((int64_t)a.dim * GT::bytes)));
+  const bool fill = !a.accumulate && (SORTED || a.rows > (int64_t)(a.row_hi - a.row_lo));
+  const u32 fill_groups = fill ? (u32)((a.rows + a.fill_rows - 1) / a.fill_rows) : 0;
+  if (a.sum_groups + fill_groups == 0) return ZERO_OK;
+  const dim3 g(a.sum_groups + fill_groups), b(kInThreads);
+  if (a.drop.thr) hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, true>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, false>), g, b, 0, st, a);
+  if (int rc = launched("embedding gradient (sums)")) return rc;
+  if (a.longest > kChunk) {
+    const u32 blocks = (u32)(((u64)a.places + kJoinThreads - 1) / kJoinThreads);
+    hipLaunchKernelGGL((grad_join_kernel<GT, kWidth<DT, GT>, SORTED>), dim3(blocks * a.slabs), dim3(kJoinThreads), 0,
+                       st, a);
+  }
+  return launched("embedding gradient (joins)");
 }
 
 // calls f with the element types of the two codes
@@ -655,13 +904,11 @@ int with_types(zero_dtype_t x, zero_dtype_t y, F&& f) {
 
 }  // namespace
 
-uint32_t grad_tile(int64_t n_ids, int64_t) {
-  uint32_t r = 16;
-  while (r < 64 && n_ids / r > 4096) r *= 2;
-  return r;
-}
-
 int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, void* stream) {
+  if (a.x_end - a.x < kGroup * (xt == ZERO_F32 ? 4 : 2) || (a.res && a.res_end - a.res < kGroup * (ot == ZERO_F32 ? 4 : 2))) {
+    hipLaunchKernelGGL(dropout_short_kernel, dim3(1), dim3(64), 0, (hipStream_t)stream, a, (int)xt, (int)ot);
+    return launched("dropout");
+  }
   return with_types(xt, ot, [&](auto x, auto o) {
     dropout_as<decltype(x), decltype(o)>(a, (hipStream_t)stream);
     return launched("dropout");
@@ -669,6 +916,12 @@ int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, voi
 }
 
 int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void* stream) {
+  const int64_t least = kGroup * (tt == ZERO_F32 ? 4 : 2);
+  if ((a.rows > 0 && a.table_end - a.table < least) || (a.pos_table && a.pos_end - a.pos_table < least)) {
+    const u64 blocks = ((u64)a.n * a.dim + 255) / 256;
+    hipLaunchKernelGGL(lookup_short_kernel, dim3((u32)blocks), dim3(256), 0, (hipStream_t)stream, a, (int)tt, (int)ot);
+    return launched("embedding lookup");
+  }
   return with_types(tt, ot, [&](auto t, auto o) {
     lookup_as<decltype(t), decltype(o)>(a, (hipStream_t)stream);
     return launched("embedding lookup");
@@ -676,6 +929,11 @@ int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void*
 }
 
 int launch_embed_grad(const GradLaunch& a, zero_dtype_t dt, zero_dtype_t gt, void* stream) {
+  if (a.n > 0 && a.dy_end - a.dy < kGroup * (dt == ZERO_F32 ? 4 : 2)) {
+    const u64 blocks = ((u64)a.rows * a.dim + 255) / 256;
+    hipLaunchKernelGGL(grad_short_kernel, dim3((u32)blocks), dim3(256), 0, (hipStream_t)stream, a, (int)dt, (int)gt);
+    return launched("embedding gradient");
+  }
   return with_types(dt, gt, [&](auto d, auto g) {
     if (a.ids) return grad_as<decltype(d), decltype(g), true>(a, (hipStream_t)stream);
     return grad_as<decltype(d), decltype(g), false>(a, (hipStream_t)stream);

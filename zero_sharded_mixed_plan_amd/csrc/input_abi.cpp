@@ -38,6 +38,7 @@ Span span(const void* p, int64_t bytes) {
 Span span(const void* p, int64_t rows, int64_t cols, int64_t ld, int eb) {
   return span(p, rows > 0 ? ((rows - 1) * ld + cols) * eb : 0);
 }
+const char* end_of(const Span& s) { return reinterpret_cast<const char*>(s.hi); }
 bool overlap(const Span& x, const Span& y) { return x.lo < y.hi && y.lo < x.hi; }
 
 // No exception leaves a C entry.
@@ -95,23 +96,21 @@ bool drop_overlaps(const zero_drop_t* d, const Span& out) {
   return d && d->step_dev && overlap(span(d->step_dev, 8), out);
 }
 
-// --- gradient workspace: n_valid, perm, skey, partial rows --------------------
+// --- gradient workspace: n_valid, order, has, partial rows ---------------------
 constexpr int64_t kHead = 256;
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-int64_t tiles_of(int64_t n, int64_t dim) {
-  const int64_t t = zk::grad_tile(n, dim);
-  return (n + t - 1) / t;
-}
-int64_t partial_offset(int64_t n) { return kHead + 2 * round_up(n * 4, 256); }
-
-int64_t ws_need(int64_t n, int64_t dim) {
-  return partial_offset(n) + tiles_of(n, dim) * 2 * round_up(dim, 8) * 4;
+int64_t slabs_of(int64_t dim) { return (dim + 511) / 512; }
+int64_t has_offset(int64_t n) { return kHead + round_up(n * 16, 256); }
+int64_t partial_offset(int64_t n, int64_t rows) { return has_offset(n) + round_up(rows, 256); }
+int64_t ws_need(int64_t n, int64_t rows, int64_t dim) {
+  return partial_offset(n, rows) + (n + zk::kChunk - 1) / zk::kChunk * 2 * slabs_of(dim) * 512 * 4;
 }
 
+// windows * slabs, the largest grid, stays below 2^31
 bool grad_sizes_ok(int64_t n, int64_t rows, int64_t dim) {
   return n >= 0 && n < kMax31 && rows >= 0 && rows < kMax31 && dim >= 1 && dim < kMax31 &&
-         tiles_of(n, dim) * ((dim + 511) / 512) < kMax31;
+         (n + zk::kWindow - 1) / zk::kWindow * slabs_of(dim) + rows < kMax31;
 }
 
 int dropout(const void* x, int64_t ld_x, zero_dtype_t xt, const void* res, int64_t ld_res, void* out,
@@ -146,6 +145,8 @@ int dropout(const void* x, int64_t ld_x, zero_dtype_t xt, const void* res, int64
     a.x = static_cast<const char*>(x) + r * a.ld_x;
     a.res = res ? static_cast<const char*>(res) + r * a.ld_res : nullptr;
     a.out = static_cast<char*>(out) + r * a.ld_out;
+    a.x_end = end_of(span(x, rows, cols, ld_x, bytes_of(xt)));
+    a.res_end = res ? end_of(span(res, rows, cols, ld_res, bytes_of(ot))) : nullptr;
     a.rows = (uint32_t)std::min(per_launch, rows - r);
     a.cols = (uint32_t)cols;
     a.units = (uint32_t)(a.rows * groups);
@@ -197,6 +198,8 @@ int lookup(const zero_embed_args_t* args, void* stream) {
     zk::LookupLaunch a{};
     a.table = static_cast<const char*>(A.table);
     a.pos_table = static_cast<const char*>(A.pos_table);
+    a.table_end = end_of(span(A.table, A.rows, A.dim, A.ld_table, tb));
+    a.pos_end = with_pos ? end_of(span(A.pos_table, A.pos_rows, A.dim, A.ld_pos, tb)) : nullptr;
     a.ids = static_cast<const char*>(A.ids) + t * A.id_bytes;
     a.pos = A.pos ? static_cast<const char*>(A.pos) + t * A.id_bytes : nullptr;
     a.ld_table = A.ld_table * tb;
@@ -228,7 +231,7 @@ int gradient(const zero_embed_grad_args_t* args, void* stream) {
   if (A.n_ids < 0 || A.n_ids >= kMax31) return fail(ZERO_EINVAL, fn + ": n_ids must lie in [0, 2^31)");
   if (A.rows < 0 || A.rows >= kMax31) return fail(ZERO_EINVAL, fn + ": rows must lie in [0, 2^31)");
   if (A.dim < 1 || A.dim >= kMax31) return fail(ZERO_EINVAL, fn + ": dim must lie in [1, 2^31)");
-  if (!grad_sizes_ok(A.n_ids, A.rows, A.dim)) return fail(ZERO_EINVAL, fn + ": n_ids * dim is out of range");
+  if (!grad_sizes_ok(A.n_ids, A.rows, A.dim)) return fail(ZERO_EINVAL, fn + ": n_ids, rows and dim are out of range together");
   if (A.id_bytes != 4 && A.id_bytes != 8) return fail(ZERO_EINVAL, fn + ": id_bytes must be 4 or 8");
   if (!A.ids && A.n_ids > 0 && A.period < 1)
     return fail(ZERO_EINVAL, fn + ": ids is NULL and the period is not at least 1");
@@ -243,7 +246,7 @@ int gradient(const zero_embed_grad_args_t* args, void* stream) {
   const double factor = (double)A.scale * ks;
   if (!std::isfinite((float)factor)) return fail(ZERO_EINVAL, fn + ": scale / (1 - p) is not finite in fp32");
   if (A.rows == 0) return ZERO_OK;
-  const int64_t need = ws_need(A.n_ids, A.dim);
+  const int64_t need = ws_need(A.n_ids, A.rows, A.dim);
   if (!A.ws || A.ws_bytes < need)
     return fail(ZERO_EINVAL, fn + ": the workspace needs " + std::to_string(need) + " bytes");
   if (!aligned(A.ws, 16)) return fail(ZERO_EALIGN, fn + ": the workspace must be 16-byte aligned");
@@ -257,6 +260,7 @@ int gradient(const zero_embed_grad_args_t* args, void* stream) {
 
   zk::GradLaunch a{};
   a.dy = static_cast<const char*>(A.dy);
+  a.dy_end = end_of(sd);
   a.ids = A.ids;
   a.grad = static_cast<char*>(A.grad);
   a.ld_dy = A.ld_dy * bytes_of(A.dy_dtype);
@@ -269,13 +273,12 @@ int gradient(const zero_embed_grad_args_t* args, void* stream) {
   a.dim = (uint32_t)A.dim;
   a.factor = (float)factor;
   a.drop = k;
-  a.tile = zk::grad_tile(A.n_ids, A.dim);
-  a.ld_partial = (uint32_t)round_up(A.dim, 8);
   char* const ws = static_cast<char*>(A.ws);
   a.n_valid = reinterpret_cast<uint32_t*>(ws);
-  a.perm = reinterpret_cast<uint32_t*>(ws + kHead);
-  a.skey = reinterpret_cast<uint32_t*>(ws + kHead + round_up(A.n_ids * 4, 256));
-  a.partial = reinterpret_cast<float*>(ws + partial_offset(A.n_ids));
+  a.order = reinterpret_cast<uint4*>(ws + kHead);
+  a.has = reinterpret_cast<uint8_t*>(ws + has_offset(A.n_ids));
+  a.partial = reinterpret_cast<float*>(ws + partial_offset(A.n_ids, A.rows));
+  a.longest = (uint32_t)A.n_ids;
   int64_t positions = A.n_ids;
   if (A.ids) {
     uint32_t lg = 0;
@@ -300,8 +303,12 @@ int gradient(const zero_embed_grad_args_t* args, void* stream) {
     a.period = (uint32_t)period;
     a.div_long = zk::fast_div((uint32_t)(occ + 1));
     a.div_short = zk::fast_div((uint32_t)occ);
+    a.longest = (uint32_t)(occ + (more > 0 ? 1 : 0));
   }
-  a.n_tiles = (uint32_t)((positions + a.tile - 1) / a.tile);
+  a.places = (uint32_t)positions;
+  a.window = zk::kWindow;
+  a.windows = (uint32_t)((positions + a.window - 1) / a.window);
+  a.slabs = (uint32_t)slabs_of(A.dim);
   // without ids to sort (an empty batch) the period's form zeroes every row
   return zk::launch_embed_grad(a, A.dy_dtype, A.grad_dtype, stream);
 }
@@ -321,7 +328,7 @@ extern "C" int zero_embed_lookup(const zero_embed_args_t* args, void* stream) {
 }
 
 extern "C" int64_t zero_embed_grad_ws_bytes(int64_t n_ids, int64_t rows, int64_t dim) {
-  return grad_sizes_ok(n_ids, rows, dim) ? ws_need(n_ids, dim) : 0;
+  return grad_sizes_ok(n_ids, rows, dim) ? ws_need(n_ids, rows, dim) : 0;
 }
 
 extern "C" int zero_embed_grad(const zero_embed_grad_args_t* args, void* stream) {
