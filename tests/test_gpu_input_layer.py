@@ -306,7 +306,7 @@ def test_gradient(n, rows, dim, dt, gt, it, kind, scale, p, off, pad, id0, accum
     (1, 1, 8, 1, 0, 0.0), (10, 4, 9, 4, 0, 0.1), (10, 7, 33, 4, 0, 0.0), (8192, 1024, 40, 1024, 0, 0.1),
     (1000, 3, 520, 1, 0, 0.0), (5003, 1, 24, 1, 0, 0.3), (50, 100, 16, 99, 0, 0.0), (37, 20, 16, 1 << 40, 0, 0.0),
     (999, 30, 17, 100, 50, 0.1), (999, 30, 17, 100, 90, 0.0), (999, 30, 17, 100, -10, 0.0), (999, 30, 17, 100, 200, 0.0),
-    (70000, 17, 16, 23, 3, 0.0), (0, 5, 8, 3, 0, 0.0)])
+    (70000, 17, 16, 23, 3, 0.0), (0, 5, 8, 3, 0, 0.0), (999, 30, 17, 3, 50, 0.0)])
 def test_gradient_of_positions(n, rows, dim, period, id0, p, accumulate):
     say(f"positions {n} -> {rows}x{dim} period {period} id0 {id0}")
     rng = np.random.default_rng(n + dim)

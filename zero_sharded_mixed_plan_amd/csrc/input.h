@@ -73,13 +73,14 @@ struct LookupLaunch {
 constexpr int kSortThreads = 1024;   // 16 waves, one workgroup per class of ids
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortMinClasses = 256; // one workgroup per CU
-constexpr int kSortList = 256;       // own positions a wave keeps in LDS between its two passes
+constexpr int kSortList = 1024;      // own positions a wave keeps in LDS between its two passes, at most
 constexpr int kSortAhead = 8;        // loads of 64 ids in flight per wave
-// rows of one class at most: 18 counters each beside the lists fit 64 KiB of LDS
-constexpr int kSortKeys = 560;
-constexpr int kChunk = 32;           // places of a run summed by one wave
-constexpr int kWindow = 16;          // places whose chunks one wave sums; kWindow + kChunk <= 64
+constexpr int kSortKeys = 1024;      // rows of one class at most: a list's entry has 10 bits for the row
+constexpr int kMinChunk = 8;         // places of a run that one wave sums:
+constexpr int kMaxLgChunk = 5;       // 8, 16 or 32
+constexpr int kGradWaves = 4096;     // as few as leave this many waves for the sums
 constexpr int kJoinThreads = 512;
+constexpr int kJoinGroups = 512;
 
 struct GradLaunch {
   const char* dy;
@@ -112,12 +113,17 @@ struct GradLaunch {
   // division of the work
   uint32_t places;        // upper bound of the order's length
   uint32_t longest;       // upper bound of a run's length
-  uint32_t window, windows;
+  uint32_t list;          // entries of a wave's list in the sort
+  uint32_t lg_chunk;
+  uint32_t window, windows;  // places whose chunks one wave sums; half a chunk, so that both fit 64 lanes
   uint32_t slabs;         // ceil(dim / 512)
+  uint32_t join_places;   // places per workgroup of the join
   uint32_t sum_groups;    // workgroups that sum; the others zero fill_rows rows each
   uint32_t fill_rows;
-  float* partial;         // [2 * ceil(places / kChunk)][slabs][512], in lane order
+  float* partial;         // [2 * ceil(places / chunk)][slabs][512], in lane order
 };
+
+uint32_t grad_lg_chunk(int64_t n_ids, int64_t dim);
 
 int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, void* stream);
 int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void* stream);

@@ -430,7 +430,7 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
 // 1. sort_kernel orders the positions t by row, equal rows by ascending t.  Each
 //    place of the order gets (t, row, its index within the row's run, the run's
 //    length); each row a flag that says whether it has any.
-// 2. grad_sum_kernel sums the runs in chunks of kChunk places, so that a frequent id
+// 2. grad_sum_kernel sums the runs in chunks of a.chunk places, so that a frequent id
 //    is shared by many waves.  A run of one chunk gives its row of the gradient,
 //    the chunks of longer ones give fp32 partial rows.  Further workgroups of the
 //    same launch zero the rows without an id.
@@ -451,14 +451,13 @@ __device__ __forceinline__ u32 row_of_id(const GradLaunch& a, u64 id) {
 // contiguous range of positions; cnt[w][k] first counts its ids of the class's
 // row k, then holds the place of its next one.
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) {
-  extern __shared__ u32 cnt[];  // [kSortWaves][keys], then start[keys], tot[keys]
-  __shared__ u32 list_t[kSortWaves][kSortList];
-  __shared__ uint16_t list_k[kSortWaves][kSortList];
+  extern __shared__ u32 cnt[];  // [kSortWaves][keys], start[keys], tot[keys], lists [kSortWaves][a.list]
   __shared__ u32 wave_sum[kSortWaves], lower_sum;
   const u32 cls = blockIdx.x, mask = (1u << a.lg_classes) - 1, keys = a.keys;
   const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   u32* const start = cnt + kSortWaves * keys;
   u32* const tot = start + keys;
+  u32* const list = tot + keys + wave * a.list;  // (position - t_lo) << 10 | row of the class
   for (u32 i = threadIdx.x; i < kSortWaves * keys; i += kSortThreads) cnt[i] = 0;
   if (threadIdx.x == 0) lower_sum = 0;
   __syncthreads();
@@ -467,26 +466,35 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
   const u32 t_lo = min(a.n, wave * chunk), t_hi = min(a.n, t_lo + chunk);
   u32* const mine = cnt + wave * keys;
 
-  // calls f(t, row) for 64 positions at a time, kSortAhead loads ahead
-  auto scan = [&](auto&& f) {
-    for (u32 t0 = t_lo; t0 < t_hi; t0 += 64 * kSortAhead) {
-      u32 row[kSortAhead];
-      if (a.id64) {
+  // calls f(first position, row) for 64 positions at a time, in batches of
+  // kSortAhead whose loads are issued a batch ahead
+  auto scan_as = [&](auto zero, auto&& f) {
+    using Id = decltype(zero);
+    const Id* const ids = reinterpret_cast<const Id*>(a.ids);
+    constexpr u32 B = 64 * kSortAhead;
+    Id next[kSortAhead];
+    auto fetch = [&](u32 t0) {
 #pragma unroll
-        for (u32 j = 0; j < kSortAhead; ++j) {
-          const u32 t = t0 + 64 * j + lane;
-          row[j] = t < t_hi ? row_of_id(a, (u64) reinterpret_cast<const int64_t*>(a.ids)[t]) : kNoRow;
-        }
-      } else {
+      for (u32 j = 0; j < kSortAhead; ++j) next[j] = ids[min(t0 + 64 * j + lane, a.n - 1)];
+    };
+    if (t_lo < t_hi) fetch(t_lo);
+    for (u32 t0 = t_lo; t0 < t_hi; t0 += B) {
+      Id id[kSortAhead];
 #pragma unroll
-        for (u32 j = 0; j < kSortAhead; ++j) {
-          const u32 t = t0 + 64 * j + lane;
-          row[j] = t < t_hi ? row_of_id(a, (u64)(int64_t) reinterpret_cast<const int32_t*>(a.ids)[t]) : kNoRow;
-        }
+      for (u32 j = 0; j < kSortAhead; ++j) id[j] = next[j];
+      if (t0 + B < t_hi) fetch(t0 + B);
+#pragma unroll
+      for (u32 j = 0; j < kSortAhead; ++j) {
+        const u32 t = t0 + 64 * j;
+        if (t >= t_hi) break;
+        const u32 row = row_of_id(a, (u64)(int64_t)id[j]);
+        f(t, t + lane < t_hi ? row : kNoRow);
       }
-#pragma unroll
-      for (u32 j = 0; j < kSortAhead; ++j) f(t0 + 64 * j + lane, row[j]);
     }
+  };
+  auto scan = [&](auto&& f) {
+    if (a.id64) scan_as(int64_t{}, f);
+    else scan_as(int32_t{}, f);
   };
   // calls f(leader lane, row k, its lanes) for each distinct k of the lanes in `own`
   auto each_row = [&](u64 own, u32 k, auto&& f) {
@@ -503,16 +511,31 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
   u32 lower = 0, listed = 0;  // wave-uniform
   scan([&](u32 t, u32 row) {
     const u32 c = row & mask;
-    const bool in = row != kNoRow;
-    lower += (u32)__popcll(__ballot(in && c < cls));
-    const u64 own = __ballot(in && c == cls);
+    const u64 in = __ballot(row != kNoRow);
+    lower += (u32)__popcll(__ballot(c < cls) & in);
+    const u64 own = __ballot(c == cls) & in;
     if (own == 0) return;
-    const u32 k = row >> a.lg_classes;
-    if (listed + (u32)__popcll(own) <= kSortList && (own >> lane & 1)) {
-      list_t[wave][listed + below(own)] = t;
-      list_k[wave][listed + below(own)] = (uint16_t)k;
-    }
+    const u32 at = listed + below(own);
     listed += (u32)__popcll(own);
+    if ((own >> lane & 1) && at < a.list) list[at] = (t + lane - t_lo) << 10 | row >> a.lg_classes;
+  });
+  // calls f(own lanes, position, row of the class) for the wave's own positions in
+  // order, from its list or, where that is too short, from the ids again
+  auto own_positions = [&](auto&& f) {
+    if (listed <= a.list) {
+      for (u32 i = 0; i < listed; i += 64) {
+        const bool in = i + lane < listed;
+        const u32 e = in ? list[i + lane] : 0;
+        f(__ballot(in), t_lo + (e >> 10), e & 1023);
+      }
+    } else {
+      scan([&](u32 t, u32 row) {
+        const u64 own = __ballot(row != kNoRow && (row & mask) == cls);
+        if (own) f(own, t + lane, row >> a.lg_classes);
+      });
+    }
+  };
+  own_positions([&](u64 own, u32, u32 k) {
     each_row(own, k, [&](int l, u32 kk, u64 same) {
       if ((int)lane == l) atomicAdd(&mine[kk], (u32)__popcll(same));
     });
@@ -521,9 +544,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
   __syncthreads();
 
   // exclusive prefix over (row, wave); thread k owns row k
-  u32 sum = 0;
-  if (threadIdx.x < keys)
-    for (int w = 0; w < kSortWaves; ++w) sum += cnt[w * keys + threadIdx.x];
+  u32 sum = 0, of_wave[kSortWaves];
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    of_wave[w] = threadIdx.x < keys ? cnt[w * keys + threadIdx.x] : 0;
+    sum += of_wave[w];
+  }
   u32 incl = sum;
   for (int o = 1; o < 64; o <<= 1) {
     const u32 y = __shfl_up(incl, o);
@@ -540,10 +566,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
     u32 at = before + incl - sum;
     start[threadIdx.x] = at;
     tot[threadIdx.x] = sum;
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const u32 x = cnt[w * keys + threadIdx.x];
       cnt[w * keys + threadIdx.x] = at;
-      at += x;
+      at += of_wave[w];
     }
     const u64 row = ((u64)threadIdx.x << a.lg_classes) + cls;
     if (row < (u64)a.rows) a.has[row] = sum != 0;
@@ -551,26 +577,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
   if (cls == mask && threadIdx.x == 0) *a.n_valid = all;
   __syncthreads();
 
-  auto place = [&](u64 own, u32 t, u32 k) {
+  own_positions([&](u64 own, u32 t, u32 k) {
     each_row(own, k, [&](int l, u32 kk, u64 same) {
       u32 at = 0;
       if ((int)lane == l) at = atomicAdd(&mine[kk], (u32)__popcll(same));
       at = __builtin_amdgcn_readlane(at, l) + below(same);
       if (same >> lane & 1) a.order[at] = make_uint4(t, (kk << a.lg_classes) + cls, at - start[kk], tot[kk]);
     });
-  };
-  if (listed <= kSortList) {
-    for (u32 i = 0; i < listed; i += 64) {
-      const bool in = i + lane < listed;
-      const u32 t = in ? list_t[wave][i + lane] : 0, k = in ? list_k[wave][i + lane] : 0;
-      place(__ballot(in), t, k);
-    }
-  } else {
-    scan([&](u32 t, u32 row) {
-      const u64 own = __ballot(row != kNoRow && (row & mask) == cls);
-      if (own) place(own, t, row >> a.lg_classes);
-    });
-  }
+  });
 }
 
 // dy of fewer than 8 elements, and so fewer than 8 ids: a thread per element
@@ -618,8 +632,10 @@ __device__ __forceinline__ uint4 order_at(const GradLaunch& a, u32 p) {
 }
 
 // Where the partial row of the chunk that begins at place p lies: at most one
-// full chunk and the shorter tail of one other run begin in an aligned kChunk places.
-__device__ __forceinline__ u32 partial_slot(u32 p, bool tail) { return 2 * (p / kChunk) + (tail ? 1 : 0); }
+// full chunk and the shorter tail of one other run begin in an aligned a.chunk places.
+__device__ __forceinline__ u32 partial_slot(const GradLaunch& a, u32 p, bool tail) {
+  return 2 * (p >> a.lg_chunk) + (tail ? 1 : 0);
+}
 
 // Writes a lane's sums to its columns of a row.
 template <class GT, int W>
@@ -676,7 +692,7 @@ __device__ __forceinline__ void fill_rows(const GradLaunch& a, u32 r0) {
 template <bool DROP> constexpr int kSumBatch = DROP ? 4 : 8;
 
 // One wave per (window of a.window places, 512 columns): it sums the chunks that
-// begin in the window.  A chunk may end up to kChunk - 1 places behind it.
+// begin in the window.  A chunk may end up to a.chunk - 1 places behind it.
 template <class DT, class GT, bool SORTED, bool DROP>
 __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a) {
   constexpr int W = kWidth<DT, GT>, P = 8 / W, B = kSumBatch<DROP>;
@@ -687,19 +703,20 @@ __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a
   const u32 lane = threadIdx.x & 63;
   const u32 w = __builtin_amdgcn_readfirstlane(blockIdx.x * (kInThreads / 64) + (threadIdx.x >> 6));
   const u32 win = w / a.slabs, slab = w - win * a.slabs;
-  const u32 total = SORTED ? *a.n_valid : a.total;
   const u32 p0 = win * a.window;
-  if (win >= a.windows || p0 >= total) return;
+  if (win >= a.windows) return;
+  const u32 total = SORTED ? *a.n_valid : a.total;
+  uint4 e = make_uint4(0, 0, 0, 0);
+  if (p0 + lane < a.places) e = order_at<SORTED>(a, p0 + lane);  // beyond total: not written, not used
+  if (p0 >= total) return;
 
-  uint4 e = make_uint4(0, 0, 1, 0);
-  if (p0 + lane < total) e = order_at<SORTED>(a, p0 + lane);
-  const u64 inside = a.window >= 64 ? ~(u64)0 : ((u64)1 << a.window) - 1;
-  const u64 heads = __ballot(p0 + lane < total && e.z % kChunk == 0) & inside;
+  const u32 chunk = 1u << a.lg_chunk, in_chunk = chunk - 1;
+  const u64 heads = __ballot(p0 + lane < total && (e.z & in_chunk) == 0) & (((u64)1 << a.window) - 1);
   if (heads == 0) return;
-  const u64 ends = __ballot(p0 + lane < total && (e.z % kChunk == kChunk - 1 || e.z + 1 == e.w));
+  const u64 ends = __ballot(p0 + lane < total && ((e.z & in_chunk) == in_chunk || e.z + 1 == e.w));
   const u32 lo = (u32)__builtin_ctzll(heads);
   const u32 last = 63 - (u32)__builtin_clzll(heads);
-  const u32 hi = last + (u32)__builtin_ctzll(ends >> last) + 1;  // window + kChunk <= 64 places: the end is in sight
+  const u32 hi = last + (u32)__builtin_ctzll(ends >> last) + 1;  // window + chunk <= 64 places: the end is in sight
 
   u32 col[P], n[P];
 #pragma unroll
@@ -737,11 +754,11 @@ __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a
       for (int j = 0; j < 8; ++j) acc[j] += v[j];
       if (ends >> i & 1) {
         const u32 len = __builtin_amdgcn_readlane(e.w, i);
-        if (len <= kChunk) {
+        if (len <= chunk) {
           write_row8<GT, W>(a, __builtin_amdgcn_readlane(e.y, i), slab, lane, acc);
         } else {
-          const bool tail = i + 1 - head < kChunk;
-          float* const q = a.partial + ((u64)partial_slot(p0 + head, tail) * a.slabs + slab) * 512 + lane * 8;
+          const bool tail = i + 1 - head < chunk;
+          float* const q = a.partial + ((u64)partial_slot(a, p0 + head, tail) * a.slabs + slab) * 512 + lane * 8;
 #pragma unroll
           for (int j = 0; j < 8; j += 4)
             *reinterpret_cast<float4*>(q + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
@@ -754,56 +771,55 @@ __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a
   }
 }
 
-// adds the partial rows [j_lo, j_hi) of the run of m chunks that begins at place p
+// adds the partial rows [j_lo, j_hi) of the run of `len` places that begins at place p
 __device__ __forceinline__ void add_partials(const GradLaunch& a, u32 p, u32 len, u32 j_lo, u32 j_hi, u32 slab,
                                              u32 lane, float acc[8]) {
-  const u32 m = (len + kChunk - 1) / kChunk;
+  const u32 full = len >> a.lg_chunk;
 #pragma unroll 4
   for (u32 j = j_lo; j < j_hi; ++j) {
-    const u32 slot = partial_slot(p + j * kChunk, j + 1 == m && len % kChunk != 0);
-    const float* const q = a.partial + ((u64)slot * a.slabs + slab) * 512 + lane * 8;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] += q[c];
+    const u32 slot = partial_slot(a, p + (j << a.lg_chunk), j == full);
+    const float4* const q = reinterpret_cast<const float4*>(a.partial + ((u64)slot * a.slabs + slab) * 512 + lane * 8);
+    const float4 x = q[0], y = q[1];
+    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+    acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
   }
 }
 
-// One workgroup per (kJoinThreads places, 512 columns).  The runs of several chunks
+// One workgroup per (a.join_places places, 512 columns).  The runs of several chunks
 // that begin there: a wave takes one of few chunks by itself, all waves together
 // one of many, each a consecutive part of it.
 template <class GT, int W, bool SORTED>
 __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunch a) {
   constexpr u32 NW = kJoinThreads / 64;
-  __shared__ u32 runs[kJoinThreads / kChunk], n_runs;
+  __shared__ uint4 runs[kJoinThreads / kMinChunk];  // (place, row, length, chunks)
+  __shared__ u32 n_runs;
   __shared__ float part[NW][64][8];
   const u32 block = blockIdx.x / a.slabs, slab = blockIdx.x - block * a.slabs;
+  const u32 p = block * a.join_places + threadIdx.x, in_chunk = (1u << a.lg_chunk) - 1;
   const u32 total = SORTED ? *a.n_valid : a.total;
-  const u32 p0 = block * kJoinThreads;
-  if (p0 >= total) return;
+  const bool mine = threadIdx.x < a.join_places && p < a.places;
+  uint4 e = make_uint4(0, 0, 0, 0);
+  if (mine) e = order_at<SORTED>(a, p);
   if (threadIdx.x == 0) n_runs = 0;
   __syncthreads();
-  const u32 p = p0 + threadIdx.x;
-  if (p < total) {
-    const uint4 e = order_at<SORTED>(a, p);
-    // heads of longer runs are more than kChunk places apart
-    if (e.z == 0 && e.w > kChunk) runs[atomicAdd(&n_runs, 1u)] = p;
-  }
+  // heads of longer runs are more than a chunk apart
+  if (mine && p < total && e.z == 0 && e.w > in_chunk + 1)
+    runs[atomicAdd(&n_runs, 1u)] = make_uint4(p, e.y, e.w, (e.w + in_chunk) >> a.lg_chunk);
   __syncthreads();
   const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6, count = n_runs;
   for (u32 r = wave; r < count; r += NW) {
-    const uint4 e = order_at<SORTED>(a, runs[r]);
-    const u32 m = (e.w + kChunk - 1) / kChunk;
-    if (m > NW) continue;
+    const uint4 run = runs[r];
+    if (run.w > NW) continue;
     float acc[8] = {};
-    add_partials(a, runs[r], e.w, 0, m, slab, lane, acc);
-    write_row8<GT, W>(a, e.y, slab, lane, acc);
+    add_partials(a, run.x, run.z, 0, run.w, slab, lane, acc);
+    write_row8<GT, W>(a, run.y, slab, lane, acc);
   }
   for (u32 r = 0; r < count; ++r) {
-    const uint4 e = order_at<SORTED>(a, runs[r]);
-    const u32 m = (e.w + kChunk - 1) / kChunk;
-    if (m <= NW) continue;
-    const u32 each = (m + NW - 1) / NW, lo = min(m, wave * each), hi = min(m, lo + each);
+    const uint4 run = runs[r];
+    if (run.w <= NW) continue;
+    const u32 each = (run.w + NW - 1) / NW, lo = min(run.w, wave * each), hi = min(run.w, lo + each);
     float acc[8] = {};
-    add_partials(a, runs[r], e.w, lo, hi, slab, lane, acc);
+    add_partials(a, run.x, run.z, lo, hi, slab, lane, acc);
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[wave][lane][j] = acc[j];
     __syncthreads();
@@ -811,7 +827,7 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunc
       for (u32 w = 1; w < NW; ++w)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += part[w][lane][j];
-      write_row8<GT, W>(a, e.y, slab, lane, acc);
+      write_row8<GT, W>(a, run.y, slab, lane, acc);
     }
     __syncthreads();
   }
@@ -862,7 +878,9 @@ void lookup_as(const LookupLaunch& a, hipStream_t st) {
 template <class DT, class GT, bool SORTED>
 int grad_as(GradLaunch a, hipStream_t st) {
   if constexpr (SORTED) {
-    const size_t lds = (size_t)(kSortWaves + 2) * a.keys * sizeof(u32);
+    const u32 range = (a.n + kSortThreads - 1) / kSortThreads * 64;  // positions per wave
+    a.list = range < (1u << 22) ? std::min<u32>(range, kSortList) : 0;
+    const size_t lds = ((size_t)(kSortWaves + 2) * a.keys + (size_t)kSortWaves * a.list) * sizeof(u32);
     hipLaunchKernelGGL(sort_kernel, dim3(1u << a.lg_classes), dim3(kSortThreads), lds, st, a);
     if (int rc = launched("embedding gradient (order)")) return rc;
   }
@@ -877,8 +895,11 @@ int grad_as(GradLaunch a, hipStream_t st) {
   if (a.drop.thr) hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, true>), g, b, 0, st, a);
   else hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, false>), g, b, 0, st, a);
   if (int rc = launched("embedding gradient (sums)")) return rc;
-  if (a.longest > kChunk) {
-    const u32 blocks = (u32)(((u64)a.places + kJoinThreads - 1) / kJoinThreads);
+  if (a.places > 0 && a.longest > 1u << a.lg_chunk) {
+    // few places leave each workgroup few runs, many of them keep the workgroups few
+    a.join_places = kJoinThreads;
+    while (a.join_places > 128 && (u64)a.places * a.slabs < (u64)a.join_places * kJoinGroups) a.join_places /= 2;
+    const u32 blocks = (a.places + a.join_places - 1) / a.join_places;
     hipLaunchKernelGGL((grad_join_kernel<GT, kWidth<DT, GT>, SORTED>), dim3(blocks * a.slabs), dim3(kJoinThreads), 0,
                        st, a);
   }
@@ -903,6 +924,15 @@ int with_types(zero_dtype_t x, zero_dtype_t y, F&& f) {
 }
 
 }  // namespace
+
+// Chunks of a run: long ones need fewer partial rows, short ones spread a small
+// batch over more waves.
+uint32_t grad_lg_chunk(int64_t n_ids, int64_t dim) {
+  const int64_t slabs = (dim + 511) / 512;
+  uint32_t lg = kMaxLgChunk;
+  while ((1u << lg) > kMinChunk && (n_ids >> (lg - 1)) * slabs < kGradWaves) --lg;
+  return lg;
+}
 
 int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, void* stream) {
   if (a.x_end - a.x < kGroup * (xt == ZERO_F32 ? 4 : 2) || (a.res && a.res_end - a.res < kGroup * (ot == ZERO_F32 ? 4 : 2))) {

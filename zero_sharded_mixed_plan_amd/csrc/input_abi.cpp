@@ -104,13 +104,14 @@ int64_t slabs_of(int64_t dim) { return (dim + 511) / 512; }
 int64_t has_offset(int64_t n) { return kHead + round_up(n * 16, 256); }
 int64_t partial_offset(int64_t n, int64_t rows) { return has_offset(n) + round_up(rows, 256); }
 int64_t ws_need(int64_t n, int64_t rows, int64_t dim) {
-  return partial_offset(n, rows) + (n + zk::kChunk - 1) / zk::kChunk * 2 * slabs_of(dim) * 512 * 4;
+  const int64_t lg = zk::grad_lg_chunk(n, dim);
+  return partial_offset(n, rows) + ((n + (1 << lg) - 1) >> lg) * 2 * slabs_of(dim) * 512 * 4;
 }
 
 // windows * slabs, the largest grid, stays below 2^31
 bool grad_sizes_ok(int64_t n, int64_t rows, int64_t dim) {
   return n >= 0 && n < kMax31 && rows >= 0 && rows < kMax31 && dim >= 1 && dim < kMax31 &&
-         (n + zk::kWindow - 1) / zk::kWindow * slabs_of(dim) + rows < kMax31;
+         ((n >> (zk::grad_lg_chunk(n, dim) - 1)) + 1) * slabs_of(dim) + rows < kMax31;
 }
 
 int dropout(const void* x, int64_t ld_x, zero_dtype_t xt, const void* res, int64_t ld_res, void* out,
@@ -306,7 +307,8 @@ int gradient(const zero_embed_grad_args_t* args, void* stream) {
     a.longest = (uint32_t)(occ + (more > 0 ? 1 : 0));
   }
   a.places = (uint32_t)positions;
-  a.window = zk::kWindow;
+  a.lg_chunk = zk::grad_lg_chunk(A.n_ids, A.dim);
+  a.window = 1u << (a.lg_chunk - 1);
   a.windows = (uint32_t)((positions + a.window - 1) / a.window);
   a.slabs = (uint32_t)slabs_of(A.dim);
   // without ids to sort (an empty batch) the period's form zeroes every row
