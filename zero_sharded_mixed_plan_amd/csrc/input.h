@@ -79,6 +79,7 @@ constexpr int kSortKeys = 1024;      // rows of one class at most: a list's entr
 constexpr int kMinChunk = 8;         // places of a run that one wave sums:
 constexpr int kMaxLgChunk = 5;       // 8, 16 or 32
 constexpr int kGradWaves = 4096;     // as few as leave this many waves for the sums
+constexpr int kFillBytes = 8192;     // zeroed by one workgroup, or one row
 constexpr int kJoinThreads = 512;
 constexpr int kJoinGroups = 512;
 
@@ -120,6 +121,7 @@ struct GradLaunch {
   uint32_t join_places;   // places per workgroup of the join
   uint32_t sum_groups;    // workgroups that sum; the others zero fill_rows rows each
   uint32_t fill_rows;
+  FastDiv fill_units;     // 16-byte units of one row
   float* partial;         // [2 * ceil(places / chunk)][slabs][512], in lane order
 };
 

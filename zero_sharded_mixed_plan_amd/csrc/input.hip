@@ -668,23 +668,24 @@ __device__ __forceinline__ void write_row8(const GradLaunch& a, u32 row, u32 sla
   }
 }
 
-// Zeroes up to a.fill_rows rows from row r0 on where they have no id.
+// Zeroes those of a.fill_rows rows from row r0 on that have no id.
 template <class GT, bool SORTED>
 __device__ __forceinline__ void fill_rows(const GradLaunch& a, u32 r0) {
-  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const u32 row = r0 + lane;
+  __shared__ uint8_t rows[64];
+  const u32 lane = threadIdx.x & 63, row = r0 + lane;
   bool empty = lane < a.fill_rows && row < (u64)a.rows;
   if (SORTED) empty = empty && a.has[row] == 0;
   else empty = empty && (row < a.row_lo || row >= a.row_hi);
-  u64 todo = __ballot(empty);
-  const float z[8] = {};
+  const u64 todo = __ballot(empty);  // the same in every wave
+  if (todo == 0) return;
+  if (empty && threadIdx.x < 64) rows[__popcll(todo & (((u64)1 << lane) - 1))] = (uint8_t)lane;
+  __syncthreads();
   constexpr u32 V = 16 / GT::bytes;
-  for (u32 i = 0; todo; ++i) {
-    const int l = __builtin_ctzll(todo);
-    todo &= todo - 1;
-    if ((i & (kInThreads / 64 - 1)) != wave) continue;
-    char* const p = a.grad + (int64_t)(r0 + l) * a.ld_grad;
-    for (u32 c = lane * V; c < a.dim; c += 64 * V) store_n<GT, V>(p + (int64_t)c * GT::bytes, z, a.dim - c);
+  const u32 per_row = a.fill_units.d, units = (u32)__popcll(todo) * per_row;
+  const float z[V] = {};
+  for (u32 u = threadIdx.x; u < units; u += kInThreads) {
+    const u32 i = quotient(u, a.fill_units), col = (u - i * per_row) * V;
+    store_n<GT, V>(a.grad + (int64_t)(r0 + rows[i]) * a.ld_grad + (int64_t)col * GT::bytes, z, a.dim - col);
   }
 }
 
@@ -886,8 +887,8 @@ int grad_as(GradLaunch a, hipStream_t st) {
   }
   const u64 waves = (u64)a.windows * a.slabs;
   a.sum_groups = (u32)((waves + 3) / 4);
-  // a workgroup zeroes about 64 KiB
-  a.fill_rows = (u32)std::max<int64_t>(1, std::min<int64_t>(64, 65536 / ((int64_t)a.dim * GT::bytes)));
+  a.fill_rows = (u32)std::max<int64_t>(1, std::min<int64_t>(64, kFillBytes / ((int64_t)a.dim * GT::bytes)));
+  a.fill_units = fast_div((a.dim + 16 / GT::bytes - 1) / (16 / GT::bytes));
   const bool fill = !a.accumulate && (SORTED || a.rows > (int64_t)(a.row_hi - a.row_lo));
   const u32 fill_groups = fill ? (u32)((a.rows + a.fill_rows - 1) / a.fill_rows) : 0;
   if (a.sum_groups + fill_groups == 0) return ZERO_OK;
