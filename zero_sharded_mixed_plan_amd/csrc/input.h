@@ -80,6 +80,17 @@ constexpr int kMinChunk = 8;         // places of a run that one wave sums:
 constexpr int kMaxLgChunk = 5;       // 8, 16 or 32
 constexpr int kGradWaves = 4096;     // as few as leave this many waves for the sums
 constexpr int kFillBytes = 8192;     // zeroed by one workgroup, or one row
+// zeroed beside the sort, whose time grows with the ids
+constexpr int64_t kEarlyBytes = 16 << 20, kEarlyBytesPerId = 2048, kEarlyGroupBytes = 65536;
+// One launch instead of three for at most this many ids times slabs of 512 columns
+// and this many bytes of gradient.  Measured against three: 64 ids, 256 x 64 fp32
+// 5.9 us (9.0), 1024 ids, 1000 x 256 fp32 9.3 (14.1).  Beyond, its 256 workgroups zero
+// too slowly (50257 x 1600 bf16 47 to 59 us against 30 to 37), and an id that fills
+// the batch waits for one CU (256 times one id, 1600 wide, 21 us against 11; 1024
+// times 86 against 16).
+constexpr uint32_t kOnceIds = 1024;
+constexpr int64_t kOnceBytes = 4 << 20;
+constexpr uint32_t kOnceRun = 16;   // ids of a row that one wave sums there
 constexpr int kJoinThreads = 512;
 constexpr int kJoinGroups = 512;
 
@@ -120,6 +131,7 @@ struct GradLaunch {
   uint32_t slabs;         // ceil(dim / 512)
   uint32_t join_places;   // places per workgroup of the join
   uint32_t sum_groups;    // workgroups that sum; the others zero fill_rows rows each
+  uint32_t early_row, early_rows;  // rows from early_row on are zeroed beside the sort, early_rows a workgroup
   uint32_t fill_rows;
   FastDiv fill_units;     // 16-byte units of one row
   float* partial;         // [2 * ceil(places / chunk)][slabs][512], in lane order

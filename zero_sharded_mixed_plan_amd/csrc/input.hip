@@ -444,16 +444,21 @@ __device__ __forceinline__ u32 row_of_id(const GradLaunch& a, u64 id) {
   return v < (u64)a.rows ? (u32)v : kNoRow;
 }
 
-// One workgroup per class c = row mod classes (frequent ids are neighbours in
-// most vocabularies, so classes are interleaved).  Every workgroup reads all ids,
-// counts those of lower classes -- which is where its own begin in the order --
-// and lists its own.  Nothing passes between workgroups.  Wave w owns a
-// contiguous range of positions; cnt[w][k] first counts its ids of the class's
-// row k, then holds the place of its next one.
-__global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) {
-  extern __shared__ u32 cnt[];  // [kSortWaves][keys], start[keys], tot[keys], lists [kSortWaves][a.list]
+// The places of class c = row mod classes in the order, found by one workgroup
+// (frequent ids are neighbours in most vocabularies, so classes are interleaved).
+// Every workgroup reads all ids, counts those of lower classes -- which is where its
+// own begin in the order -- and lists its own.  Nothing passes between workgroups.
+// Wave w owns a contiguous range of positions; cnt[w][k] first counts its ids of
+// the class's row k, then holds the place of its next one.
+//   lds: cnt[kSortWaves][keys], start[keys] (the first place of row k), tot[keys] (its
+//        ids), lists [kSortWaves][a.list]
+// Calls counted(first place of the class, first place behind it) between the two
+// parts, with start and tot written but not yet seen by all waves, and then
+// emit(place, position, row of the class) for each id of the class.
+template <class Counted, class Emit>
+__device__ __forceinline__ void order_class(const GradLaunch& a, u32 cls, u32* cnt, Counted&& counted, Emit&& emit) {
   __shared__ u32 wave_sum[kSortWaves], lower_sum;
-  const u32 cls = blockIdx.x, mask = (1u << a.lg_classes) - 1, keys = a.keys;
+  const u32 mask = (1u << a.lg_classes) - 1, keys = a.keys;
   const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   u32* const start = cnt + kSortWaves * keys;
   u32* const tot = start + keys;
@@ -571,10 +576,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
       cnt[w * keys + threadIdx.x] = at;
       at += of_wave[w];
     }
-    const u64 row = ((u64)threadIdx.x << a.lg_classes) + cls;
-    if (row < (u64)a.rows) a.has[row] = sum != 0;
   }
-  if (cls == mask && threadIdx.x == 0) *a.n_valid = all;
+  counted(lower_sum, all);
   __syncthreads();
 
   own_positions([&](u64 own, u32 t, u32 k) {
@@ -582,9 +585,39 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
       u32 at = 0;
       if ((int)lane == l) at = atomicAdd(&mine[kk], (u32)__popcll(same));
       at = __builtin_amdgcn_readlane(at, l) + below(same);
-      if (same >> lane & 1) a.order[at] = make_uint4(t, (kk << a.lg_classes) + cls, at - start[kk], tot[kk]);
+      if (same >> lane & 1) emit(at, t, kk);
     });
   });
+}
+
+// One workgroup per class.  It reads little and takes 4 to 25 us, so further
+// workgroups of the launch zero the rows from a.early_row on meanwhile, whether
+// they have ids or not: those that do are written again by the launches that follow.
+template <class GT>
+__global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) {
+  if (blockIdx.x >> a.lg_classes) {
+    const u32 r0 = a.early_row + (blockIdx.x - (1u << a.lg_classes)) * a.early_rows;
+    constexpr u32 V = 16 / GT::bytes;
+    const u32 per_row = a.fill_units.d, units = min(a.early_rows, (u32)a.rows - r0) * per_row;
+    const float z[V] = {};
+    for (u32 u = threadIdx.x; u < units; u += kSortThreads) {
+      const u32 i = quotient(u, a.fill_units), col = (u - i * per_row) * V;
+      store_n<GT, V>(a.grad + (int64_t)(r0 + i) * a.ld_grad + (int64_t)col * GT::bytes, z, a.dim - col);
+    }
+    return;
+  }
+  extern __shared__ u32 lds[];
+  const u32 cls = blockIdx.x, *const start = lds + kSortWaves * a.keys, *const tot = start + a.keys;
+  order_class(
+      a, cls, lds,
+      [&](u32, u32 behind) {
+        const u64 row = ((u64)threadIdx.x << a.lg_classes) + cls;
+        if (threadIdx.x < a.keys && row < (u64)a.rows) a.has[row] = tot[threadIdx.x] != 0;
+        if (cls + 1 == 1u << a.lg_classes && threadIdx.x == 0) *a.n_valid = behind;
+      },
+      [&](u32 at, u32 t, u32 k) {
+        a.order[at] = make_uint4(t, (k << a.lg_classes) + cls, at - start[k], tot[k]);
+      });
 }
 
 // dy of fewer than 8 elements, and so fewer than 8 ids: a thread per element
@@ -673,7 +706,7 @@ template <class GT, bool SORTED>
 __device__ __forceinline__ void fill_rows(const GradLaunch& a, u32 r0) {
   __shared__ uint8_t rows[64];
   const u32 lane = threadIdx.x & 63, row = r0 + lane;
-  bool empty = lane < a.fill_rows && row < (u64)a.rows;
+  bool empty = lane < a.fill_rows && row < (SORTED ? (u64)a.early_row : (u64)a.rows);
   if (SORTED) empty = empty && a.has[row] == 0;
   else empty = empty && (row < a.row_lo || row >= a.row_hi);
   const u64 todo = __ballot(empty);  // the same in every wave
@@ -834,6 +867,99 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunc
   }
 }
 
+// A small batch in one launch: the workgroup of a class orders its ids in LDS, sums
+// its rows and zeroes those without an id.  Waves take (row, 512 columns) each;
+// a run of more than kOnceRun ids is summed by all waves together, which still
+// leaves a very frequent id to one CU: hence for small batches only.
+template <class DT, class GT, bool DROP>
+__global__ __launch_bounds__(kSortThreads) void grad_once_kernel(const GradLaunch a) {
+  constexpr int W = kWidth<DT, GT>, P = 8 / W, B = 4;
+  extern __shared__ u32 lds[];
+  __shared__ float part[kSortWaves][64][8];
+  const u32 cls = blockIdx.x, *const start = lds + kSortWaves * a.keys, *const tot = start + a.keys;
+  u32* const places = lds + (kSortWaves + 2) * a.keys + kSortWaves * a.list;  // [n] the class's positions in order
+  const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ u32 first;
+  order_class(
+      a, cls, lds, [&](u32 before, u32) { if (threadIdx.x == 0) first = before; },
+      [&](u32 at, u32 t, u32) { places[at - first] = t; });
+  __syncthreads();
+  const u32 step = DROP ? drop_step(a.drop) : 0;
+
+  // the sum of the class's places [lo, hi) in a slab
+  auto sum = [&](u32 lo, u32 hi, u32 slab, float acc[8]) {
+    u32 col[P], n[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      col[q] = (slab * 64 + piece_group<W>(lane, q)) * kGroup + piece_col<W>(lane);
+      n[q] = col[q] < a.dim ? a.dim - col[q] : 0;
+    }
+    const u32 drop_group = slab * 64 + piece_group<W>(lane, lane & (P - 1));
+    for (u32 i0 = lo; i0 < hi; i0 += B) {
+      Raw<DT, W> x[B][P];
+      u32 t[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) t[b] = __builtin_amdgcn_readfirstlane(places[min(i0 + b, hi - 1)]);
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          x[b][q] = Raw<DT, W>{};
+          if (i0 + b < hi && n[q]) {
+            const u32 d = load_w<DT, W>(a.dy + (int64_t)t[b] * a.ld_dy + (int64_t)col[q] * DT::bytes, a.dy_end, x[b][q]);
+            if (a.n - t[b] <= kGroup) move_down<DT, W>(x[b][q], d);
+          }
+        }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (i0 + b >= hi) break;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < P; ++q) widen<DT, W>(x[b][q], v + q * W);
+        if constexpr (DROP) drop8<W>(a.drop, step, t[b], drop_group, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += v[j];
+      }
+    }
+  };
+
+  // long runs first: all waves meet there
+  const u32 across = min(a.slabs, (u32)kSortWaves), splits = kSortWaves / across;
+  for (u32 k = 0; k < a.keys; ++k) {
+    const u32 len = __builtin_amdgcn_readfirstlane(tot[k]);
+    if (len <= kOnceRun) continue;
+    const u32 row = (k << a.lg_classes) + cls, at = __builtin_amdgcn_readfirstlane(start[k]) - first;
+    const u32 split = wave / across, each = (len + splits - 1) / splits;
+    for (u32 s0 = 0; s0 < a.slabs; s0 += across) {
+      const u32 slab = s0 + wave % across;
+      float acc[8] = {};
+      if (split < splits && slab < a.slabs) sum(at + min(len, split * each), at + min(len, (split + 1) * each), slab, acc);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part[wave][lane][j] = acc[j];
+      __syncthreads();
+      if (split == 0 && slab < a.slabs) {
+        for (u32 w = 1; w < splits; ++w)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] += part[w * across + wave][lane][j];
+        write_row8<GT, W>(a, row, slab, lane, acc);
+      }
+      __syncthreads();
+    }
+  }
+  for (u32 i = wave; i < a.keys * a.slabs; i += kSortWaves) {
+    const u32 k = i / a.slabs, slab = i - k * a.slabs;
+    const u32 len = __builtin_amdgcn_readfirstlane(tot[k]);
+    const u64 row = ((u64)k << a.lg_classes) + cls;
+    if (row >= (u64)a.rows || len > kOnceRun || (len == 0 && a.accumulate)) continue;
+    float acc[8] = {};
+    if (len) {
+      const u32 at = __builtin_amdgcn_readfirstlane(start[k]) - first;
+      sum(at, at + len, slab, acc);
+    }
+    write_row8<GT, W>(a, (u32)row, slab, lane, acc);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
@@ -878,19 +1004,37 @@ void lookup_as(const LookupLaunch& a, hipStream_t st) {
 
 template <class DT, class GT, bool SORTED>
 int grad_as(GradLaunch a, hipStream_t st) {
+  const int64_t row_bytes = (int64_t)a.dim * GT::bytes;
+  a.fill_units = fast_div((a.dim + 16 / GT::bytes - 1) / (16 / GT::bytes));
   if constexpr (SORTED) {
     const u32 range = (a.n + kSortThreads - 1) / kSortThreads * 64;  // positions per wave
     a.list = range < (1u << 22) ? std::min<u32>(range, kSortList) : 0;
     const size_t lds = ((size_t)(kSortWaves + 2) * a.keys + (size_t)kSortWaves * a.list) * sizeof(u32);
-    hipLaunchKernelGGL(sort_kernel, dim3(1u << a.lg_classes), dim3(kSortThreads), lds, st, a);
+    if ((u64)a.n * a.slabs <= kOnceIds && a.rows * row_bytes <= kOnceBytes) {
+      const dim3 g(1u << a.lg_classes), b(kSortThreads);
+      const size_t all = lds + a.n * sizeof(u32);
+      if (a.drop.thr) hipLaunchKernelGGL((grad_once_kernel<DT, GT, true>), g, b, all, st, a);
+      else hipLaunchKernelGGL((grad_once_kernel<DT, GT, false>), g, b, all, st, a);
+      return launched("embedding gradient");
+    }
+    u32 early_groups = 0;
+    a.early_row = (u32)a.rows;
+    if (!a.accumulate) {
+      // as many as fit beside the sort, 64 KiB or one row a workgroup
+      a.early_rows = (u32)std::max<int64_t>(1, kEarlyGroupBytes / row_bytes);
+      const int64_t bytes = kEarlyBytes + kEarlyBytesPerId * (int64_t)a.n;
+      early_groups = (u32)(std::min<int64_t>(a.rows, bytes / row_bytes) / a.early_rows);
+      a.early_row = (u32)(a.rows - (int64_t)early_groups * a.early_rows);
+    }
+    hipLaunchKernelGGL(sort_kernel<GT>, dim3((1u << a.lg_classes) + early_groups), dim3(kSortThreads), lds, st, a);
     if (int rc = launched("embedding gradient (order)")) return rc;
   }
   const u64 waves = (u64)a.windows * a.slabs;
   a.sum_groups = (u32)((waves + 3) / 4);
-  a.fill_rows = (u32)std::max<int64_t>(1, std::min<int64_t>(64, kFillBytes / ((int64_t)a.dim * GT::bytes)));
-  a.fill_units = fast_div((a.dim + 16 / GT::bytes - 1) / (16 / GT::bytes));
+  a.fill_rows = (u32)std::max<int64_t>(1, std::min<int64_t>(64, kFillBytes / row_bytes));
   const bool fill = !a.accumulate && (SORTED || a.rows > (int64_t)(a.row_hi - a.row_lo));
-  const u32 fill_groups = fill ? (u32)((a.rows + a.fill_rows - 1) / a.fill_rows) : 0;
+  const int64_t fill_to = SORTED ? (int64_t)a.early_row : a.rows;
+  const u32 fill_groups = fill ? (u32)((fill_to + a.fill_rows - 1) / a.fill_rows) : 0;
   if (a.sum_groups + fill_groups == 0) return ZERO_OK;
   const dim3 g(a.sum_groups + fill_groups), b(kInThreads);
   if (a.drop.thr) hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, true>), g, b, 0, st, a);
