@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <type_traits>
 
 #include "input.h"
 
@@ -174,6 +175,30 @@ __device__ __forceinline__ void store_n(char* p, const float* v, u32 n) {
 
 __device__ __forceinline__ u32 quotient(u32 n, const FastDiv& f) { return (u32)(((u64)n * f.m) >> f.sh); }
 
+// (row, group) of unit u0 + i, for i < 64 and the wave's first unit u0.  WIDE: a row
+// has at least 64 groups, so the wave meets at most two rows, first and first + 1,
+// and what belongs to them is found once for the wave by scalar instructions rather than
+// by every lane (lookup of 32768 rows, 4096 wide: 66 us against 79).
+struct Unit {
+  u32 row, grp;
+  bool second;
+};
+template <bool WIDE>
+__device__ __forceinline__ Unit unit_at(u32 u0, u32 i, u32 first, const FastDiv& groups) {
+  Unit r;
+  if constexpr (WIDE) {
+    const u32 at = u0 - first * groups.d + i;  // counted from the first row's beginning
+    r.second = at >= groups.d;
+    r.row = first + (r.second ? 1 : 0);
+    r.grp = at - (r.second ? groups.d : 0);
+  } else {
+    r.second = false;
+    r.row = quotient(u0 + i, groups);
+    r.grp = u0 + i - r.row * groups.d;
+  }
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // dropout's generator
 // ---------------------------------------------------------------------------
@@ -262,58 +287,52 @@ __global__ void dropout_short_kernel(const DropoutLaunch a, int xt, int ot) {
   }
 }
 
-// A unit is (row, 8-column group), numbered row by row.  A wave takes U times 64
-// consecutive units (256 apart within a workgroup), all loads before the arithmetic.
-template <class XT, class OT, int U, bool DROP>
+// A unit is (row, 8-column group), numbered row by row; a wave takes 64 consecutive ones.
+template <class XT, class OT, bool DROP, bool WIDE>
 __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch a) {
   constexpr int W = kWidth<XT, OT>, P = 8 / W;
   const u32 lane = threadIdx.x & 63;
-  const u32 base = blockIdx.x * (u32)(kInThreads * U) + (threadIdx.x & ~63u);
+  const u32 u0 = __builtin_amdgcn_readfirstlane(blockIdx.x * (u32)kInThreads + (threadIdx.x & ~63u));
+  const u32 first = quotient(u0, a.groups);
   const u32 step = DROP ? drop_step(a.drop) : 0;
-  u32 row[U][P], grp[U][P], n[U][P], dx[U][P], dr[U][P];
-  Raw<XT, W> x[U][P];
-  Raw<OT, W> r[U][P];
+  u32 row[P], grp[P], n[P], dx[P], dr[P];
+  Raw<XT, W> x[P];
+  Raw<OT, W> r[P];
 #pragma unroll
-  for (int i = 0; i < U; ++i)
+  for (int q = 0; q < P; ++q) {
+    const Unit w = unit_at<WIDE>(u0, piece_group<W>(lane, q), first, a.groups);
+    row[q] = w.row;
+    grp[q] = w.grp;
+    const u32 col = w.grp * kGroup + piece_col<W>(lane);
+    n[q] = u0 + piece_group<W>(lane, q) < a.units && col < a.cols ? a.cols - col : 0;
+    dx[q] = dr[q] = 0;
+    if (n[q] == 0) continue;
+    dx[q] = load_w<XT, W>(a.x + (int64_t)w.row * a.ld_x + (int64_t)col * XT::bytes, a.x_end, x[q]);
+    if (a.res) dr[q] = load_w<OT, W>(a.res + (int64_t)w.row * a.ld_res + (int64_t)col * OT::bytes, a.res_end, r[q]);
+  }
+  float v[8];
 #pragma unroll
-    for (int q = 0; q < P; ++q) {
-      const u32 u = base + i * kInThreads + piece_group<W>(lane, q);
-      row[i][q] = quotient(u, a.groups);
-      grp[i][q] = u - row[i][q] * a.groups.d;
-      const u32 col = grp[i][q] * kGroup + piece_col<W>(lane);
-      n[i][q] = u < a.units && col < a.cols ? a.cols - col : 0;
-      dx[i][q] = dr[i][q] = 0;
-      if (n[i][q] == 0) continue;
-      dx[i][q] = load_w<XT, W>(a.x + (int64_t)row[i][q] * a.ld_x + (int64_t)col * XT::bytes, a.x_end, x[i][q]);
-      if (a.res)
-        dr[i][q] = load_w<OT, W>(a.res + (int64_t)row[i][q] * a.ld_res + (int64_t)col * OT::bytes, a.res_end, r[i][q]);
+  for (int q = 0; q < P; ++q) {
+    move_down<XT, W>(x[q], dx[q]);
+    widen<XT, W>(x[q], v + q * W);
+  }
+  if constexpr (DROP) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= a.drop.ks;
+    drop8<W>(a.drop, step, own_piece<P>(lane, row), own_piece<P>(lane, grp), v);
+  }
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    if (n[q] == 0) continue;
+    if (a.res) {
+      float o[W];
+      move_down<OT, W>(r[q], dr[q]);
+      widen<OT, W>(r[q], o);
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[q * W + j] += o[j];
     }
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    float v[8];
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-      move_down<XT, W>(x[i][q], dx[i][q]);
-      widen<XT, W>(x[i][q], v + q * W);
-    }
-    if constexpr (DROP) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= a.drop.ks;
-      drop8<W>(a.drop, step, own_piece<P>(lane, row[i]), own_piece<P>(lane, grp[i]), v);
-    }
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-      if (n[i][q] == 0) continue;
-      if (a.res) {
-        float o[W];
-        move_down<OT, W>(r[i][q], dr[i][q]);
-        widen<OT, W>(r[i][q], o);
-#pragma unroll
-        for (int j = 0; j < W; ++j) v[q * W + j] += o[j];
-      }
-      const u32 col = grp[i][q] * kGroup + piece_col<W>(lane);
-      store_n<OT, W>(a.out + (int64_t)row[i][q] * a.ld_out + (int64_t)col * OT::bytes, v + q * W, n[i][q]);
-    }
+    const u32 col = grp[q] * kGroup + piece_col<W>(lane);
+    store_n<OT, W>(a.out + (int64_t)row[q] * a.ld_out + (int64_t)col * OT::bytes, v + q * W, n[q]);
   }
 }
 
@@ -350,32 +369,54 @@ __global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
   store_one(a.out + t * a.ld_out + (int64_t)c * one_bytes(ot), ot, v);
 }
 
-template <class TT, class OT, int U, bool DROP>
+// As above, with U times 64 units a wave, 256 apart, all loads before the arithmetic.
+template <class TT, class OT, int U, bool DROP, bool WIDE>
 __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a) {
   constexpr int W = kWidth<TT, OT>, P = 8 / W;
   const u32 lane = threadIdx.x & 63;
-  const u32 base = blockIdx.x * (u32)(kInThreads * U) + (threadIdx.x & ~63u);
+  const u32 base = __builtin_amdgcn_readfirstlane(blockIdx.x * (u32)(kInThreads * U) + (threadIdx.x & ~63u));
   const u32 step = DROP ? drop_step(a.drop) : 0;
   u32 row[U][P], grp[U][P], n[U][P], dx[U][P], dy[U][P];
-  int64_t tab[U][P], pos[U][P];
+  const char* tab[U][P];  // the table's row, or null
+  const char* pos[U][P];
   Raw<TT, W> x[U][P], y[U][P];
+  // unsigned: an id below id0, or so far from it that the difference wraps, is outside too
+  auto table_row = [&](u32 t) -> const char* {
+    const u64 v = (u64)id_at(a.ids, a.id64, min(t, a.n - 1)) - (u64)a.id0;
+    return v < (u64)a.rows ? a.table + (int64_t)v * a.ld_table : nullptr;
+  };
+  auto pos_row = [&](u32 t) -> const char* {
+    const u64 v = (u64)pos_at(a, min(t, a.n - 1));
+    return v < (u64)a.pos_rows ? a.pos_table + (int64_t)v * a.ld_pos : nullptr;
+  };
 #pragma unroll
-  for (int i = 0; i < U; ++i)
+  for (int i = 0; i < U; ++i) {
+    const u32 u0 = base + i * kInThreads, first = quotient(u0, a.groups);
+    const char *t0 = nullptr, *t1 = nullptr, *p0 = nullptr, *p1 = nullptr;
+    if constexpr (WIDE) {
+      t0 = table_row(first);
+      t1 = table_row(first + 1);
+      if (a.pos_table) {
+        p0 = pos_row(first);
+        p1 = pos_row(first + 1);
+      }
+    }
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-      const u32 u = base + i * kInThreads + piece_group<W>(lane, q);
-      row[i][q] = quotient(u, a.groups);
-      grp[i][q] = u - row[i][q] * a.groups.d;
-      const u32 col = grp[i][q] * kGroup + piece_col<W>(lane);
-      n[i][q] = u < a.units && col < a.dim ? a.dim - col : 0;
-      // behind the last unit: the id of the last row, whose table row is not read
-      tab[i][q] = id_at(a.ids, a.id64, min(row[i][q], a.n - 1));
+      const Unit w = unit_at<WIDE>(u0, piece_group<W>(lane, q), first, a.groups);
+      row[i][q] = w.row;
+      grp[i][q] = w.grp;
+      const u32 col = w.grp * kGroup + piece_col<W>(lane);
+      n[i][q] = u0 + piece_group<W>(lane, q) < a.units && col < a.dim ? a.dim - col : 0;
+      pos[i][q] = nullptr;
+      if constexpr (WIDE) {
+        tab[i][q] = w.second ? t1 : t0;
+        pos[i][q] = w.second ? p1 : p0;
+      } else {
+        tab[i][q] = table_row(w.row);
+        if (a.pos_table) pos[i][q] = pos_row(w.row);
+      }
     }
-  if (a.pos_table) {
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int q = 0; q < P; ++q) pos[i][q] = pos_at(a, min(row[i][q], a.n - 1));
   }
 #pragma unroll
   for (int i = 0; i < U; ++i)
@@ -385,12 +426,8 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
       y[i][q] = Raw<TT, W>{};
       dx[i][q] = dy[i][q] = 0;
       const int64_t col = (int64_t)(grp[i][q] * kGroup + piece_col<W>(lane)) * TT::bytes;
-      // unsigned: an id below id0, or so far from it that the difference wraps, is outside too
-      const u64 v = (u64)tab[i][q] - (u64)a.id0;
-      if (n[i][q] != 0 && v < (u64)a.rows)
-        dx[i][q] = load_w<TT, W>(a.table + (int64_t)v * a.ld_table + col, a.table_end, x[i][q]);
-      if (a.pos_table && n[i][q] != 0 && (u64)pos[i][q] < (u64)a.pos_rows)
-        dy[i][q] = load_w<TT, W>(a.pos_table + pos[i][q] * a.ld_pos + col, a.pos_end, y[i][q]);
+      if (n[i][q] != 0 && tab[i][q]) dx[i][q] = load_w<TT, W>(tab[i][q] + col, a.table_end, x[i][q]);
+      if (n[i][q] != 0 && pos[i][q]) dy[i][q] = load_w<TT, W>(pos[i][q] + col, a.pos_end, y[i][q]);
     }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -972,34 +1009,41 @@ int launched(const char* what) {
   return fail(ZERO_EHIP, buf);
 }
 
-constexpr u32 kFewUnits = 256 * 256 * 4;  // below: one unit per lane, to spread the work over the CUs
+// Units per lane of a lookup: one, or two from this many units on.  Measured with
+// bf16 rows of 4096: 8192 ids (4.2M units) 17.3 us against 18.5, 32768 ids (16.8M)
+// 78 against 64.  A dropout is never faster with two (8192 x 1600 bf16 with residual
+// 13.4 against 13.9 us, 16384 x 4097 fp32 90.9 against 91.8).
+constexpr u32 kLookupUnits = 1u << 23;
+
+// calls f(drop, wide rows) with constants
+template <class F>
+void with_form(u32 groups, u32 thr, F&& f) {
+  auto wide = [&](auto d) { groups >= 64 ? f(d, std::true_type{}) : f(d, std::false_type{}); };
+  thr ? wide(std::true_type{}) : wide(std::false_type{});
+}
+dim3 stream_grid(u32 units, int per_lane) {
+  const u64 per = (u64)kInThreads * per_lane;
+  return dim3((u32)((units + per - 1) / per));
+}
 
 template <class XT, class OT>
 void dropout_as(const DropoutLaunch& a, hipStream_t st) {
-  const dim3 b(kInThreads);
-  const u32 per = a.units < kFewUnits ? kInThreads : 2 * kInThreads;
-  const dim3 g((u32)(((u64)a.units + per - 1) / per));
-  if (per == kInThreads) {
-    if (a.drop.thr) hipLaunchKernelGGL((dropout_kernel<XT, OT, 1, true>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((dropout_kernel<XT, OT, 1, false>), g, b, 0, st, a);
-  } else {
-    if (a.drop.thr) hipLaunchKernelGGL((dropout_kernel<XT, OT, 2, true>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((dropout_kernel<XT, OT, 2, false>), g, b, 0, st, a);
-  }
+  with_form(a.groups.d, a.drop.thr, [&](auto d, auto w) {
+    hipLaunchKernelGGL((dropout_kernel<XT, OT, decltype(d)::value, decltype(w)::value>), stream_grid(a.units, 1),
+                       dim3(kInThreads), 0, st, a);
+  });
 }
 
 template <class TT, class OT>
 void lookup_as(const LookupLaunch& a, hipStream_t st) {
-  const dim3 b(kInThreads);
-  const u32 per = a.units < kFewUnits ? kInThreads : 2 * kInThreads;
-  const dim3 g((u32)(((u64)a.units + per - 1) / per));
-  if (per == kInThreads) {
-    if (a.drop.thr) hipLaunchKernelGGL((lookup_kernel<TT, OT, 1, true>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((lookup_kernel<TT, OT, 1, false>), g, b, 0, st, a);
-  } else {
-    if (a.drop.thr) hipLaunchKernelGGL((lookup_kernel<TT, OT, 2, true>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((lookup_kernel<TT, OT, 2, false>), g, b, 0, st, a);
-  }
+  with_form(a.groups.d, a.drop.thr, [&](auto d, auto w) {
+    if (a.units < kLookupUnits)
+      hipLaunchKernelGGL((lookup_kernel<TT, OT, 1, decltype(d)::value, decltype(w)::value>), stream_grid(a.units, 1),
+                         dim3(kInThreads), 0, st, a);
+    else
+      hipLaunchKernelGGL((lookup_kernel<TT, OT, 2, decltype(d)::value, decltype(w)::value>), stream_grid(a.units, 2),
+                         dim3(kInThreads), 0, st, a);
+  });
 }
 
 template <class DT, class GT, bool SORTED>

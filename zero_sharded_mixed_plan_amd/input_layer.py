@@ -10,14 +10,23 @@ libzero_shard.so (zero_embed_lookup, zero_embed_grad, zero_dropout).
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Union
 
 import torch
 
 from . import _abi
-from .optim import dtype_code
+from .optim import _CODES, dtype_code
 
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+# The calls' host time is what the smallest sizes cost, so the argument structs are
+# packed in one go (native layout, as the header declares them; the sizes are
+# checked against the ctypes declarations below) and the stream is asked for by number.
+_EMBED = struct.Struct("@PqqqiiPqqfPqqPqPqiP")
+_GRAD = struct.Struct("@PqiiPqqqqqfiPqiPPq")
+assert _EMBED.size == ctypes.sizeof(_abi.zero_embed_args_t)
+assert _GRAD.size == ctypes.sizeof(_abi.zero_embed_grad_args_t)
 
 
 class Dropout:
@@ -33,22 +42,16 @@ class Dropout:
     __slots__ = ("c", "_step", "_ref")
 
     def __init__(self, p: float, seed: int = 0, site: int = 0, step: Union[int, torch.Tensor] = 0, row0: int = 0):
-        c = _abi.zero_drop_t()
-        c.p = p
-        c.seed = seed & 0xFFFFFFFFFFFFFFFF
-        c.site = site
-        c.row0 = row0
         self._step = None
         if isinstance(step, torch.Tensor):
             if step.dtype != torch.int64 or step.numel() != 1 or not step.is_cuda:
                 raise ValueError("step must be an integer or a device int64 tensor of one element")
             self._step = step
-            c.step_dev = step.data_ptr()
-        else:
-            c.step = step
-        if c.site != site or c.row0 != row0 or (self._step is None and c.step != step):
+            step = 0
+        if not (0 <= site < 1 << 32 and 0 <= step < 1 << 32 and 0 <= row0 < 1 << 32):
             raise ValueError("site, row0 or step out of range")
-        self.c = c
+        self.c = c = _abi.zero_drop_t(p, seed & 0xFFFFFFFFFFFFFFFF, site, 0, step,
+                                      None if self._step is None else self._step.data_ptr(), row0)
         self._ref = ctypes.addressof(c)
 
     @property
@@ -56,50 +59,53 @@ class Dropout:
         return self.c.p
 
 
-def _place(*tensors):
-    """The one device of the tensors; its current stream."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be on the GPU")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors are on different devices")
-    return dev, torch.cuda.current_stream(dev).cuda_stream
+def _place(first, *others):
+    """The index of the tensors' one device."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors are on different devices" if t.is_cuda else "tensors must be on the GPU")
+    return dev.index
 
 
 def _call(fn, dev, *args):
-    """Run a library call with the tensors' device current."""
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args)
+    """Run a library call on the current stream of device `dev`, with it current."""
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != _abi.ZERO_OK:
         _abi._check(rc)
 
 
 def _rows(t: torch.Tensor, what: str):
     """A tensor [..., cols] as rows: (rows, cols, stride between rows)."""
-    if t.dim() == 2:
-        n, c = t.shape
-        if n <= 1 or t.is_contiguous():
-            if c > 1 and t.stride(1) != 1:
-                raise ValueError(f"{what}: the columns must be adjacent")
-            return n, c, c
-        if (c > 1 and t.stride(1) != 1) or t.stride(0) < c:
-            raise ValueError(f"{what}: the columns must be adjacent and the rows apart")
-        return n, c, t.stride(0)
-    if t.dim() == 0 or not t.is_contiguous():
+    shape = t.shape
+    if t.is_contiguous():
+        if len(shape) == 2:
+            return shape[0], shape[1], shape[1]
+        if len(shape) == 0:
+            raise ValueError(f"{what}: a tensor without dimensions has no rows")
+        n = 1
+        for s in shape[:-1]:
+            n *= s
+        return n, shape[-1], shape[-1]
+    if len(shape) != 2:
         raise ValueError(f"{what}: a tensor that is not a matrix must be contiguous")
-    c = t.shape[-1]
-    n = 1
-    for s in t.shape[:-1]:
-        n *= s
-    return n, c, c
+    n, c = shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the columns must be adjacent")
+    ld = t.stride(0) if n > 1 else c
+    if ld < c:
+        raise ValueError(f"{what}: the rows must not overlap")
+    return n, c, ld
+
+
+def _code(dt: torch.dtype) -> int:
+    return _CODES[dt] if dt in _CODES else dtype_code(dt)
 
 
 def _flat_ids(t: torch.Tensor, what: str) -> int:
@@ -112,10 +118,10 @@ def _flat_ids(t: torch.Tensor, what: str) -> int:
     return b
 
 
-def _drop(drop: Optional[Dropout], dev):
+def _drop(drop: Optional[Dropout], dev: int) -> int:
     if drop is None:
-        return None
-    if drop._step is not None and drop._step.device != dev:
+        return 0
+    if drop._step is not None and drop._step.device.index != dev:
         raise ValueError("the dropout's step is on another device")
     return drop._ref
 
@@ -136,14 +142,13 @@ def dropout(x: torch.Tensor, drop: Optional[Dropout], *, residual: Optional[torc
         raise ValueError("x, residual and out must have one shape")
     if residual is not None and residual.dtype != out.dtype:
         raise ValueError("residual and out must have one type")
-    dev, st = _place(x, residual, out)
+    dev = _place(x, residual, out)
     n, cols, ld_x = _rows(x, "x")
     if n == 0 or cols == 0:
         return out
-    ld_r = 0 if residual is None else _rows(residual, "residual")[2]
-    _call(_abi.lib().zero_dropout, dev, x.data_ptr(), ld_x, dtype_code(x.dtype),
-          None if residual is None else residual.data_ptr(), ld_r, out.data_ptr(), _rows(out, "out")[2],
-          dtype_code(out.dtype), n, cols, _drop(drop, dev), st or None)
+    ptr_r, ld_r = (0, 0) if residual is None else (residual.data_ptr(), _rows(residual, "residual")[2])
+    _call(_abi.lib().zero_dropout, dev, x.data_ptr(), ld_x, _code(x.dtype), ptr_r, ld_r, out.data_ptr(),
+          _rows(out, "out")[2], _code(out.dtype), n, cols, _drop(drop, dev))
     return out
 
 
@@ -165,41 +170,29 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, id0
         out = torch.empty((*ids.shape, dim), dtype=out_dtype or table.dtype, device=table.device)
     elif out.shape != (*ids.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [*ids.shape, dim] of out_dtype")
-    a = _abi.zero_embed_args_t()
+    ptr_pt = ld_pt = n_pt = ptr_pos = 0
     if pos_table is not None:
-        if pos_table.dim() != 2 or pos_table.shape[1] != dim or pos_table.dtype != table.dtype:
+        n_pt, pos_dim, ld_pt = _rows(pos_table, "pos_table")
+        if pos_table.dim() != 2 or pos_dim != dim or pos_table.dtype != table.dtype:
             raise ValueError("pos_table must be [positions, dim] of the table's type")
-        a.pos_rows, _, a.ld_pos = _rows(pos_table, "pos_table")
-        a.pos_table = pos_table.data_ptr()
+        ptr_pt = pos_table.data_ptr()
         if pos is not None:
             if pos.shape != ids.shape or pos.dtype != ids.dtype:
                 raise ValueError("pos must have the shape and type of ids")
             _flat_ids(pos, "pos")
-            a.pos = pos.data_ptr()
+            ptr_pos = pos.data_ptr()
         elif pos_period < 1:
             raise ValueError("pos_table needs pos or a pos_period of at least 1")
-        a.pos_period = pos_period
     elif pos is not None:
         raise ValueError("pos without a pos_table")
-    dev, st = _place(ids, table, out, pos_table, pos)
+    dev = _place(table, ids, out, pos_table, pos)
     n = ids.numel()
     if n == 0 or dim == 0:
         return out
-    a.table = table.data_ptr()
-    a.ld_table = ld
-    a.rows = rows
-    a.id0 = id0
-    a.table_dtype = dtype_code(table.dtype)
-    a.id_bytes = idb
-    a.ids = ids.data_ptr()
-    a.n_ids = n
-    a.dim = dim
-    a.scale = scale
-    a.out = out.data_ptr()
-    a.ld_out = _rows(out, "out")[2]
-    a.out_dtype = dtype_code(out.dtype)
-    a.drop = _drop(drop, dev)
-    _call(_abi.lib().zero_embed_lookup, dev, ctypes.addressof(a), st or None)
+    _call(_abi.lib().zero_embed_lookup, dev, _EMBED.pack(
+        table.data_ptr(), ld, rows, id0, _code(table.dtype), idb, ids.data_ptr(), n, dim, scale,
+        ptr_pt, ld_pt, n_pt, ptr_pos, pos_period, out.data_ptr(), _rows(out, "out")[2], _code(out.dtype),
+        _drop(drop, dev)))
     return out
 
 
@@ -228,39 +221,24 @@ def embedding_grad(dy: torch.Tensor, ids: Optional[torch.Tensor], grad: torch.Te
     n, cols, ld_dy = _rows(dy, "dy")
     if cols != dim:
         raise ValueError("dy and grad must have one width")
-    a = _abi.zero_embed_grad_args_t()
-    a.id_bytes = 8
+    ptr_ids, idb = 0, 8
     if ids is not None:
         if ids.shape != dy.shape[:-1]:
             raise ValueError("dy must be [*ids.shape, dim]")
-        a.id_bytes = _flat_ids(ids, "ids")
-        a.ids = ids.data_ptr() if n else None
+        idb = _flat_ids(ids, "ids")
+        ptr_ids = ids.data_ptr() if n else 0
     elif period < 1:
         raise ValueError("ids None needs a period of at least 1")
-    a.period = max(period, 1)
-    dev, st = _place(dy, grad, ids, workspace)
+    dev = _place(grad, dy, ids, workspace)
     if rows == 0 or dim == 0:
         return grad
     L = _abi.lib()
     if workspace is None:
-        need = L.zero_embed_grad_ws_bytes(n, rows, dim)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(L.zero_embed_grad_ws_bytes(n, rows, dim), dtype=torch.uint8, device=grad.device)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    a.dy = dy.data_ptr()
-    a.ld_dy = ld_dy
-    a.dy_dtype = dtype_code(dy.dtype)
-    a.n_ids = n
-    a.dim = dim
-    a.id0 = id0
-    a.rows = rows
-    a.scale = scale
-    a.grad_dtype = dtype_code(grad.dtype)
-    a.grad = grad.data_ptr()
-    a.ld_grad = ld_grad
-    a.accumulate = 1 if accumulate else 0
-    a.drop = _drop(drop, dev)
-    a.ws = workspace.data_ptr()
-    a.ws_bytes = workspace.numel()
-    _call(L.zero_embed_grad, dev, ctypes.addressof(a), st or None)
+    _call(L.zero_embed_grad, dev, _GRAD.pack(
+        dy.data_ptr(), ld_dy, _code(dy.dtype), idb, ptr_ids, max(period, 1), n, dim, id0, rows, scale,
+        _code(grad.dtype), grad.data_ptr(), ld_grad, 1 if accumulate else 0, _drop(drop, dev),
+        workspace.data_ptr(), workspace.numel()))
     return grad
