@@ -175,28 +175,16 @@ __device__ __forceinline__ void store_n(char* p, const float* v, u32 n) {
 
 __device__ __forceinline__ u32 quotient(u32 n, const FastDiv& f) { return (u32)(((u64)n * f.m) >> f.sh); }
 
-// (row, group) of unit u0 + i, for i < 64 and the wave's first unit u0.  WIDE: a row
-// has at least 64 groups, so the wave meets at most two rows, first and first + 1,
-// and what belongs to them is found once for the wave by scalar instructions rather than
-// by every lane (lookup of 32768 rows, 4096 wide: 66 us against 79).
+// (row, group) of unit u0 + i, for i < 64 and the wave's first unit u0 in row `first`.
+// ONE: a row's groups are a multiple of 64, so the wave has one row, and what belongs
+// to it is found once by scalar instructions rather than by every lane.
 struct Unit {
   u32 row, grp;
-  bool second;
 };
-template <bool WIDE>
+template <bool ONE>
 __device__ __forceinline__ Unit unit_at(u32 u0, u32 i, u32 first, const FastDiv& groups) {
-  Unit r;
-  if constexpr (WIDE) {
-    const u32 at = u0 - first * groups.d + i;  // counted from the first row's beginning
-    r.second = at >= groups.d;
-    r.row = first + (r.second ? 1 : 0);
-    r.grp = at - (r.second ? groups.d : 0);
-  } else {
-    r.second = false;
-    r.row = quotient(u0 + i, groups);
-    r.grp = u0 + i - r.row * groups.d;
-  }
-  return r;
+  const u32 row = ONE ? first : quotient(u0 + i, groups);
+  return Unit{row, u0 + i - row * groups.d};
 }
 
 // ---------------------------------------------------------------------------
@@ -229,35 +217,44 @@ __device__ __forceinline__ u32 drop_step(const DropK& d) {
   return d.step_dev ? (u32)*d.step_dev : d.step;
 }
 
-// Zeroes the dropped among a lane's 8 values; the kept are not scaled.  (row, group)
-// is the group whose numbers this lane computes: its own (W = 8), or that of piece
-// lane % 2 (W = 4), where the two lanes of a pair hold half of each group and
-// exchange two words.  Every lane of the wave has to take part.
+// The random words of a lane's 8 values.  (row, group) is the group whose numbers this
+// lane computes: its own (W = 8), or that of piece lane % 2 (W = 4), where the two
+// lanes of a pair hold half of each group and exchange two words.  Every lane of the
+// wave has to take part.  Drawn after the loads of the values are issued and before they are used,
+// the words cost little time of their own.
+struct Words {
+  u32 w[4];
+};
 template <int W>
-__device__ __forceinline__ void drop8(const DropK& d, u32 step, u32 row, u32 group, float v[8]) {
+__device__ __forceinline__ Words draw(const DropK& d, u32 step, u32 row, u32 group) {
   // The empty asm keeps the compiler from holding all twenty round keys in scalar
   // registers across calls (the gradient's unrolled loop ran out of them); two
   // scalar adds a round are free beside the vector multiplies.
-  u32 k0 = d.key0, k1 = d.key1, w[4];
+  u32 k0 = d.key0, k1 = d.key1;
   asm volatile("" : "+s"(k0), "+s"(k1));
-  philox(group, d.row0 + row, step, d.site, k0, k1, w);
+  Words r;
+  philox(group, d.row0 + row, step, d.site, k0, k1, r.w);
   if constexpr (W == 4) {
     const bool odd = threadIdx.x & 1;
     // to the other lane of the pair: quad_perm [1, 0, 3, 2]
-    const u32 a = __builtin_amdgcn_mov_dpp((int)(odd ? w[0] : w[2]), 0xB1, 0xF, 0xF, true);
-    const u32 b = __builtin_amdgcn_mov_dpp((int)(odd ? w[1] : w[3]), 0xB1, 0xF, 0xF, true);
+    const u32 a = __builtin_amdgcn_mov_dpp((int)(odd ? r.w[0] : r.w[2]), 0xB1, 0xF, 0xF, true);
+    const u32 b = __builtin_amdgcn_mov_dpp((int)(odd ? r.w[1] : r.w[3]), 0xB1, 0xF, 0xF, true);
     if (odd) {
-      w[0] = a;
-      w[1] = b;
+      r.w[0] = a;
+      r.w[1] = b;
     } else {
-      w[2] = a;
-      w[3] = b;
+      r.w[2] = a;
+      r.w[3] = b;
     }
   }
+  return r;
+}
+// zeroes the dropped among the values; the kept are not scaled
+__device__ __forceinline__ void drop8(const DropK& d, const Words& r, float v[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v[2 * j] = (w[j] & 0xffffu) >= d.thr ? v[2 * j] : 0.0f;
-    v[2 * j + 1] = (w[j] >> 16) >= d.thr ? v[2 * j + 1] : 0.0f;
+    v[2 * j] = (r.w[j] & 0xffffu) >= d.thr ? v[2 * j] : 0.0f;
+    v[2 * j + 1] = (r.w[j] >> 16) >= d.thr ? v[2 * j + 1] : 0.0f;
   }
 }
 
@@ -288,7 +285,7 @@ __global__ void dropout_short_kernel(const DropoutLaunch a, int xt, int ot) {
 }
 
 // A unit is (row, 8-column group), numbered row by row; a wave takes 64 consecutive ones.
-template <class XT, class OT, bool DROP, bool WIDE>
+template <class XT, class OT, bool DROP, bool ONE>
 __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch a) {
   constexpr int W = kWidth<XT, OT>, P = 8 / W;
   const u32 lane = threadIdx.x & 63;
@@ -300,7 +297,7 @@ __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch
   Raw<OT, W> r[P];
 #pragma unroll
   for (int q = 0; q < P; ++q) {
-    const Unit w = unit_at<WIDE>(u0, piece_group<W>(lane, q), first, a.groups);
+    const Unit w = unit_at<ONE>(u0, piece_group<W>(lane, q), first, a.groups);
     row[q] = w.row;
     grp[q] = w.grp;
     const u32 col = w.grp * kGroup + piece_col<W>(lane);
@@ -310,6 +307,8 @@ __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch
     dx[q] = load_w<XT, W>(a.x + (int64_t)w.row * a.ld_x + (int64_t)col * XT::bytes, a.x_end, x[q]);
     if (a.res) dr[q] = load_w<OT, W>(a.res + (int64_t)w.row * a.ld_res + (int64_t)col * OT::bytes, a.res_end, r[q]);
   }
+  Words random{};
+  if constexpr (DROP) random = draw<W>(a.drop, step, own_piece<P>(lane, row), own_piece<P>(lane, grp));
   float v[8];
 #pragma unroll
   for (int q = 0; q < P; ++q) {
@@ -319,7 +318,7 @@ __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch
   if constexpr (DROP) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= a.drop.ks;
-    drop8<W>(a.drop, step, own_piece<P>(lane, row), own_piece<P>(lane, grp), v);
+    drop8(a.drop, random, v);
   }
 #pragma unroll
   for (int q = 0; q < P; ++q) {
@@ -370,7 +369,7 @@ __global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
 }
 
 // As above, with U times 64 units a wave, 256 apart, all loads before the arithmetic.
-template <class TT, class OT, int U, bool DROP, bool WIDE>
+template <class TT, class OT, int U, bool DROP, bool ONE>
 __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a) {
   constexpr int W = kWidth<TT, OT>, P = 8 / W;
   const u32 lane = threadIdx.x & 63;
@@ -392,26 +391,22 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const u32 u0 = base + i * kInThreads, first = quotient(u0, a.groups);
-    const char *t0 = nullptr, *t1 = nullptr, *p0 = nullptr, *p1 = nullptr;
-    if constexpr (WIDE) {
+    const char *t0 = nullptr, *p0 = nullptr;
+    if constexpr (ONE) {
       t0 = table_row(first);
-      t1 = table_row(first + 1);
-      if (a.pos_table) {
-        p0 = pos_row(first);
-        p1 = pos_row(first + 1);
-      }
+      if (a.pos_table) p0 = pos_row(first);
     }
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-      const Unit w = unit_at<WIDE>(u0, piece_group<W>(lane, q), first, a.groups);
+      const Unit w = unit_at<ONE>(u0, piece_group<W>(lane, q), first, a.groups);
       row[i][q] = w.row;
       grp[i][q] = w.grp;
       const u32 col = w.grp * kGroup + piece_col<W>(lane);
       n[i][q] = u0 + piece_group<W>(lane, q) < a.units && col < a.dim ? a.dim - col : 0;
       pos[i][q] = nullptr;
-      if constexpr (WIDE) {
-        tab[i][q] = w.second ? t1 : t0;
-        pos[i][q] = w.second ? p1 : p0;
+      if constexpr (ONE) {
+        tab[i][q] = t0;
+        pos[i][q] = p0;
       } else {
         tab[i][q] = table_row(w.row);
         if (a.pos_table) pos[i][q] = pos_row(w.row);
@@ -429,6 +424,12 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
       if (n[i][q] != 0 && tab[i][q]) dx[i][q] = load_w<TT, W>(tab[i][q] + col, a.table_end, x[i][q]);
       if (n[i][q] != 0 && pos[i][q]) dy[i][q] = load_w<TT, W>(pos[i][q] + col, a.pos_end, y[i][q]);
     }
+  Words random[U];
+  if constexpr (DROP) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      random[i] = draw<W>(a.drop, step, a.t0 + own_piece<P>(lane, row[i]), own_piece<P>(lane, grp[i]));
+  }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     float v[8];
@@ -449,7 +450,7 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
     if constexpr (DROP) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= a.drop.ks;
-      drop8<W>(a.drop, step, a.t0 + own_piece<P>(lane, row[i]), own_piece<P>(lane, grp[i]), v);
+      drop8(a.drop, random[i], v);
     }
 #pragma unroll
     for (int q = 0; q < P; ++q) {
@@ -813,6 +814,12 @@ __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a
           if (a.n - t <= kGroup) move_down<DT, W>(x[b][q], d);
         }
       }
+    Words random[B];
+    if constexpr (DROP) {
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (i0 + b < hi) random[b] = draw<W>(a.drop, step, __builtin_amdgcn_readlane(e.x, i0 + b), drop_group);
+    }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       const u32 i = i0 + b;
@@ -820,7 +827,7 @@ __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a
       float v[8];
 #pragma unroll
       for (int q = 0; q < P; ++q) widen<DT, W>(x[b][q], v + q * W);
-      if constexpr (DROP) drop8<W>(a.drop, step, __builtin_amdgcn_readlane(e.x, i), drop_group, v);
+      if constexpr (DROP) drop8(a.drop, random[b], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += v[j];
       if (ends >> i & 1) {
@@ -947,13 +954,19 @@ __global__ __launch_bounds__(kSortThreads) void grad_once_kernel(const GradLaunc
             if (a.n - t[b] <= kGroup) move_down<DT, W>(x[b][q], d);
           }
         }
+      Words random[B];
+      if constexpr (DROP) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          if (i0 + b < hi) random[b] = draw<W>(a.drop, step, t[b], drop_group);
+      }
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         if (i0 + b >= hi) break;
         float v[8];
 #pragma unroll
         for (int q = 0; q < P; ++q) widen<DT, W>(x[b][q], v + q * W);
-        if constexpr (DROP) drop8<W>(a.drop, step, t[b], drop_group, v);
+        if constexpr (DROP) drop8(a.drop, random[b], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += v[j];
       }
@@ -1015,11 +1028,11 @@ int launched(const char* what) {
 // 13.4 against 13.9 us, 16384 x 4097 fp32 90.9 against 91.8).
 constexpr u32 kLookupUnits = 1u << 23;
 
-// calls f(drop, wide rows) with constants
+// calls f(drop, one row per wave) with constants
 template <class F>
 void with_form(u32 groups, u32 thr, F&& f) {
-  auto wide = [&](auto d) { groups >= 64 ? f(d, std::true_type{}) : f(d, std::false_type{}); };
-  thr ? wide(std::true_type{}) : wide(std::false_type{});
+  auto one = [&](auto d) { groups % 64 == 0 ? f(d, std::true_type{}) : f(d, std::false_type{}); };
+  thr ? one(std::true_type{}) : one(std::false_type{});
 }
 dim3 stream_grid(u32 units, int per_lane) {
   const u64 per = (u64)kInThreads * per_lane;
