@@ -15,6 +15,7 @@ import numpy as np
 import pytest
 import torch
 
+import zero_sharded_mixed_plan_amd as Z
 from oracle import input_layer as OI
 from oracle import step as OS
 from gpu_harness import say, storage
@@ -245,6 +246,8 @@ def _ids(kind, n, rows, rng):
         return np.where(np.arange(n) < n // 3 + 1, rows // 2, 0)
     if kind == "outside":
         return rng.integers(-5, rows + 5, size=n)
+    if kind == "in turn":                             # every row equally often
+        return rng.permutation(np.arange(n) % rows)
     if kind == "none inside":
         return np.full(n, -1)
     if kind == "each once":
@@ -270,6 +273,15 @@ GRAD = [  # n, rows, dim, dy, grad, ids, kind, scale, p, offset, pad, id0
     (70001, 2000, 16, "bf16", "f32", torch.int32, "zipf", 1.0, 0.1, 0, 0, 0),
     (300, 300000, 24, "bf16", "bf16", torch.int64, "uniform", 1.0, 0.0, 0, 0, 0),
     (200, 64, 1100, "f32", "f32", torch.int64, "zipf", 1.0, 1.0, 0, 0, 0),
+    # the most rows a workgroup of the order pass counts, with its longest lists
+    (20000, 262144, 8, "f32", "f32", torch.int32, "zipf", 1.0, 0.0, 0, 0, 0),
+    # three launches and one, on either side of the rule between them
+    (1024, 900, 512, "bf16", "f32", torch.int64, "two", 1.0, 0.1, 0, 0, 0),
+    (1025, 900, 512, "bf16", "f32", torch.int64, "two", 1.0, 0.1, 0, 0, 0),
+    # runs of exactly a chunk, and one more
+    (8 * 41, 41, 600, "f32", "f32", torch.int64, "uniform", 1.0, 0.0, 0, 0, 0),
+    (40000, 1250, 24, "bf16", "f32", torch.int64, "in turn", 1.0, 0.0, 0, 0, 0),
+    (41250, 1250, 24, "bf16", "f32", torch.int64, "in turn", 1.0, 0.0, 0, 0, 0),
 ]
 
 
@@ -361,6 +373,24 @@ def test_gradient_hides_dropped_infinities_and_padding():
     a = L.embedding_grad(x, ids, torch.empty(7, dim, device="cuda"), drop=d)
     b = L.embedding_grad(bad, ids, torch.empty(7, dim, device="cuda"), drop=d)
     assert torch.equal(a, b)
+
+
+def test_empty_batch_zeroes_the_gradient():
+    """No ids: every row is zero, with an id array and without, through the C call."""
+    for rows, dim in ((5, 40), (3000, 600)):
+        for accumulate in (0, 1):
+            grad = torch.full((rows, dim), 3.0, device="cuda")
+            ws = torch.empty(Z.zero_embed_grad_ws_bytes(0, rows, dim), dtype=torch.uint8, device="cuda")
+            a = Z.zero_embed_grad_args_t()
+            a.dy, a.ids, a.id_bytes = ws.data_ptr(), ws.data_ptr(), 8
+            a.dim, a.rows, a.ld_grad, a.ld_dy = dim, rows, dim, dim
+            a.scale, a.grad, a.accumulate = 1.0, grad.data_ptr(), accumulate
+            a.ws, a.ws_bytes = ws.data_ptr(), ws.numel()
+            Z.zero_embed_grad(a, torch.cuda.current_stream().cuda_stream)
+            assert bool((grad == (3.0 if accumulate else 0.0)).all())
+            ids = torch.empty(0, dtype=torch.int64, device="cuda")
+            L.embedding_grad(torch.empty(0, dim, device="cuda"), ids, grad, accumulate=bool(accumulate))
+            assert bool((grad == (3.0 if accumulate else 0.0)).all())
 
 
 def test_workspace_of_a_larger_call_serves_a_smaller_one():

@@ -2,6 +2,9 @@
 vectors, and arguments that the library and the torch layer refuse before
 anything is enqueued (no GPU is touched here)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -188,11 +191,23 @@ def test_workspace_bytes():
         assert f(*bad) == 0
 
 
-def test_structs_match_the_header():
-    """Sizes and the last fields' places as the C compiler lays them out."""
-    assert ctypes.sizeof(Z.zero_drop_t) == 48 and Z.zero_drop_t.row0.offset == 40
-    assert ctypes.sizeof(Z.zero_embed_args_t) == 144 and Z.zero_embed_args_t.drop.offset == 136
-    assert ctypes.sizeof(Z.zero_embed_grad_args_t) == 128 and Z.zero_embed_grad_args_t.ws_bytes.offset == 120
+def test_structs_match_the_header(tmp_path):
+    """Sizes and every field's place as the C compiler lays the header's structs out."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    types = {"zero_drop_t": Z.zero_drop_t, "zero_embed_args_t": Z.zero_embed_args_t,
+             "zero_embed_grad_args_t": Z.zero_embed_grad_args_t}
+    body = "".join(f'printf("%zu\\n", sizeof({n}));' +
+                   "".join(f'printf("%zu\\n", offsetof({n}, {f[0]}));' for f in t._fields_)
+                   for n, t in types.items())
+    src = tmp_path / "layout.c"
+    src.write_text(f"#include <stdio.h>\n#include <zero_shard.h>\nint main(void) {{ {body} return 0; }}\n")
+    cc = shutil.which("gcc") or shutil.which("cc")
+    subprocess.run([cc, "-std=c11", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "layout")],
+                   check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "layout")], check=True, capture_output=True,
+                                          text=True).stdout.split()]
+    want = [x for t in types.values() for x in [ctypes.sizeof(t)] + [getattr(t, f[0]).offset for f in t._fields_]]
+    assert got == want
 
 
 def test_torch_layer_refuses():

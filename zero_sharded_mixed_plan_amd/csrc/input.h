@@ -81,7 +81,7 @@ constexpr int kMaxLgChunk = 5;       // 8, 16 or 32
 constexpr int kGradWaves = 4096;     // as few as leave this many waves for the sums
 constexpr int kFillBytes = 8192;     // zeroed by one workgroup, or one row
 // zeroed beside the sort, whose time grows with the ids
-constexpr int64_t kEarlyBytes = 16 << 20, kEarlyBytesPerId = 2048, kEarlyGroupBytes = 65536;
+constexpr int64_t kEarlyBytes = 24 << 20, kEarlyBytesPerId = 1536, kEarlyGroupBytes = 65536;
 // One launch instead of three for at most this many ids times slabs of 512 columns
 // and this many bytes of gradient.  Measured against three: 64 ids, 256 x 64 fp32
 // 5.9 us (9.0), 1024 ids, 1000 x 256 fp32 9.3 (14.1).  Beyond, its 256 workgroups zero

@@ -1100,7 +1100,7 @@ int grad_as(GradLaunch a, hipStream_t st) {
   if (a.places > 0 && a.longest > 1u << a.lg_chunk) {
     // few places leave each workgroup few runs, many of them keep the workgroups few
     a.join_places = kJoinThreads;
-    while (a.join_places > 128 && (u64)a.places * a.slabs < (u64)a.join_places * kJoinGroups) a.join_places /= 2;
+    while (a.join_places > 64 && (u64)a.places * a.slabs < (u64)a.join_places * kJoinGroups) a.join_places /= 2;
     const u32 blocks = (a.places + a.join_places - 1) / a.join_places;
     hipLaunchKernelGGL((grad_join_kernel<GT, kWidth<DT, GT>, SORTED>), dim3(blocks * a.slabs), dim3(kJoinThreads), 0,
                        st, a);
