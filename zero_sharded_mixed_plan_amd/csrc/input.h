@@ -76,21 +76,31 @@ constexpr int kSortMinClasses = 256; // one workgroup per CU
 constexpr int kSortList = 1024;      // own positions a wave keeps in LDS between its two passes, at most
 constexpr int kSortAhead = 8;        // loads of 64 ids in flight per wave
 constexpr int kSortKeys = 1024;      // rows of one class at most: a list's entry has 10 bits for the row
-constexpr int kMinChunk = 8;         // places of a run that one wave sums:
-constexpr int kMaxLgChunk = 5;       // 8, 16 or 32
-constexpr int kGradWaves = 4096;     // as few as leave this many waves for the sums
-constexpr int kFillBytes = 8192;     // zeroed by one workgroup, or one row
-// zeroed beside the sort, whose time grows with the ids
+// Places of a run that one wave sums: 8, 16 or 32, the most that leave kGradWaves
+// waves for the sums (8192 ids, 1600 wide: 16 against 8 with twice the waves, 45.1
+// against 48.6 us; 3001 ids, 777 wide: 8 against 16, 22 against 27 us).
+constexpr int kMinChunk = 8;
+constexpr int kMaxLgChunk = 5;
+constexpr int kGradWaves = 4096;
+// Zeroed by one workgroup, or one row: 8 KiB; 16 to 64 KiB took 37 to 38 us for 8192
+// ids into 50257 x 1600 bf16 (36.7) and 330 to 339 for 65536 into 128256 x 4096 (316).
+constexpr int kFillBytes = 8192;
+// Zeroed beside the sort, whose time grows with the ids: 8192 ids into 50257 x 1600
+// bf16 36.7 us, against 42 with none and 39.6 with 8 MiB and 1.5 KiB an id; 65536 into 128256 x
+// 4096 316 us against 320.
 constexpr int64_t kEarlyBytes = 24 << 20, kEarlyBytesPerId = 1536, kEarlyGroupBytes = 65536;
 // One launch instead of three for at most this many ids times slabs of 512 columns
-// and this many bytes of gradient.  Measured against three: 64 ids, 256 x 64 fp32
-// 5.9 us (9.0), 1024 ids, 1000 x 256 fp32 9.3 (14.1).  Beyond, its 256 workgroups zero
-// too slowly (50257 x 1600 bf16 47 to 59 us against 30 to 37), and an id that fills
-// the batch waits for one CU (256 times one id, 1600 wide, 21 us against 11; 1024
-// times 86 against 16).
+// and this many bytes of gradient, in rows not too many to go through.  Measured
+// against three: 64 ids, 256 x 64 fp32 5.9 us (9.0), 1024 ids, 1000 x 256 fp32 9.3
+// (14.1), 16 to 500 ids, 30000 x 32 to 1000 x 1024 fp32 5.7 to 10.7 (9.2 to 14.1).  Beyond,
+// its 256 workgroups zero too slowly (50257 x 1600 bf16 47 to 59 us against 30 to 37),
+// 400 rows each take 18 us (100000 x 8 fp32, against 10 to 13), and an id that
+// fills the batch waits for one CU (256 times one id, 1600 wide, 21 us against 11;
+// 1024 times 86 against 16).
 constexpr uint32_t kOnceIds = 1024;
 constexpr int64_t kOnceBytes = 4 << 20;
-constexpr uint32_t kOnceRun = 16;   // ids of a row that one wave sums there
+constexpr uint32_t kOnceKeys = 128;  // rows of one class
+constexpr uint32_t kOnceRun = 16;    // ids of a row that one wave sums there
 constexpr int kJoinThreads = 512;
 constexpr int kJoinGroups = 512;
 

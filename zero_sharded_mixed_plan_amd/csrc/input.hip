@@ -9,6 +9,11 @@
 // Philox4x32-10 call, whose 128 bits serve 8 elements with 16 bits each.
 // Tensors sit anywhere in a flat buffer, so vectors are element aligned only;
 // gfx950 takes 16-byte global accesses at any such address.
+// Results are stored non-temporally: they are read by another kernel, if at all,
+// and leave the L2 to what is read again (8192 x 1600 bf16, dropout with residual,
+// 13.6 us against 15.5; lookup of 32768 rows of 4096, 79 against 85).
+// Figures here are of one MI355X, calls back to back from a graph on four sets of inputs;
+// a plain streaming copy of 2 GiB moves 6.6 TB/s there.
 // Arithmetic is IEEE fp32, one rounding per operation (the build disables
 // contraction); 16-bit results are rounded once, to nearest even.
 #include <hip/hip_runtime.h>
@@ -268,7 +273,7 @@ __device__ __forceinline__ bool kept(const DropK& d, u32 row, u32 col) {
 }
 
 // Tensors of fewer than 8 elements are too short for the vector accesses of the
-// kernels below; one workgroup serves them element by element.
+// kernels below; the *_short_kernels serve them element by element.
 
 // ---------------------------------------------------------------------------
 // dropout
@@ -285,6 +290,8 @@ __global__ void dropout_short_kernel(const DropoutLaunch a, int xt, int ot) {
 }
 
 // A unit is (row, 8-column group), numbered row by row; a wave takes 64 consecutive ones.
+// Bound by HBM: 8192 x 1600 bf16 with residual 13.0 us (6.0 TB/s), 16384 x 4097 fp32 92 us
+// (5.8 TB/s); the vector units are busy a third of the time.
 template <class XT, class OT, bool DROP, bool ONE>
 __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch a) {
   constexpr int W = kWidth<XT, OT>, P = 8 / W;
@@ -369,6 +376,10 @@ __global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
 }
 
 // As above, with U times 64 units a wave, 256 apart, all loads before the arithmetic.
+// 32768 of 128256 rows of 4096 bf16: 66 us.  Its 371 MB would take 56 us at the copy's
+// rate; the eight L2 caches between them fetch the frequent rows again, 450 MB in all,
+// which it moves at 6.8 TB/s.  8192 x 1600 bf16 with positions and dropout: 11.8
+// us for 41 MB; there the random words' arithmetic and two dependent loads set the pace.
 template <class TT, class OT, int U, bool DROP, bool ONE>
 __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a) {
   constexpr int W = kWidth<TT, OT>, P = 8 / W;
@@ -474,6 +485,13 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
 //    same launch zero the rows without an id.
 // 3. grad_join_kernel adds the partial rows of each longer run, in order.
 // No floating-point atomics: the same call gives the same bits.
+// The smallest calls take one launch instead (grad_once_kernel).
+//
+// The gradient is mostly a write: 8192 ids into 50257 x 1600 bf16 move 187 MB, of
+// which 161 MB are the result, and take 36.7 us, 28.4 at the copy's rate: 8.5 us order (39 MB
+// of zero rows beside it), 24 us sums, 4 us joins.  65536 ids into 128256 x 4096 bf16
+// (1.59 GB): 316 us, 241 at the copy's rate: 45 us order (128 MB of zero rows), 260 us
+// sums at 5.7 TB/s, 9 us joins.
 
 // The row of position t's id, or kNoRow.
 constexpr u32 kNoRow = ~0u;
@@ -487,7 +505,9 @@ __device__ __forceinline__ u32 row_of_id(const GradLaunch& a, u64 id) {
 // Every workgroup reads all ids, counts those of lower classes -- which is where its
 // own begin in the order -- and lists its own.  Nothing passes between workgroups.
 // Wave w owns a contiguous range of positions; cnt[w][k] first counts its ids of
-// the class's row k, then holds the place of its next one.
+// the class's row k, then holds the place of its next one.  The scan is a compare
+// and a ballot per 64 ids; the few own ones go to a list, and counting and placing
+// run over that.  8192 ids: 8 us, 65536: 25 us, bound by instruction issue.
 //   lds: cnt[kSortWaves][keys], start[keys] (the first place of row k), tot[keys] (its
 //        ids), lists [kSortWaves][a.list]
 // Calls counted(first place of the class, first place behind it) between the two
@@ -562,6 +582,7 @@ __device__ __forceinline__ void order_class(const GradLaunch& a, u32 cls, u32* c
     listed += (u32)__popcll(own);
     if ((own >> lane & 1) && at < a.list) list[at] = (t + lane - t_lo) << 10 | row >> a.lg_classes;
   });
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the list is read by other lanes of the wave
   // calls f(own lanes, position, row of the class) for the wave's own positions in
   // order, from its list or, where that is too short, from the ids again
   auto own_positions = [&](auto&& f) {
@@ -764,7 +785,9 @@ __device__ __forceinline__ void fill_rows(const GradLaunch& a, u32 r0) {
 template <bool DROP> constexpr int kSumBatch = DROP ? 4 : 8;
 
 // One wave per (window of a.window places, 512 columns): it sums the chunks that
-// begin in the window.  A chunk may end up to a.chunk - 1 places behind it.
+// begin in the window.  A chunk may end up to a.chunk - 1 places behind it.  The
+// workgroups that zero come after those that sum, and keep the memory busy while
+// the last of these wait for their rows.
 template <class DT, class GT, bool SORTED, bool DROP>
 __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a) {
   constexpr int W = kWidth<DT, GT>, P = 8 / W, B = kSumBatch<DROP>;
@@ -975,25 +998,29 @@ __global__ __launch_bounds__(kSortThreads) void grad_once_kernel(const GradLaunc
 
   // long runs first: all waves meet there
   const u32 across = min(a.slabs, (u32)kSortWaves), splits = kSortWaves / across;
-  for (u32 k = 0; k < a.keys; ++k) {
-    const u32 len = __builtin_amdgcn_readfirstlane(tot[k]);
-    if (len <= kOnceRun) continue;
-    const u32 row = (k << a.lg_classes) + cls, at = __builtin_amdgcn_readfirstlane(start[k]) - first;
-    const u32 split = wave / across, each = (len + splits - 1) / splits;
-    for (u32 s0 = 0; s0 < a.slabs; s0 += across) {
-      const u32 slab = s0 + wave % across;
-      float acc[8] = {};
-      if (split < splits && slab < a.slabs) sum(at + min(len, split * each), at + min(len, (split + 1) * each), slab, acc);
+  const u32 split = wave / across;
+  for (u32 k0 = 0; k0 < a.keys; k0 += 64) {
+    u64 longs = __ballot(k0 + lane < a.keys && tot[min(k0 + lane, a.keys - 1)] > kOnceRun);
+    for (; longs; longs &= longs - 1) {
+      const u32 k = k0 + (u32)__builtin_ctzll(longs), row = (k << a.lg_classes) + cls;
+      const u32 len = __builtin_amdgcn_readfirstlane(tot[k]), at = __builtin_amdgcn_readfirstlane(start[k]) - first;
+      const u32 each = (len + splits - 1) / splits;
+      for (u32 s0 = 0; s0 < a.slabs; s0 += across) {
+        const u32 slab = s0 + wave % across;
+        float acc[8] = {};
+        if (split < splits && slab < a.slabs)
+          sum(at + min(len, split * each), at + min(len, (split + 1) * each), slab, acc);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) part[wave][lane][j] = acc[j];
-      __syncthreads();
-      if (split == 0 && slab < a.slabs) {
-        for (u32 w = 1; w < splits; ++w)
+        for (int j = 0; j < 8; ++j) part[wave][lane][j] = acc[j];
+        __syncthreads();
+        if (split == 0 && slab < a.slabs) {
+          for (u32 w = 1; w < splits; ++w)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] += part[w * across + wave][lane][j];
-        write_row8<GT, W>(a, row, slab, lane, acc);
+            for (int j = 0; j < 8; ++j) acc[j] += part[w * across + wave][lane][j];
+          write_row8<GT, W>(a, row, slab, lane, acc);
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
   for (u32 i = wave; i < a.keys * a.slabs; i += kSortWaves) {
@@ -1023,8 +1050,8 @@ int launched(const char* what) {
 }
 
 // Units per lane of a lookup: one, or two from this many units on.  Measured with
-// bf16 rows of 4096: 8192 ids (4.2M units) 17.3 us against 18.5, 32768 ids (16.8M)
-// 78 against 64.  A dropout is never faster with two (8192 x 1600 bf16 with residual
+// bf16 rows of 4096: 8192 ids (4.2M units) 17.5 us against 18.3, 32768 ids (16.8M)
+// 80 against 66.  A dropout is never faster with two (8192 x 1600 bf16 with residual
 // 13.4 against 13.9 us, 16384 x 4097 fp32 90.9 against 91.8).
 constexpr u32 kLookupUnits = 1u << 23;
 
@@ -1067,7 +1094,7 @@ int grad_as(GradLaunch a, hipStream_t st) {
     const u32 range = (a.n + kSortThreads - 1) / kSortThreads * 64;  // positions per wave
     a.list = range < (1u << 22) ? std::min<u32>(range, kSortList) : 0;
     const size_t lds = ((size_t)(kSortWaves + 2) * a.keys + (size_t)kSortWaves * a.list) * sizeof(u32);
-    if ((u64)a.n * a.slabs <= kOnceIds && a.rows * row_bytes <= kOnceBytes) {
+    if ((u64)a.n * a.slabs <= kOnceIds && a.rows * row_bytes <= kOnceBytes && a.keys <= kOnceKeys) {
       const dim3 g(1u << a.lg_classes), b(kSortThreads);
       const size_t all = lds + a.n * sizeof(u32);
       if (a.drop.thr) hipLaunchKernelGGL((grad_once_kernel<DT, GT, true>), g, b, all, st, a);

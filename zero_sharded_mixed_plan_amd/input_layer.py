@@ -135,7 +135,7 @@ def dropout(x: torch.Tensor, drop: Optional[Dropout], *, residual: Optional[torc
     out may be x or residual.  The backward pass is dropout(dout, drop, out_dtype=x.dtype).
     """
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or (x if residual is None else residual).dtype, device=x.device)
+        out = x.new_empty(x.shape, dtype=out_dtype or (x if residual is None else residual).dtype)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out has another type than out_dtype")
     if out.shape != x.shape or (residual is not None and residual.shape != x.shape):
@@ -167,7 +167,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, id0
     idb = _flat_ids(ids, "ids")
     rows, dim, ld = _rows(table, "table")
     if out is None:
-        out = torch.empty((*ids.shape, dim), dtype=out_dtype or table.dtype, device=table.device)
+        out = table.new_empty((*ids.shape, dim), dtype=out_dtype or table.dtype)
     elif out.shape != (*ids.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [*ids.shape, dim] of out_dtype")
     ptr_pt = ld_pt = n_pt = ptr_pos = 0
