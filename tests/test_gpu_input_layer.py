@@ -278,6 +278,9 @@ GRAD = [  # n, rows, dim, dy, grad, ids, kind, scale, p, offset, pad, id0
     # three launches and one, on either side of the rule between them
     (1024, 900, 512, "bf16", "f32", torch.int64, "two", 1.0, 0.1, 0, 0, 0),
     (1025, 900, 512, "bf16", "f32", torch.int64, "two", 1.0, 0.1, 0, 0, 0),
+    # few ids into many rows, past the one-launch form
+    (60, 70000, 130, "bf16", "f32", torch.int32, "zipf", 1.0, 0.1, 3, 0, 0),
+    (1, 33000, 260, "f32", "f32", torch.int64, "one", 1.0, 0.0, 0, 1, 0),
     # runs of exactly a chunk, and one more
     (8 * 41, 41, 600, "f32", "f32", torch.int64, "uniform", 1.0, 0.0, 0, 0, 0),
     (40000, 1250, 24, "bf16", "f32", torch.int64, "in turn", 1.0, 0.0, 0, 0, 0),

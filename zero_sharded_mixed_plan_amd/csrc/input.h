@@ -91,14 +91,13 @@ constexpr int kFillBytes = 8192;
 constexpr int64_t kEarlyBytes = 24 << 20, kEarlyBytesPerId = 1536, kEarlyGroupBytes = 65536;
 // One launch instead of three for at most this many ids times slabs of 512 columns
 // and this many bytes of gradient, in rows not too many to go through.  Measured
-// against three: 64 ids, 256 x 64 fp32 5.9 us (9.0), 1024 ids, 1000 x 256 fp32 9.3
-// (14.1), 16 to 500 ids, 30000 x 32 to 1000 x 1024 fp32 5.7 to 10.7 (9.2 to 14.1).  Beyond,
-// its 256 workgroups zero too slowly (50257 x 1600 bf16 47 to 59 us against 30 to 37),
-// 400 rows each take 18 us (100000 x 8 fp32, against 10 to 13), and an id that
-// fills the batch waits for one CU (256 times one id, 1600 wide, 21 us against 11;
-// 1024 times 86 against 16).
+// against three: 64 ids, 256 x 64 fp32 5.8 us (9.0), 1000 ids, 8000 x 512 bf16 9.3
+// (13.7), 250 ids, 10000 x 1600 bf16 11.2 (12.7).  Beyond, its 256 workgroups zero too
+// slowly (50257 x 1600 bf16 47 us against 30), 400 rows each take 18 us
+// (100000 x 8 fp32, against 10), and an id that fills the batch waits for one CU
+// (1000 times one id, 512 wide, 23 us against 15; 2500 times 57 against 19).
 constexpr uint32_t kOnceIds = 1024;
-constexpr int64_t kOnceBytes = 4 << 20;
+constexpr int64_t kOnceBytes = 32 << 20;
 constexpr uint32_t kOnceKeys = 128;  // rows of one class
 constexpr uint32_t kOnceRun = 16;    // ids of a row that one wave sums there
 constexpr int kJoinThreads = 512;
