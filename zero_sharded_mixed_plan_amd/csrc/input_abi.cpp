@@ -53,32 +53,32 @@ int guarded(F&& f) noexcept {
   }
 }
 
-int matrix(const std::string& fn, const char* what, const void* p, int64_t rows, int64_t cols, int64_t ld,
+int matrix(const char* fn, const char* what, const void* p, int64_t rows, int64_t cols, int64_t ld,
            zero_dtype_t t) {
   const int eb = bytes_of(t);
-  if (eb == 0) return fail(ZERO_EINVAL, fn + ": unsupported dtype of " + what);
+  if (eb == 0) return fail(ZERO_EINVAL, std::string(fn) + ": unsupported dtype of " + what);
   if (rows == 0) return ZERO_OK;
-  if (!p) return fail(ZERO_EINVAL, fn + ": " + what + " is NULL");
-  if (ld < cols && rows > 1) return fail(ZERO_EINVAL, fn + ": the rows of " + what + " overlap (stride < columns)");
+  if (!p) return fail(ZERO_EINVAL, std::string(fn) + ": " + what + " is NULL");
+  if (ld < cols && rows > 1) return fail(ZERO_EINVAL, std::string(fn) + ": the rows of " + what + " overlap (stride < columns)");
   if (ld < 0 || ld > kMaxLd || rows > kMaxLd || (rows > 1 && ld > (int64_t(1) << 60) / rows))
-    return fail(ZERO_EINVAL, fn + ": the stride of " + what + " is out of range");
-  if (!aligned(p, eb)) return fail(ZERO_EALIGN, fn + ": " + what + " is not element aligned");
+    return fail(ZERO_EINVAL, std::string(fn) + ": the stride of " + what + " is out of range");
+  if (!aligned(p, eb)) return fail(ZERO_EALIGN, std::string(fn) + ": " + what + " is not element aligned");
   return ZERO_OK;
 }
 
 // the drop of `rows` rows, as the kernels take it
-int make_drop(const std::string& fn, const zero_drop_t* d, int64_t rows, zk::DropK* k, double* ks) {
+int make_drop(const char* fn, const zero_drop_t* d, int64_t rows, zk::DropK* k, double* ks) {
   *k = zk::DropK{};
   k->ks = 1.0f;
   *ks = 1.0;
   if (!d) return ZERO_OK;
-  if (!(d->p >= 0.0 && d->p <= 1.0)) return fail(ZERO_EINVAL, fn + ": p must lie in [0, 1]");
-  if (d->reserved != 0) return fail(ZERO_EINVAL, fn + ": drop.reserved must be 0");
+  if (!(d->p >= 0.0 && d->p <= 1.0)) return fail(ZERO_EINVAL, std::string(fn) + ": p must lie in [0, 1]");
+  if (d->reserved != 0) return fail(ZERO_EINVAL, std::string(fn) + ": drop.reserved must be 0");
   if (!d->step_dev && (d->step < 0 || d->step >= (int64_t(1) << 32)))
-    return fail(ZERO_EINVAL, fn + ": the step must lie in [0, 2^32)");
-  if (d->step_dev && !aligned(d->step_dev, 8)) return fail(ZERO_EALIGN, fn + ": step_dev must be 8-byte aligned");
+    return fail(ZERO_EINVAL, std::string(fn) + ": the step must lie in [0, 2^32)");
+  if (d->step_dev && !aligned(d->step_dev, 8)) return fail(ZERO_EALIGN, std::string(fn) + ": step_dev must be 8-byte aligned");
   if (d->row0 < 0 || d->row0 > (int64_t(1) << 32) - rows)
-    return fail(ZERO_EINVAL, fn + ": row0 + rows must lie in [0, 2^32]");
+    return fail(ZERO_EINVAL, std::string(fn) + ": row0 + rows must lie in [0, 2^32]");
   const double t = std::nearbyint(d->p * 65536.0);
   k->thr = (uint32_t)t;
   *ks = t < 65536.0 ? 65536.0 / (65536.0 - t) : 0.0;
@@ -116,9 +116,9 @@ bool grad_sizes_ok(int64_t n, int64_t rows, int64_t dim) {
 
 int dropout(const void* x, int64_t ld_x, zero_dtype_t xt, const void* res, int64_t ld_res, void* out,
             int64_t ld_out, zero_dtype_t ot, int64_t rows, int64_t cols, const zero_drop_t* drop, void* stream) {
-  const std::string fn = "zero_dropout";
-  if (rows < 0 || rows >= kMaxLd) return fail(ZERO_EINVAL, fn + ": rows out of range");
-  if (cols < 1 || cols >= kMax31) return fail(ZERO_EINVAL, fn + ": cols must lie in [1, 2^31)");
+  const char* const fn = "zero_dropout";
+  if (rows < 0 || rows >= kMaxLd) return fail(ZERO_EINVAL, std::string(fn) + ": rows out of range");
+  if (cols < 1 || cols >= kMax31) return fail(ZERO_EINVAL, std::string(fn) + ": cols must lie in [1, 2^31)");
   int rc;
   if ((rc = matrix(fn, "x", x, rows, cols, ld_x, xt))) return rc;
   if (res && (rc = matrix(fn, "the residual", res, rows, cols, ld_res, ot))) return rc;
@@ -130,11 +130,11 @@ int dropout(const void* x, int64_t ld_x, zero_dtype_t xt, const void* res, int64
   const Span so = span(out, rows, cols, ld_out, bytes_of(ot));
   const bool same_x = out == x && xt == ot && (ld_out == ld_x || rows == 1);
   if (!same_x && overlap(so, span(x, rows, cols, ld_x, bytes_of(xt))))
-    return fail(ZERO_EINVAL, fn + ": out overlaps x");
+    return fail(ZERO_EINVAL, std::string(fn) + ": out overlaps x");
   const bool same_res = out == res && (ld_out == ld_res || rows == 1);
   if (res && !same_res && overlap(so, span(res, rows, cols, ld_res, bytes_of(ot))))
-    return fail(ZERO_EINVAL, fn + ": out overlaps the residual");
-  if (drop_overlaps(drop, so)) return fail(ZERO_EINVAL, fn + ": out overlaps step_dev");
+    return fail(ZERO_EINVAL, std::string(fn) + ": out overlaps the residual");
+  if (drop_overlaps(drop, so)) return fail(ZERO_EINVAL, std::string(fn) + ": out overlaps step_dev");
 
   const int64_t groups = (cols + zk::kGroup - 1) / zk::kGroup;
   const int64_t per_launch = std::max<int64_t>(1, zk::kMaxUnits / groups);
@@ -160,38 +160,38 @@ int dropout(const void* x, int64_t ld_x, zero_dtype_t xt, const void* res, int64
 }
 
 int lookup(const zero_embed_args_t* args, void* stream) {
-  const std::string fn = "zero_embed_lookup";
-  if (!args) return fail(ZERO_EINVAL, fn + ": args is NULL");
+  const char* const fn = "zero_embed_lookup";
+  if (!args) return fail(ZERO_EINVAL, std::string(fn) + ": args is NULL");
   const zero_embed_args_t& A = *args;
-  if (A.n_ids < 0 || A.n_ids >= kMax31) return fail(ZERO_EINVAL, fn + ": n_ids must lie in [0, 2^31)");
-  if (A.dim < 1 || A.dim >= kMax31) return fail(ZERO_EINVAL, fn + ": dim must lie in [1, 2^31)");
-  if (A.rows < 0 || A.pos_rows < 0) return fail(ZERO_EINVAL, fn + ": a table has a negative number of rows");
-  if (A.id_bytes != 4 && A.id_bytes != 8) return fail(ZERO_EINVAL, fn + ": id_bytes must be 4 or 8");
-  if (!std::isfinite(A.scale)) return fail(ZERO_EINVAL, fn + ": scale is not finite");
+  if (A.n_ids < 0 || A.n_ids >= kMax31) return fail(ZERO_EINVAL, std::string(fn) + ": n_ids must lie in [0, 2^31)");
+  if (A.dim < 1 || A.dim >= kMax31) return fail(ZERO_EINVAL, std::string(fn) + ": dim must lie in [1, 2^31)");
+  if (A.rows < 0 || A.pos_rows < 0) return fail(ZERO_EINVAL, std::string(fn) + ": a table has a negative number of rows");
+  if (A.id_bytes != 4 && A.id_bytes != 8) return fail(ZERO_EINVAL, std::string(fn) + ": id_bytes must be 4 or 8");
+  if (!std::isfinite(A.scale)) return fail(ZERO_EINVAL, std::string(fn) + ": scale is not finite");
   int rc;
   if ((rc = matrix(fn, "the table", A.table, A.rows, A.dim, A.ld_table, A.table_dtype))) return rc;
   const bool with_pos = A.pos_table != nullptr;
   if (with_pos) {
     if ((rc = matrix(fn, "the position table", A.pos_table, A.pos_rows, A.dim, A.ld_pos, A.table_dtype))) return rc;
-    if (!A.pos && A.pos_period < 1) return fail(ZERO_EINVAL, fn + ": pos_period must be at least 1");
-    if (A.pos && !aligned(A.pos, A.id_bytes)) return fail(ZERO_EALIGN, fn + ": pos is not element aligned");
+    if (!A.pos && A.pos_period < 1) return fail(ZERO_EINVAL, std::string(fn) + ": pos_period must be at least 1");
+    if (A.pos && !aligned(A.pos, A.id_bytes)) return fail(ZERO_EALIGN, std::string(fn) + ": pos is not element aligned");
   } else if (A.pos) {
-    return fail(ZERO_EINVAL, fn + ": pos without a position table");
+    return fail(ZERO_EINVAL, std::string(fn) + ": pos without a position table");
   }
   if ((rc = matrix(fn, "out", A.out, A.n_ids, A.dim, A.ld_out, A.out_dtype))) return rc;
   zk::DropK k;
   double ks;
   if ((rc = make_drop(fn, A.drop, A.n_ids, &k, &ks))) return rc;
   if (A.n_ids == 0) return ZERO_OK;
-  if (!A.ids) return fail(ZERO_EINVAL, fn + ": ids is NULL");
-  if (!aligned(A.ids, A.id_bytes)) return fail(ZERO_EALIGN, fn + ": ids is not element aligned");
+  if (!A.ids) return fail(ZERO_EINVAL, std::string(fn) + ": ids is NULL");
+  if (!aligned(A.ids, A.id_bytes)) return fail(ZERO_EALIGN, std::string(fn) + ": ids is not element aligned");
   const int tb = bytes_of(A.table_dtype), ob = bytes_of(A.out_dtype);
   const Span so = span(A.out, A.n_ids, A.dim, A.ld_out, ob);
   if (overlap(so, span(A.table, A.rows, A.dim, A.ld_table, tb)) ||
       overlap(so, span(A.ids, A.n_ids * A.id_bytes)) ||
       (with_pos && overlap(so, span(A.pos_table, A.pos_rows, A.dim, A.ld_pos, tb))) ||
       (A.pos && overlap(so, span(A.pos, A.n_ids * A.id_bytes))) || drop_overlaps(A.drop, so))
-    return fail(ZERO_EINVAL, fn + ": out overlaps an input");
+    return fail(ZERO_EINVAL, std::string(fn) + ": out overlaps an input");
 
   const int64_t groups = (A.dim + zk::kGroup - 1) / zk::kGroup;
   const int64_t per_launch = std::max<int64_t>(1, zk::kMaxUnits / groups);
@@ -226,38 +226,38 @@ int lookup(const zero_embed_args_t* args, void* stream) {
 }
 
 int gradient(const zero_embed_grad_args_t* args, void* stream) {
-  const std::string fn = "zero_embed_grad";
-  if (!args) return fail(ZERO_EINVAL, fn + ": args is NULL");
+  const char* const fn = "zero_embed_grad";
+  if (!args) return fail(ZERO_EINVAL, std::string(fn) + ": args is NULL");
   const zero_embed_grad_args_t& A = *args;
-  if (A.n_ids < 0 || A.n_ids >= kMax31) return fail(ZERO_EINVAL, fn + ": n_ids must lie in [0, 2^31)");
-  if (A.rows < 0 || A.rows >= kMax31) return fail(ZERO_EINVAL, fn + ": rows must lie in [0, 2^31)");
-  if (A.dim < 1 || A.dim >= kMax31) return fail(ZERO_EINVAL, fn + ": dim must lie in [1, 2^31)");
-  if (!grad_sizes_ok(A.n_ids, A.rows, A.dim)) return fail(ZERO_EINVAL, fn + ": n_ids, rows and dim are out of range together");
-  if (A.id_bytes != 4 && A.id_bytes != 8) return fail(ZERO_EINVAL, fn + ": id_bytes must be 4 or 8");
+  if (A.n_ids < 0 || A.n_ids >= kMax31) return fail(ZERO_EINVAL, std::string(fn) + ": n_ids must lie in [0, 2^31)");
+  if (A.rows < 0 || A.rows >= kMax31) return fail(ZERO_EINVAL, std::string(fn) + ": rows must lie in [0, 2^31)");
+  if (A.dim < 1 || A.dim >= kMax31) return fail(ZERO_EINVAL, std::string(fn) + ": dim must lie in [1, 2^31)");
+  if (!grad_sizes_ok(A.n_ids, A.rows, A.dim)) return fail(ZERO_EINVAL, std::string(fn) + ": n_ids, rows and dim are out of range together");
+  if (A.id_bytes != 4 && A.id_bytes != 8) return fail(ZERO_EINVAL, std::string(fn) + ": id_bytes must be 4 or 8");
   if (!A.ids && A.n_ids > 0 && A.period < 1)
-    return fail(ZERO_EINVAL, fn + ": ids is NULL and the period is not at least 1");
-  if (!std::isfinite(A.scale)) return fail(ZERO_EINVAL, fn + ": scale is not finite");
+    return fail(ZERO_EINVAL, std::string(fn) + ": ids is NULL and the period is not at least 1");
+  if (!std::isfinite(A.scale)) return fail(ZERO_EINVAL, std::string(fn) + ": scale is not finite");
   int rc;
   if ((rc = matrix(fn, "dy", A.dy, A.n_ids, A.dim, A.ld_dy, A.dy_dtype))) return rc;
   if ((rc = matrix(fn, "grad", A.grad, A.rows, A.dim, A.ld_grad, A.grad_dtype))) return rc;
-  if (A.ids && !aligned(A.ids, A.id_bytes)) return fail(ZERO_EALIGN, fn + ": ids is not element aligned");
+  if (A.ids && !aligned(A.ids, A.id_bytes)) return fail(ZERO_EALIGN, std::string(fn) + ": ids is not element aligned");
   zk::DropK k;
   double ks;
   if ((rc = make_drop(fn, A.drop, A.n_ids, &k, &ks))) return rc;
   const double factor = (double)A.scale * ks;
-  if (!std::isfinite((float)factor)) return fail(ZERO_EINVAL, fn + ": scale / (1 - p) is not finite in fp32");
+  if (!std::isfinite((float)factor)) return fail(ZERO_EINVAL, std::string(fn) + ": scale / (1 - p) is not finite in fp32");
   if (A.rows == 0) return ZERO_OK;
   const int64_t need = ws_need(A.n_ids, A.rows, A.dim);
   if (!A.ws || A.ws_bytes < need)
-    return fail(ZERO_EINVAL, fn + ": the workspace needs " + std::to_string(need) + " bytes");
-  if (!aligned(A.ws, 16)) return fail(ZERO_EALIGN, fn + ": the workspace must be 16-byte aligned");
+    return fail(ZERO_EINVAL, std::string(fn) + ": the workspace needs " + std::to_string(need) + " bytes");
+  if (!aligned(A.ws, 16)) return fail(ZERO_EALIGN, std::string(fn) + ": the workspace must be 16-byte aligned");
   const Span sg = span(A.grad, A.rows, A.dim, A.ld_grad, bytes_of(A.grad_dtype)), sw = span(A.ws, need);
   const Span sd = span(A.dy, A.n_ids, A.dim, A.ld_dy, bytes_of(A.dy_dtype));
   const Span si = span(A.ids, A.n_ids * A.id_bytes);
-  if (overlap(sg, sw)) return fail(ZERO_EINVAL, fn + ": grad overlaps the workspace");
+  if (overlap(sg, sw)) return fail(ZERO_EINVAL, std::string(fn) + ": grad overlaps the workspace");
   for (const Span& o : {sg, sw})
     if (overlap(o, sd) || overlap(o, si) || drop_overlaps(A.drop, o))
-      return fail(ZERO_EINVAL, fn + ": grad or the workspace overlaps an input");
+      return fail(ZERO_EINVAL, std::string(fn) + ": grad or the workspace overlaps an input");
 
   zk::GradLaunch a{};
   a.dy = static_cast<const char*>(A.dy);

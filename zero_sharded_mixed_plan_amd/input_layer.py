@@ -25,6 +25,8 @@ _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 # checked against the ctypes declarations below) and the stream is asked for by number.
 _EMBED = struct.Struct("@PqqqiiPqqfPqqPqPqiP")
 _GRAD = struct.Struct("@PqiiPqqqqqfiPqiPPq")
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 assert _EMBED.size == ctypes.sizeof(_abi.zero_embed_args_t)
 assert _GRAD.size == ctypes.sizeof(_abi.zero_embed_grad_args_t)
 
@@ -59,24 +61,24 @@ class Dropout:
         return self.c.p
 
 
-def _place(first, *others):
-    """The index of the tensors' one device."""
-    dev = first.device
-    if dev.type != "cuda":
+def _device(first: torch.Tensor, *others) -> int:
+    """The index of the tensors' one GPU."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on the GPU")
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors are on different devices" if t.is_cuda else "tensors must be on the GPU")
-    return dev.index
+    return dev
 
 
 def _call(fn, dev, *args):
     """Run a library call on the current stream of device `dev`, with it current."""
-    if dev == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        rc = fn(*args, _current_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            rc = fn(*args, _current_stream(dev))
     if rc != _abi.ZERO_OK:
         _abi._check(rc)
 
@@ -134,21 +136,29 @@ def dropout(x: torch.Tensor, drop: Optional[Dropout], *, residual: Optional[torc
     x's shape and, in this order, the type of out, out_dtype, the residual, x.
     out may be x or residual.  The backward pass is dropout(dout, drop, out_dtype=x.dtype).
     """
-    if out is None:
-        out = x.new_empty(x.shape, dtype=out_dtype or (x if residual is None else residual).dtype)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out has another type than out_dtype")
-    if out.shape != x.shape or (residual is not None and residual.shape != x.shape):
-        raise ValueError("x, residual and out must have one shape")
-    if residual is not None and residual.dtype != out.dtype:
-        raise ValueError("residual and out must have one type")
-    dev = _place(x, residual, out)
     n, cols, ld_x = _rows(x, "x")
+    if out is None:
+        dt = out_dtype or (x if residual is None else residual).dtype
+        out = torch.empty_like(x) if dt is x.dtype and ld_x == cols else x.new_empty(x.shape, dtype=dt)
+        ld_out = cols
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out has another type than out_dtype")
+        if out.shape != x.shape:
+            raise ValueError("x, residual and out must have one shape")
+        ld_out = _rows(out, "out")[2]
+    ptr_r = ld_r = 0
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("x, residual and out must have one shape")
+        if residual.dtype != out.dtype:
+            raise ValueError("residual and out must have one type")
+        ptr_r, ld_r = residual.data_ptr(), _rows(residual, "residual")[2]
+    dev = _device(x, residual, out)
     if n == 0 or cols == 0:
         return out
-    ptr_r, ld_r = (0, 0) if residual is None else (residual.data_ptr(), _rows(residual, "residual")[2])
-    _call(_abi.lib().zero_dropout, dev, x.data_ptr(), ld_x, _code(x.dtype), ptr_r, ld_r, out.data_ptr(),
-          _rows(out, "out")[2], _code(out.dtype), n, cols, _drop(drop, dev))
+    _call(_abi.lib().zero_dropout, dev, x.data_ptr(), ld_x, _code(x.dtype), ptr_r, ld_r, out.data_ptr(), ld_out,
+          _code(out.dtype), n, cols, _drop(drop, dev))
     return out
 
 
@@ -168,8 +178,11 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, id0
     rows, dim, ld = _rows(table, "table")
     if out is None:
         out = table.new_empty((*ids.shape, dim), dtype=out_dtype or table.dtype)
+        ld_out = dim
     elif out.shape != (*ids.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [*ids.shape, dim] of out_dtype")
+    else:
+        ld_out = _rows(out, "out")[2]
     ptr_pt = ld_pt = n_pt = ptr_pos = 0
     if pos_table is not None:
         n_pt, pos_dim, ld_pt = _rows(pos_table, "pos_table")
@@ -185,13 +198,13 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, id0
             raise ValueError("pos_table needs pos or a pos_period of at least 1")
     elif pos is not None:
         raise ValueError("pos without a pos_table")
-    dev = _place(table, ids, out, pos_table, pos)
+    dev = _device(table, ids, out, pos_table, pos)
     n = ids.numel()
     if n == 0 or dim == 0:
         return out
     _call(_abi.lib().zero_embed_lookup, dev, _EMBED.pack(
         table.data_ptr(), ld, rows, id0, _code(table.dtype), idb, ids.data_ptr(), n, dim, scale,
-        ptr_pt, ld_pt, n_pt, ptr_pos, pos_period, out.data_ptr(), _rows(out, "out")[2], _code(out.dtype),
+        ptr_pt, ld_pt, n_pt, ptr_pos, pos_period, out.data_ptr(), ld_out, _code(out.dtype),
         _drop(drop, dev)))
     return out
 
@@ -229,7 +242,7 @@ def embedding_grad(dy: torch.Tensor, ids: Optional[torch.Tensor], grad: torch.Te
         ptr_ids = ids.data_ptr() if n else 0
     elif period < 1:
         raise ValueError("ids None needs a period of at least 1")
-    dev = _place(grad, dy, ids, workspace)
+    dev = _device(grad, dy, ids, workspace)
     if rows == 0 or dim == 0:
         return grad
     L = _abi.lib()
