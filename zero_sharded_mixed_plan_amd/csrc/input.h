@@ -82,6 +82,7 @@ constexpr int kSortKeys = 1024;      // rows of one class at most: a list's entr
 constexpr int kMinChunk = 8;
 constexpr int kMaxLgChunk = 5;
 constexpr int kGradWaves = 4096;
+constexpr int64_t kLineRow = 1024;   // bytes of a row from which on whole cache lines are zeroed
 // Zeroed by one workgroup, or one row: 8 KiB; 16 to 64 KiB took 37 to 38 us for 8192
 // ids into 50257 x 1600 bf16 (36.7) and 330 to 339 for 65536 into 128256 x 4096 (316).
 constexpr int kFillBytes = 8192;
@@ -142,7 +143,8 @@ struct GradLaunch {
   uint32_t sum_groups;    // workgroups that sum; the others zero fill_rows rows each
   uint32_t early_row, early_rows;  // rows from early_row on are zeroed beside the sort, early_rows a workgroup
   uint32_t fill_rows;
-  FastDiv fill_units;     // 16-byte units of one row
+  FastDiv fill_units;     // 16-byte units of one row,
+  uint32_t fill_align;    // counted from a multiple of this
   float* partial;         // [2 * ceil(places / chunk)][slabs][512], in lane order
 };
 
