@@ -552,8 +552,9 @@ int zero_checkpoint_load(const zero_plan_t* plan, int32_t rank, const char* path
  * keeps everything; D = 65536 (p = 1) drops everything.
  *
  * step_dev: the step number is read from this device int64 (8-byte aligned) at
- * run time instead of `step`, so that a captured graph draws a new mask on
- * every replay; &ctl->step of a zero_step_ctl_t counts the steps applied.
+ * run time instead of `step` (its low 32 bits count), so that a captured graph draws
+ * a new mask on every replay; &ctl->step of a zero_step_ctl_t counts the steps
+ * applied (after a skipped step the next one draws the same mask).
  */
 typedef struct zero_drop {
   double p;                /* 0 <= p <= 1                                        */
@@ -572,8 +573,9 @@ typedef struct zero_drop {
  *
  * x [rows, cols] of x_dtype, out and residual (or NULL) [rows, cols] of
  * out_dtype; rows ld_x, ld_out, ld_res elements apart, columns adjacent.  Element
- * alignment suffices.  out may be x itself (same address, stride and type) or
- * the residual itself; any other overlap is refused.  1 <= cols < 2^31.
+ * alignment suffices.  What lies between an input's rows may be read, and has no
+ * effect (so in the calls below).  out may be x itself (same address, stride and
+ * type) or the residual itself; any other overlap is refused.  1 <= cols < 2^31.
  * drop == NULL: nothing is dropped.  rows == 0: nothing to do.
  * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
  */
