@@ -247,7 +247,7 @@ def embedding_grad(dy: torch.Tensor, ids: Optional[torch.Tensor], grad: torch.Te
         return grad
     L = _abi.lib()
     if workspace is None:
-        workspace = torch.empty(L.zero_embed_grad_ws_bytes(n, rows, dim), dtype=torch.uint8, device=grad.device)
+        workspace = grad.new_empty(L.zero_embed_grad_ws_bytes(n, rows, dim), dtype=torch.uint8)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _call(L.zero_embed_grad, dev, _GRAD.pack(
