@@ -658,6 +658,7 @@ typedef struct zero_embed_grad_args {
  * and must not be shared by calls that overlap in time.  grad and ws must not overlap
  * an input or each other.
  * zero_embed_grad_ws_bytes: the bytes ws needs; 0 if an argument is out of range.
+ * They never fall as an argument grows: a workspace of the largest sizes serves all calls.
  * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
  */
 int64_t zero_embed_grad_ws_bytes(int64_t n_ids, int64_t rows, int64_t dim);

@@ -644,3 +644,16 @@ def test_tensors_of_a_few_elements_at_the_end_of_memory(n, dim, dt, gt):
     want, cnt, mag = OI.lookup_grad(x.f64(), None, 4, period=3, drop=d)
     close(grad.v, want, mag, (cnt + 4)[:, None])
     grad.check()
+
+
+def test_workspace_of_a_full_batch_serves_its_shorter_last_one():
+    """Across the steps of the chunk length, where a shorter batch uses more partial rows."""
+    rows, dim = 700, 1600
+    ws = L.embedding_grad_workspace(8192, rows, dim)
+    ws.fill_(0xFF)
+    for n in (8192, 8191, 5000, 4097):
+        say(f"workspace of 8192 ids, {n} ids")
+        dy = torch.randn(n, dim, device="cuda").bfloat16()
+        ids = torch.randint(0, rows, (n,), device="cuda") // 40 * 40      # long runs: every chunk a partial row
+        a = L.embedding_grad(dy, ids, torch.empty(rows, dim, device="cuda"), workspace=ws)
+        assert torch.equal(a, L.embedding_grad(dy, ids, torch.empty(rows, dim, device="cuda")))

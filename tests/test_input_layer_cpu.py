@@ -240,3 +240,30 @@ def test_torch_layer_refuses():
         L.Dropout(0.1, site=1 << 33)
     with pytest.raises(ValueError, match="int64 tensor"):
         L.Dropout(0.1, step=torch.zeros(1, dtype=torch.int64))
+
+
+def test_workspace_never_shrinks_as_the_call_grows():
+    """A workspace of the largest sizes serves every smaller call: on both sides of
+    each step of the chunk length, and over widths and rows."""
+    f = Z.zero_embed_grad_ws_bytes
+    steps = [n for k in range(3, 22) for n in (2 ** k - 1, 2 ** k, 2 ** k + 1, 5 * 2 ** (k - 2), 5000 + k)]
+    for dim in (1, 8, 511, 512, 513, 777, 1600, 2048, 4096, 8192, 70000):
+        need = [f(n, 50257, dim) for n in sorted(steps)]
+        assert min(need) > 0 and need == sorted(need), dim
+    for n in (1, 7, 500, 4096, 8191, 8192, 32768, 40000):
+        need = [f(n, 1000, dim) for dim in range(1, 9000, 41)]
+        assert min(need) > 0 and need == sorted(need), n
+        need = [f(n, rows, 512) for rows in (0, 1, 255, 256, 257, 100000, (1 << 31) - 9000, (1 << 31) - 1)]
+        assert min(need) > 0 and need == sorted(need), n
+    # a width at which the chunk length steps
+    assert f(4096, 1000, 3584) <= f(4096, 1000, 3585)
+
+
+def test_a_shorter_batch_is_not_refused_the_largest_ones_workspace():
+    """The last batch of a loop that allocated for 8192 ids; it gets as far as the
+    overlap check."""
+    big = Z.zero_embed_grad_ws_bytes(8192, 50257, 1600)
+    for n in (8191, 5000, 4097, 1):
+        with pytest.raises(Z.ZeroError, match="overlaps an input"):
+            Z.zero_embed_grad(_grad_args(n_ids=n, rows=50257, dim=1600, ld_dy=1600, ld_grad=1600, ids=5 * P,
+                                         ws_bytes=big))

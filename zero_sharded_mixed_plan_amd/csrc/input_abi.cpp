@@ -103,15 +103,25 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t slabs_of(int64_t dim) { return (dim + 511) / 512; }
 int64_t has_offset(int64_t n) { return kHead + round_up(n * 16, 256); }
 int64_t partial_offset(int64_t n, int64_t rows) { return has_offset(n) + round_up(rows, 256); }
+// Pairs of partial rows (512 columns of a chunk and of a tail): ceil(n / chunk) * slabs
+// are used.  The chunk halves as a batch shrinks, so that number rises again below
+// each such step; what is set aside must not, or a workspace of the largest batch would
+// be too small for others.  Chunks under the longest leave fewer than kGradWaves whole
+// ones and one begun in each slab, and no more than the shortest chunks do; either bound
+// and the longest chunks' own number grow with n and dim.
+int64_t partial_pairs(int64_t n, int64_t dim) {
+  const int64_t slabs = slabs_of(dim), longest = int64_t(1) << zk::kMaxLgChunk;
+  return std::max(std::min((n + zk::kMinChunk - 1) / zk::kMinChunk * slabs, zk::kGradWaves + slabs),
+                  (n + longest - 1) / longest * slabs);
+}
 int64_t ws_need(int64_t n, int64_t rows, int64_t dim) {
-  const int64_t lg = zk::grad_lg_chunk(n, dim);
-  return partial_offset(n, rows) + ((n + (1 << lg) - 1) >> lg) * 2 * slabs_of(dim) * 512 * 4;
+  return partial_offset(n, rows) + partial_pairs(n, dim) * 2 * 512 * 4;
 }
 
-// windows * slabs, the largest grid, stays below 2^31
+// The waves that sum, at most two a pair, and all workgroups are counted in 32 bits.
 bool grad_sizes_ok(int64_t n, int64_t rows, int64_t dim) {
   return n >= 0 && n < kMax31 && rows >= 0 && rows < kMax31 && dim >= 1 && dim < kMax31 &&
-         ((n >> (zk::grad_lg_chunk(n, dim) - 1)) + 1) * slabs_of(dim) + rows < kMax31;
+         partial_pairs(n, dim) < kMax31 - 4;
 }
 
 int dropout(const void* x, int64_t ld_x, zero_dtype_t xt, const void* res, int64_t ld_res, void* out,
