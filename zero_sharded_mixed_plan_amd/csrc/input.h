@@ -36,6 +36,9 @@ struct DropK {
 constexpr int kInThreads = 256;      // threads per workgroup of the streaming kernels here
 constexpr int kGroup = 8;            // columns per lane and row: one generator call, 16 bytes of a 16-bit type
 constexpr int64_t kMaxUnits = (int64_t(1) << 31) - 1;  // (row, 8-column group) units of one launch
+// Workgroups of one launch where their number has no such bound: HIP takes fewer than
+// 2^32 threads, and beside the milliseconds of so many another launch costs nothing.
+constexpr uint32_t kMaxGroups = 1u << 20;
 
 struct DropoutLaunch {
   const char* x;
@@ -141,6 +144,7 @@ struct GradLaunch {
   uint32_t slabs;         // ceil(dim / 512)
   uint32_t join_places;   // places per workgroup of the join
   uint32_t sum_groups;    // workgroups that sum; the others zero fill_rows rows each
+  uint32_t first_group;   // of this launch, among all workgroups that sum and zero, or that join
   uint32_t early_row, early_rows;  // rows from early_row on are zeroed beside the sort, early_rows a workgroup
   uint32_t fill_rows;
   FastDiv fill_units;     // 16-byte units of one row,

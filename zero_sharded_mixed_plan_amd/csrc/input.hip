@@ -360,19 +360,19 @@ __device__ __forceinline__ int64_t pos_at(const LookupLaunch& a, u32 i) {
 }
 
 __global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
-  const u64 i = (u64)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (u64)a.n * a.dim) return;
-  const u32 t = (u32)(i / a.dim), c = (u32)(i % a.dim);
-  const u64 row = (u64)id_at(a.ids, a.id64, t) - (u64)a.id0;
-  const int64_t col = (int64_t)c * one_bytes(tt);
-  float v = row < (u64)a.rows ? load_one(a.table + (int64_t)row * a.ld_table + col, tt) * a.scale : 0.0f;
-  if (a.pos_table) {
-    const int64_t pos = pos_at(a, t);
-    if ((u64)pos < (u64)a.pos_rows) v += load_one(a.pos_table + pos * a.ld_pos + col, tt);
+  for (u64 i = (u64)blockIdx.x * blockDim.x + threadIdx.x; i < (u64)a.n * a.dim; i += (u64)gridDim.x * blockDim.x) {
+    const u32 t = (u32)(i / a.dim), c = (u32)(i % a.dim);
+    const u64 row = (u64)id_at(a.ids, a.id64, t) - (u64)a.id0;
+    const int64_t col = (int64_t)c * one_bytes(tt);
+    float v = row < (u64)a.rows ? load_one(a.table + (int64_t)row * a.ld_table + col, tt) * a.scale : 0.0f;
+    if (a.pos_table) {
+      const int64_t pos = pos_at(a, t);
+      if ((u64)pos < (u64)a.pos_rows) v += load_one(a.pos_table + pos * a.ld_pos + col, tt);
+    }
+    v *= a.drop.ks;
+    if (!kept(a.drop, a.t0 + t, c)) v = 0.0f;
+    store_one(a.out + t * a.ld_out + (int64_t)c * one_bytes(ot), ot, v);
   }
-  v *= a.drop.ks;
-  if (!kept(a.drop, a.t0 + t, c)) v = 0.0f;
-  store_one(a.out + t * a.ld_out + (int64_t)c * one_bytes(ot), ot, v);
 }
 
 // As above, with U times 64 units a wave, 256 apart, all loads before the arithmetic.
@@ -700,26 +700,26 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) 
       });
 }
 
-// dy of fewer than 8 elements, and so fewer than 8 ids: a thread per element
+// dy of fewer than 8 elements, and so fewer than 8 ids: element by element
 __global__ void grad_short_kernel(const GradLaunch a, int dt, int gt) {
-  const u64 i = (u64)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (u64)a.rows * a.dim) return;
-  const u32 row = (u32)(i / a.dim), c = (u32)(i % a.dim);
-  float sum = 0.0f;
-  bool any = false;
-  for (u32 t = 0; t < a.n; ++t) {
-    const u64 id = a.ids ? (u64)id_at(a.ids, a.id64, t) : t % a.period;
-    if (row_of_id(a, id) != row) continue;
-    any = true;
-    if (kept(a.drop, t, c)) sum += load_one(a.dy + t * a.ld_dy + (int64_t)c * one_bytes(dt), dt);
+  for (u64 i = (u64)blockIdx.x * blockDim.x + threadIdx.x; i < (u64)a.rows * a.dim; i += (u64)gridDim.x * blockDim.x) {
+    const u32 row = (u32)(i / a.dim), c = (u32)(i % a.dim);
+    float sum = 0.0f;
+    bool any = false;
+    for (u32 t = 0; t < a.n; ++t) {
+      const u64 id = a.ids ? (u64)id_at(a.ids, a.id64, t) : t % a.period;
+      if (row_of_id(a, id) != row) continue;
+      any = true;
+      if (kept(a.drop, t, c)) sum += load_one(a.dy + t * a.ld_dy + (int64_t)c * one_bytes(dt), dt);
+    }
+    char* const p = a.grad + (int64_t)row * a.ld_grad + (int64_t)c * one_bytes(gt);
+    sum *= a.factor;
+    if (a.accumulate) {
+      if (!any) continue;
+      sum += load_one(p, gt);
+    }
+    store_one(p, gt, sum);
   }
-  char* const p = a.grad + (int64_t)row * a.ld_grad + (int64_t)c * one_bytes(gt);
-  sum *= a.factor;
-  if (a.accumulate) {
-    if (!any) return;
-    sum += load_one(p, gt);
-  }
-  store_one(p, gt, sum);
 }
 
 // place p of the order: (t, row, index within the run, length of the run)
@@ -810,12 +810,13 @@ template <bool DROP> constexpr int kSumBatch = DROP ? 4 : 8;
 template <class DT, class GT, bool SORTED, bool DROP>
 __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a) {
   constexpr int W = kWidth<DT, GT>, P = 8 / W, B = kSumBatch<DROP>;
-  if (blockIdx.x >= a.sum_groups) {
-    fill_rows<GT, SORTED>(a, (blockIdx.x - a.sum_groups) * a.fill_rows);
+  const u32 group = a.first_group + blockIdx.x;
+  if (group >= a.sum_groups) {
+    fill_rows<GT, SORTED>(a, (group - a.sum_groups) * a.fill_rows);
     return;
   }
   const u32 lane = threadIdx.x & 63;
-  const u32 w = __builtin_amdgcn_readfirstlane(blockIdx.x * (kInThreads / 64) + (threadIdx.x >> 6));
+  const u32 w = __builtin_amdgcn_readfirstlane(group * (kInThreads / 64) + (threadIdx.x >> 6));
   const u32 win = w / a.slabs, slab = w - win * a.slabs;
   const u32 p0 = win * a.window;
   if (win >= a.windows) return;
@@ -914,7 +915,7 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunc
   __shared__ uint4 runs[kJoinThreads / kMinChunk];  // (place, row, length, chunks)
   __shared__ u32 n_runs;
   __shared__ float part[NW][64][8];
-  const u32 block = blockIdx.x / a.slabs, slab = blockIdx.x - block * a.slabs;
+  const u32 group = a.first_group + blockIdx.x, block = group / a.slabs, slab = group - block * a.slabs;
   const u32 p = block * a.join_places + threadIdx.x, in_chunk = (1u << a.lg_chunk) - 1;
   const u32 total = SORTED ? *a.n_valid : a.total;
   const bool mine = threadIdx.x < a.join_places && p < a.places;
@@ -1105,6 +1106,15 @@ void lookup_as(const LookupLaunch& a, hipStream_t st) {
   });
 }
 
+// calls launch(grid) for `groups` workgroups in parts of at most kMaxGroups
+template <class F>
+void in_parts(GradLaunch& a, u32 groups, F&& launch) {
+  for (u64 g = 0; g < groups; g += kMaxGroups) {
+    a.first_group = (u32)g;
+    launch(dim3((u32)std::min<u64>(groups - g, kMaxGroups)));
+  }
+}
+
 template <class DT, class GT, bool SORTED>
 int grad_as(GradLaunch a, hipStream_t st) {
   const int64_t row_bytes = (int64_t)a.dim * GT::bytes;
@@ -1129,7 +1139,8 @@ int grad_as(GradLaunch a, hipStream_t st) {
       // as many as fit beside the sort, 64 KiB or one row a workgroup
       a.early_rows = (u32)std::max<int64_t>(1, kEarlyGroupBytes / row_bytes);
       const int64_t bytes = kEarlyBytes + kEarlyBytesPerId * (int64_t)a.n;
-      early_groups = (u32)(std::min<int64_t>(a.rows, bytes / row_bytes) / a.early_rows);
+      // (there are at most 2 kMaxGroups classes, so that the launch has fewer than 2^32 threads)
+      early_groups = (u32)std::min<int64_t>(std::min<int64_t>(a.rows, bytes / row_bytes) / a.early_rows, kMaxGroups);
       a.early_row = (u32)(a.rows - (int64_t)early_groups * a.early_rows);
     }
     hipLaunchKernelGGL(sort_kernel<GT>, dim3((1u << a.lg_classes) + early_groups), dim3(kSortThreads), lds, st, a);
@@ -1142,17 +1153,19 @@ int grad_as(GradLaunch a, hipStream_t st) {
   const int64_t fill_to = SORTED ? (int64_t)a.early_row : a.rows;
   const u32 fill_groups = fill ? (u32)((fill_to + a.fill_rows - 1) / a.fill_rows) : 0;
   if (a.sum_groups + fill_groups == 0) return ZERO_OK;
-  const dim3 g(a.sum_groups + fill_groups), b(kInThreads);
-  if (a.drop.thr) hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, true>), g, b, 0, st, a);
-  else hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, false>), g, b, 0, st, a);
+  in_parts(a, a.sum_groups + fill_groups, [&](dim3 g) {
+    if (a.drop.thr) hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, true>), g, dim3(kInThreads), 0, st, a);
+    else hipLaunchKernelGGL((grad_sum_kernel<DT, GT, SORTED, false>), g, dim3(kInThreads), 0, st, a);
+  });
   if (int rc = launched("embedding gradient (sums)")) return rc;
   if (a.places > 0 && a.longest > 1u << a.lg_chunk) {
     // few places leave each workgroup few runs, many of them keep the workgroups few
     a.join_places = kJoinThreads;
     while (a.join_places > 64 && (u64)a.places * a.slabs < (u64)a.join_places * kJoinGroups) a.join_places /= 2;
     const u32 blocks = (a.places + a.join_places - 1) / a.join_places;
-    hipLaunchKernelGGL((grad_join_kernel<GT, kWidth<DT, GT>, SORTED>), dim3(blocks * a.slabs), dim3(kJoinThreads), 0,
-                       st, a);
+    in_parts(a, blocks * a.slabs, [&](dim3 g) {
+      hipLaunchKernelGGL((grad_join_kernel<GT, kWidth<DT, GT>, SORTED>), g, dim3(kJoinThreads), 0, st, a);
+    });
   }
   return launched("embedding gradient (joins)");
 }
@@ -1199,7 +1212,7 @@ int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, voi
 int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void* stream) {
   const int64_t least = kGroup * (tt == ZERO_F32 ? 4 : 2);
   if ((a.rows > 0 && a.table_end - a.table < least) || (a.pos_table && a.pos_end - a.pos_table < least)) {
-    const u64 blocks = ((u64)a.n * a.dim + 255) / 256;
+    const u64 blocks = std::min<u64>(((u64)a.n * a.dim + 255) / 256, kMaxGroups);
     hipLaunchKernelGGL(lookup_short_kernel, dim3((u32)blocks), dim3(256), 0, (hipStream_t)stream, a, (int)tt, (int)ot);
     return launched("embedding lookup");
   }
@@ -1211,7 +1224,7 @@ int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void*
 
 int launch_embed_grad(const GradLaunch& a, zero_dtype_t dt, zero_dtype_t gt, void* stream) {
   if (a.n > 0 && a.dy_end - a.dy < kGroup * (dt == ZERO_F32 ? 4 : 2)) {
-    const u64 blocks = ((u64)a.rows * a.dim + 255) / 256;
+    const u64 blocks = std::min<u64>(((u64)a.rows * a.dim + 255) / 256, kMaxGroups);
     hipLaunchKernelGGL(grad_short_kernel, dim3((u32)blocks), dim3(256), 0, (hipStream_t)stream, a, (int)dt, (int)gt);
     return launched("embedding gradient");
   }
