@@ -657,3 +657,48 @@ def test_workspace_of_a_full_batch_serves_its_shorter_last_one():
         ids = torch.randint(0, rows, (n,), device="cuda") // 40 * 40      # long runs: every chunk a partial row
         a = L.embedding_grad(dy, ids, torch.empty(rows, dim, device="cuda"), workspace=ws)
         assert torch.equal(a, L.embedding_grad(dy, ids, torch.empty(rows, dim, device="cuda")))
+
+
+class _Embed(torch.autograd.Function):
+    """Embedding with dropout as a torch model's own function: the calls' place in autograd."""
+
+    @staticmethod
+    def forward(ctx, ids, table, drop):
+        ctx.save_for_backward(ids)
+        ctx.shape, ctx.drop = table.shape, drop
+        return L.embedding(ids, table, drop=drop)
+
+    @staticmethod
+    def backward(ctx, dy):
+        ids, = ctx.saved_tensors
+        return None, L.embedding_grad(dy.contiguous(), ids, dy.new_empty(ctx.shape), drop=ctx.drop), None
+
+
+class _Drop(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, drop):
+        ctx.drop = drop
+        return L.dropout(x, drop)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return L.dropout(dy.contiguous(), ctx.drop), None
+
+
+def test_inside_autograd_functions():
+    """Called directly on what requires grad they are refused; from a Function they
+    give autograd the gradients of the oracle."""
+    rng = np.random.default_rng(12)
+    table = torch.from_numpy(rng.normal(size=(13, 40)).astype(np.float32)).cuda().requires_grad_()
+    ids = torch.from_numpy(rng.integers(0, 13, size=30)).cuda()
+    c = torch.from_numpy(rng.normal(size=(30, 40)).astype(np.float32)).cuda()
+    with pytest.raises(ValueError, match="requires grad"):
+        L.embedding(ids, table)
+    with pytest.raises(ValueError, match="requires grad"):
+        L.dropout(table, None)
+    d0, d1 = drop_of(0.2), dict(drop_of(0.3), site=5)
+    (_Drop.apply(_Embed.apply(ids, table, L_drop(d0)), L_drop(d1)) * c).sum().backward()
+    cs = c.cpu().double().numpy()
+    inner = OI.dropout(cs, d1)
+    want, cnt, mag = OI.lookup_grad(inner, ids.cpu().numpy(), 13, drop=d0)
+    close(table.grad, want, mag, (cnt + 6)[:, None])       # and the outer dropout's factor, rounded twice

@@ -267,3 +267,22 @@ def test_a_shorter_batch_is_not_refused_the_largest_ones_workspace():
         with pytest.raises(Z.ZeroError, match="overlaps an input"):
             Z.zero_embed_grad(_grad_args(n_ids=n, rows=50257, dim=1600, ld_dy=1600, ld_grad=1600, ids=5 * P,
                                          ws_bytes=big))
+
+
+def test_torch_layer_refuses_to_lose_a_gradient():
+    """No history is recorded, so with grad mode on a tensor that requires grad is
+    refused; without, the calls get on to the next check (no GPU here)."""
+    w = torch.zeros(4, 8, requires_grad=True)
+    x, ids = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    calls = [lambda w: L.dropout(w, None), lambda w: L.dropout(x, None, residual=w),
+             lambda w: L.dropout(x, None, out=w), lambda w: L.dropout(w * 2, L.Dropout(0.5)),
+             lambda w: L.embedding(ids, w), lambda w: L.embedding(ids, x, pos_table=w, pos_period=4),
+             lambda w: L.embedding(ids, x, out=w), lambda w: L.embedding_grad(w, ids, x),
+             lambda w: L.embedding_grad(x, ids, w)]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires grad"):
+            call(w)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+            call(w)
+        with pytest.raises(ValueError, match="GPU"):
+            call(w.detach())

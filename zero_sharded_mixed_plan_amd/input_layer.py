@@ -6,6 +6,11 @@ The tables are tensors of the all-gather buffer that the sharded step writes
 (ZeroAdam.grad_view).  torch supplies device memory and the stream (the current
 stream of the tensors' device); every step of the computation runs in
 libzero_shard.so (zero_embed_lookup, zero_embed_grad, zero_dropout).
+
+The calls record no history for autograd: a loop calls the backward pass itself, or
+from a torch.autograd.Function.  With grad mode on, a tensor that requires grad is
+refused, since its gradient would be lost without a sign; detach it, or call under
+torch.no_grad() (inside a Function's forward and backward, grad mode is off).
 """
 from __future__ import annotations
 
@@ -62,7 +67,14 @@ class Dropout:
 
 
 def _device(first: torch.Tensor, *others) -> int:
-    """The index of the tensors' one GPU."""
+    """The index of the tensors' one GPU.  Also refuses what autograd would lose."""
+    lost = first.requires_grad
+    for t in others:
+        if t is not None and t.requires_grad:
+            lost = True
+    if lost and torch.is_grad_enabled():
+        raise ValueError("a tensor requires grad, and these calls record no history for autograd: "
+                         "detach it, or call under torch.no_grad()")
     dev = first.get_device()
     if dev < 0:
         raise ValueError("tensors must be on the GPU")
