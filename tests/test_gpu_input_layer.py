@@ -702,3 +702,20 @@ def test_inside_autograd_functions():
     inner = OI.dropout(cs, d1)
     want, cnt, mag = OI.lookup_grad(inner, ids.cpu().numpy(), 13, drop=d0)
     close(table.grad, want, mag, (cnt + 6)[:, None])       # and the outer dropout's factor, rounded twice
+
+
+@pytest.mark.parametrize("device_control", [False, True])
+def test_the_optimizers_dropout_follows_its_steps(device_control):
+    """One Dropout object kept over a loop draws each step's own mask, with the step
+    count on the host or on the device, and repeats it after a skipped step."""
+    opt = ZeroAdam([4096], 1, 0, lr=1e-3, grad_dtype=torch.bfloat16, device_control=device_control)
+    d = opt.dropout(0.5, seed=3, site=2)
+    x = torch.randn(16, 100, device="cuda")
+    grads = torch.ones(1, opt.plan.padded_numel, dtype=torch.bfloat16, device="cuda")
+    t = 0
+    for skipped in (False, False, True, False):
+        assert torch.equal(L.dropout(x, d), L.dropout(x, L.Dropout(0.5, seed=3, site=2, step=t))), t
+        grads.fill_(float("inf") if skipped else 1.0)
+        opt.step(grads, full=True)
+        t += not skipped
+    assert opt.t == t == 3

@@ -286,3 +286,18 @@ def test_torch_layer_refuses_to_lose_a_gradient():
             call(w)
         with pytest.raises(ValueError, match="GPU"):
             call(w.detach())
+
+
+def test_a_dropouts_step_can_be_a_function():
+    """Asked at every call; what it gives is checked like any step number."""
+    n = [4]
+    d = L.Dropout(0.5, step=lambda: n[0])
+    assert d.c.step == 4
+    n[0] = 7
+    assert L._drop(d, 0) == ctypes.addressof(d.c) and d.c.step == 7
+    n[0] = 1 << 32
+    L._drop(d, 0)
+    with pytest.raises(Z.ZeroError, match="step must lie in"):
+        _dropout(drop=d.c)
+    with pytest.raises(ValueError, match="out of range"):
+        L.Dropout(0.5, step=lambda: -1)

@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
-from typing import Optional, Union
+from typing import Callable, Optional, Union
 
 import torch
 
@@ -41,15 +41,20 @@ class Dropout:
     matrix are dropped is a function of seed, site, step, the row's place in the
     whole batch (row0 + row) and the column.
 
-    step: an integer, or a device int64 tensor of one element that the kernels
-    read when they run (a captured graph then draws a new mask at every replay;
-    ZeroAdam.dropout passes the step control's count).  The tensor must stay alive
+    step: an integer; a function that gives one, asked at every call; or a device
+    int64 tensor of one element that the kernels read when they run (a captured
+    graph then draws a new mask at every replay).  ZeroAdam.dropout passes the count
+    of the steps applied in one of the last two forms.  The tensor must stay alive
     until the work is done.
     """
-    __slots__ = ("c", "_step", "_ref")
+    __slots__ = ("c", "_step", "_count", "_ref")
 
-    def __init__(self, p: float, seed: int = 0, site: int = 0, step: Union[int, torch.Tensor] = 0, row0: int = 0):
-        self._step = None
+    def __init__(self, p: float, seed: int = 0, site: int = 0,
+                 step: Union[int, Callable[[], int], torch.Tensor] = 0, row0: int = 0):
+        self._step = self._count = None
+        if callable(step):
+            self._count = step
+            step = step()
         if isinstance(step, torch.Tensor):
             if step.dtype != torch.int64 or step.numel() != 1 or not step.is_cuda:
                 raise ValueError("step must be an integer or a device int64 tensor of one element")
@@ -68,19 +73,20 @@ class Dropout:
 
 def _device(first: torch.Tensor, *others) -> int:
     """The index of the tensors' one GPU.  Also refuses what autograd would lose."""
-    lost = first.requires_grad
+    dev, lost, other = first.get_device(), first.requires_grad, None
     for t in others:
-        if t is not None and t.requires_grad:
-            lost = True
+        if t is not None:
+            if t.requires_grad:
+                lost = True
+            if t.get_device() != dev:
+                other = t
     if lost and torch.is_grad_enabled():
         raise ValueError("a tensor requires grad, and these calls record no history for autograd: "
                          "detach it, or call under torch.no_grad()")
-    dev = first.get_device()
-    if dev < 0:
+    if dev < 0 or (other is not None and not other.is_cuda):
         raise ValueError("tensors must be on the GPU")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors are on different devices" if t.is_cuda else "tensors must be on the GPU")
+    if other is not None:
+        raise ValueError("tensors are on different devices")
     return dev
 
 
@@ -137,6 +143,8 @@ def _drop(drop: Optional[Dropout], dev: int) -> int:
         return 0
     if drop._step is not None and drop._step.device.index != dev:
         raise ValueError("the dropout's step is on another device")
+    if drop._count is not None:
+        drop.c.step = drop._count()
     return drop._ref
 
 

@@ -258,12 +258,13 @@ class ZeroAdam:
 
     def dropout(self, p: float, seed: int = 0, site: int = 0, row0: int = 0):
         """The input_layer.Dropout of the coming step: its step number is the
-        number of steps applied so far, read on the device with device control."""
+        number of steps applied so far, as of each call that uses it (with device
+        control, as of each run of its kernels), so one object serves a whole loop."""
         from .input_layer import Dropout
         if self.ctl:
             o = _abi.zero_step_ctl_t.step.offset
             return Dropout(p, seed, site, self.ctl.buf[o:o + 8].view(torch.int64), row0)
-        return Dropout(p, seed, site, self._t, row0)
+        return Dropout(p, seed, site, lambda: self._t, row0)
 
     # -- sharded checkpoint ----------------------------------------------------
     def _ptrs(self):
