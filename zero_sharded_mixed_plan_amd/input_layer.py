@@ -72,22 +72,21 @@ class Dropout:
 
 
 def _device(first: torch.Tensor, *others) -> int:
-    """The index of the tensors' one GPU.  Also refuses what autograd would lose."""
-    dev, lost, other = first.get_device(), first.requires_grad, None
+    """The index of the tensors' one GPU."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
     for t in others:
-        if t is not None:
-            if t.requires_grad:
-                lost = True
-            if t.get_device() != dev:
-                other = t
-    if lost and torch.is_grad_enabled():
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors are on different devices" if t.is_cuda else "tensors must be on the GPU")
+    return dev
+
+
+def _no_history() -> None:
+    """Called where a tensor requires grad."""
+    if torch.is_grad_enabled():
         raise ValueError("a tensor requires grad, and these calls record no history for autograd: "
                          "detach it, or call under torch.no_grad()")
-    if dev < 0 or (other is not None and not other.is_cuda):
-        raise ValueError("tensors must be on the GPU")
-    if other is not None:
-        raise ValueError("tensors are on different devices")
-    return dev
 
 
 def _call(fn, dev, *args):
@@ -157,6 +156,7 @@ def dropout(x: torch.Tensor, drop: Optional[Dropout], *, residual: Optional[torc
     out may be x or residual.  The backward pass is dropout(dout, drop, out_dtype=x.dtype).
     """
     n, cols, ld_x = _rows(x, "x")
+    given = out
     if out is None:
         dt = out_dtype or (x if residual is None else residual).dtype
         out = torch.empty_like(x) if dt is x.dtype and ld_x == cols else x.new_empty(x.shape, dtype=dt)
@@ -174,7 +174,10 @@ def dropout(x: torch.Tensor, drop: Optional[Dropout], *, residual: Optional[torc
         if residual.dtype != out.dtype:
             raise ValueError("residual and out must have one type")
         ptr_r, ld_r = residual.data_ptr(), _rows(residual, "residual")[2]
-    dev = _device(x, residual, out)
+    if (x.requires_grad or residual is not None and residual.requires_grad
+            or given is not None and given.requires_grad):
+        _no_history()
+    dev = _device(x, residual, given)
     if n == 0 or cols == 0:
         return out
     _call(_abi.lib().zero_dropout, dev, x.data_ptr(), ld_x, _code(x.dtype), ptr_r, ld_r, out.data_ptr(), ld_out,
@@ -196,6 +199,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, id0
         raise ValueError("table must be a matrix")
     idb = _flat_ids(ids, "ids")
     rows, dim, ld = _rows(table, "table")
+    given = out
     if out is None:
         out = table.new_empty((*ids.shape, dim), dtype=out_dtype or table.dtype)
         ld_out = dim
@@ -218,7 +222,10 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, id0
             raise ValueError("pos_table needs pos or a pos_period of at least 1")
     elif pos is not None:
         raise ValueError("pos without a pos_table")
-    dev = _device(table, ids, out, pos_table, pos)
+    if (table.requires_grad or pos_table is not None and pos_table.requires_grad
+            or given is not None and given.requires_grad):
+        _no_history()
+    dev = _device(table, ids, given, pos_table, pos)
     n = ids.numel()
     if n == 0 or dim == 0:
         return out
@@ -262,6 +269,8 @@ def embedding_grad(dy: torch.Tensor, ids: Optional[torch.Tensor], grad: torch.Te
         ptr_ids = ids.data_ptr() if n else 0
     elif period < 1:
         raise ValueError("ids None needs a period of at least 1")
+    if dy.requires_grad or grad.requires_grad:
+        _no_history()
     dev = _device(grad, dy, ids, workspace)
     if rows == 0 or dim == 0:
         return grad
