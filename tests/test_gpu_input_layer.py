@@ -719,3 +719,32 @@ def test_the_optimizers_dropout_follows_its_steps(device_control):
         opt.step(grads, full=True)
         t += not skipped
     assert opt.t == t == 3
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_rows_that_are_not_there_are_positive_zeros(dt):
+    """With a scale below zero too, in every form: no -0 from an id outside the
+    table, nor in a gradient's row without an id."""
+    def plus_zero(x):
+        return not x.any() and not torch.signbit(x.float()).any()
+
+    for rows, dim in ((3, 2), (6, 40), (5, 512)):
+        table = torch.ones(rows, dim, device="cuda").to(T[dt])
+        ids = torch.tensor([0, -1, rows, rows - 1], device="cuda")
+        y = L.embedding(ids, table, scale=-2.0)
+        assert plus_zero(y[1:3]) and (y[0] == -2).all() and (y[3] == -2).all()
+        # ... where a position adds -0, or has no row itself
+        pos = torch.full((2, dim), -0.0, device="cuda").to(T[dt])
+        assert plus_zero(L.embedding(ids, table, scale=-2.0, pos_table=pos, pos_period=4)[1:3])
+    # element by element; one launch; sorted; by period
+    for n, rows, dim in ((2, 9, 3), (10, 300, 40), (3000, 900, 40), (3000, 900, 1024)):
+        dy = torch.ones(n, dim, device="cuda").to(T[dt])
+        for ids, period in ((torch.arange(n, device="cuda") % 3 * 2, 0), (None, 4)):
+            for out in (torch.float32, T[dt]):
+                grad = torch.full((rows, dim), 3.0, device="cuda", dtype=out)
+                L.embedding_grad(dy, ids, grad, scale=-0.5, period=period)
+                there = [0, 2, 4] if ids is not None else [0, 1, 2, 3]
+                there = there[:n]
+                idle = torch.ones(rows, dtype=torch.bool, device="cuda")
+                idle[there] = False
+                assert plus_zero(grad[idle]) and (grad[there] < 0).all(), (n, rows, dim, period)

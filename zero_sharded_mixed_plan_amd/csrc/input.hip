@@ -367,7 +367,7 @@ __global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
     float v = row < (u64)a.rows ? load_one(a.table + (int64_t)row * a.ld_table + col, tt) * a.scale : 0.0f;
     if (a.pos_table) {
       const int64_t pos = pos_at(a, t);
-      if ((u64)pos < (u64)a.pos_rows) v += load_one(a.pos_table + pos * a.ld_pos + col, tt);
+      v += (u64)pos < (u64)a.pos_rows ? load_one(a.pos_table + pos * a.ld_pos + col, tt) : 0.0f;
     }
     v *= a.drop.ks;
     if (!kept(a.drop, a.t0 + t, c)) v = 0.0f;
@@ -428,7 +428,8 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
   for (int i = 0; i < U; ++i)
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-      x[i][q] = Raw<TT, W>{};
+#pragma unroll
+      for (u32& w : x[i][q].w) w = a.null_word;
       y[i][q] = Raw<TT, W>{};
       dx[i][q] = dy[i][q] = 0;
       const int64_t col = (int64_t)(grp[i][q] * kGroup + piece_col<W>(lane)) * TT::bytes;
@@ -713,7 +714,7 @@ __global__ void grad_short_kernel(const GradLaunch a, int dt, int gt) {
       if (kept(a.drop, t, c)) sum += load_one(a.dy + t * a.ld_dy + (int64_t)c * one_bytes(dt), dt);
     }
     char* const p = a.grad + (int64_t)row * a.ld_grad + (int64_t)c * one_bytes(gt);
-    sum *= a.factor;
+    if (any) sum *= a.factor;  // else +0, whatever the factor's sign
     if (a.accumulate) {
       if (!any) continue;
       sum += load_one(p, gt);
@@ -750,9 +751,10 @@ __device__ __forceinline__ u32 partial_slot(const GradLaunch& a, u32 p, bool tai
   return 2 * (p >> a.lg_chunk) + (tail ? 1 : 0);
 }
 
-// Writes a lane's sums to its columns of a row.
+// Writes a lane's sums, times the factor, to its columns of a row.
 template <class GT, int W>
-__device__ __forceinline__ void write_row8(const GradLaunch& a, u32 row, u32 slab, u32 lane, const float acc[8]) {
+__device__ __forceinline__ void write_row8(const GradLaunch& a, u32 row, u32 slab, u32 lane, const float acc[8],
+                                           float factor) {
 #pragma unroll
   for (int q = 0; q < 8 / W; ++q) {
     const u32 col = (slab * 64 + piece_group<W>(lane, q)) * kGroup + piece_col<W>(lane);
@@ -761,7 +763,7 @@ __device__ __forceinline__ void write_row8(const GradLaunch& a, u32 row, u32 sla
     const u32 n = a.dim - col;
     float v[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = acc[q * W + j] * a.factor;
+    for (int j = 0; j < W; ++j) v[j] = acc[q * W + j] * factor;
     if (a.accumulate) {
       constexpr int type = std::is_same<GT, F32>::value ? ZERO_F32 : std::is_same<GT, BF16>::value ? ZERO_BF16 : ZERO_F16;
       if (n >= W) {
@@ -876,7 +878,7 @@ __global__ __launch_bounds__(kInThreads) void grad_sum_kernel(const GradLaunch a
       if (ends >> i & 1) {
         const u32 len = __builtin_amdgcn_readlane(e.w, i);
         if (len <= chunk) {
-          write_row8<GT, W>(a, __builtin_amdgcn_readlane(e.y, i), slab, lane, acc);
+          write_row8<GT, W>(a, __builtin_amdgcn_readlane(e.y, i), slab, lane, acc, a.factor);
         } else {
           const bool tail = i + 1 - head < chunk;
           float* const q = a.partial + ((u64)partial_slot(a, p0 + head, tail) * a.slabs + slab) * 512 + lane * 8;
@@ -933,7 +935,7 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunc
     if (run.w > NW) continue;
     float acc[8] = {};
     add_partials(a, run.x, run.z, 0, run.w, slab, lane, acc);
-    write_row8<GT, W>(a, run.y, slab, lane, acc);
+    write_row8<GT, W>(a, run.y, slab, lane, acc, a.factor);
   }
   for (u32 r = 0; r < count; ++r) {
     const uint4 run = runs[r];
@@ -948,7 +950,7 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradLaunc
       for (u32 w = 1; w < NW; ++w)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += part[w][lane][j];
-      write_row8<GT, W>(a, run.y, slab, lane, acc);
+      write_row8<GT, W>(a, run.y, slab, lane, acc, a.factor);
     }
     __syncthreads();
   }
@@ -1037,7 +1039,7 @@ __global__ __launch_bounds__(kSortThreads) void grad_once_kernel(const GradLaunc
           for (u32 w = 1; w < splits; ++w)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] += part[w * across + wave][lane][j];
-          write_row8<GT, W>(a, row, slab, lane, acc);
+          write_row8<GT, W>(a, row, slab, lane, acc, a.factor);
         }
         __syncthreads();
       }
@@ -1053,7 +1055,7 @@ __global__ __launch_bounds__(kSortThreads) void grad_once_kernel(const GradLaunc
       const u32 at = __builtin_amdgcn_readfirstlane(start[k]) - first;
       sum(at, at + len, slab, acc);
     }
-    write_row8<GT, W>(a, (u32)row, slab, lane, acc);
+    write_row8<GT, W>(a, (u32)row, slab, lane, acc, len ? a.factor : 0.0f);  // no id: +0, whatever its sign
   }
 }
 
