@@ -748,3 +748,21 @@ def test_rows_that_are_not_there_are_positive_zeros(dt):
                 idle = torch.ones(rows, dtype=torch.bool, device="cuda")
                 idle[there] = False
                 assert plus_zero(grad[idle]) and (grad[there] < 0).all(), (n, rows, dim, period)
+
+
+def test_lookup_with_a_position_table_without_rows():
+    """Every position is outside it and reads zeros, given one by one or by a period,
+    through the torch layer and with an address through the C call."""
+    table = torch.randn(9, 136, device="cuda").bfloat16()
+    ids, at = torch.arange(-1, 10, device="cuda"), torch.arange(11, device="cuda")
+    want = L.embedding(ids, table)
+    assert torch.equal(L.embedding(ids, table, pos_table=table[:0], pos=at), want)
+    assert torch.equal(L.embedding(ids, table, pos_table=table[:0], pos_period=4), want)
+    out = torch.empty_like(want)
+    a = Z.zero_embed_args_t()
+    a.table, a.ld_table, a.rows, a.table_dtype = table.data_ptr(), 136, 9, Z.ZERO_BF16
+    a.ids, a.id_bytes, a.n_ids, a.dim, a.scale = ids.data_ptr(), 8, 11, 136, 1.0
+    a.pos_table, a.ld_pos, a.pos_rows, a.pos = table.data_ptr(), 136, 0, at.data_ptr()
+    a.out, a.ld_out, a.out_dtype = out.data_ptr(), 136, Z.ZERO_BF16
+    Z.zero_embed_lookup(a, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(out, want)

@@ -1213,7 +1213,7 @@ int launch_dropout(const DropoutLaunch& a, zero_dtype_t xt, zero_dtype_t ot, voi
 
 int launch_lookup(const LookupLaunch& a, zero_dtype_t tt, zero_dtype_t ot, void* stream) {
   const int64_t least = kGroup * (tt == ZERO_F32 ? 4 : 2);
-  if ((a.rows > 0 && a.table_end - a.table < least) || (a.pos_table && a.pos_end - a.pos_table < least)) {
+  if ((a.rows > 0 && a.table_end - a.table < least) || (a.pos_table && a.pos_rows > 0 && a.pos_end - a.pos_table < least)) {
     const u64 blocks = std::min<u64>(((u64)a.n * a.dim + 255) / 256, kMaxGroups);
     hipLaunchKernelGGL(lookup_short_kernel, dim3((u32)blocks), dim3(256), 0, (hipStream_t)stream, a, (int)tt, (int)ot);
     return launched("embedding lookup");

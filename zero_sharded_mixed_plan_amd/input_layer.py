@@ -217,7 +217,8 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, id0
             if pos.shape != ids.shape or pos.dtype != ids.dtype:
                 raise ValueError("pos must have the shape and type of ids")
             _flat_ids(pos, "pos")
-            ptr_pos = pos.data_ptr()
+            if n_pt:  # a table without rows has no address: its positions all read zeros
+                ptr_pos = pos.data_ptr()
         elif pos_period < 1:
             raise ValueError("pos_table needs pos or a pos_period of at least 1")
     elif pos is not None:
