@@ -766,3 +766,40 @@ def test_lookup_with_a_position_table_without_rows():
     a.out, a.ld_out, a.out_dtype = out.data_ptr(), 136, Z.ZERO_BF16
     Z.zero_embed_lookup(a, torch.cuda.current_stream().cuda_stream)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("ot", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cols", [1031, 1600, 4096])
+def test_every_element_is_rounded_alike(cols, ot):
+    """Each operation in fp32, its result rounded to the output's type: the same bits
+    wherever an element stands.  2^21 fp32 values and more, so that hundreds lie where
+    one rounding of the exact product to 16 bits and two roundings differ."""
+    rows = (1 << 21) // cols + 1
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda")
+    r = torch.randn(rows, cols, generator=g, device="cuda").to(T[ot])
+    d = drop_of(0.1, rows_at=3)
+    keep = torch.from_numpy(OI.keep(rows, cols, **d)).cuda()
+    ks = torch.tensor(OI.keep_scale(0.1), dtype=torch.float32, device="cuda")
+    zero = torch.zeros((), device="cuda")
+
+    def same(got, want32):
+        return torch.equal(got, want32.to(T[ot]))
+
+    kept = torch.where(keep, x * ks, zero)
+    assert same(L.dropout(x, L_drop(d), out_dtype=T[ot]), kept)
+    assert same(L.dropout(x, L_drop(d), residual=r), kept + r.float())
+    ids = torch.randperm(rows, generator=g, device="cuda")
+    assert same(L.embedding(ids, x, scale=1.3, out_dtype=T[ot]), x[ids] * 1.3)
+    y = L.embedding(ids, x, scale=1.3, pos_table=x, pos_period=rows, drop=L_drop(d), out_dtype=T[ot])
+    assert same(y, torch.where(keep, (x[ids] * 1.3 + x) * ks, zero))
+    # each id once: many ids; few, in one launch; by period
+    for n in (rows, 200):
+        grad = torch.empty(rows, cols, dtype=T[ot], device="cuda")
+        L.embedding_grad(x[:n], ids[:n], grad, scale=1.3)
+        assert same(grad[ids[:n]], x[:n] * 1.3)
+        L.embedding_grad(x[:n], None, grad[:n], scale=1.3, period=n)
+        assert same(grad[:n], x[:n] * 1.3)
+        grad.copy_(r)
+        L.embedding_grad(x[:n], ids[:n], grad, scale=1.3, accumulate=True)
+        assert same(grad[ids[:n]], x[:n] * 1.3 + r[ids[:n]].float())

@@ -138,11 +138,18 @@ __device__ __forceinline__ float load_one(const char* p, int type) {
   return type == ZERO_BF16 ? __uint_as_float(h << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
 }
 
+// An fp32 result in the bits of its type.  The compiler would merge the conversion to
+// fp16 with a product before it into one instruction that rounds once, but only in some
+// of the unrolled copies, so that a value's last bit hung on its place in the tensor; the
+// empty asm hides the product.
 template <class T>
 __device__ __forceinline__ u32 bits_of(float v) {
   if constexpr (T::bytes == 4) return __float_as_uint(v);
   else if constexpr (std::is_same<T, BF16>::value) return __builtin_bit_cast(uint16_t, (__bf16)v);
-  else return __builtin_bit_cast(uint16_t, (_Float16)v);
+  else {
+    asm("" : "+v"(v));
+    return __builtin_bit_cast(uint16_t, (_Float16)v);
+  }
 }
 
 __device__ __forceinline__ void store_one(char* p, int type, float v) {
