@@ -803,3 +803,63 @@ def test_every_element_is_rounded_alike(cols, ot):
         grad.copy_(r)
         L.embedding_grad(x[:n], ids[:n], grad, scale=1.3, accumulate=True)
         assert same(grad[ids[:n]], x[:n] * 1.3 + r[ids[:n]].float())
+
+
+# ---------------------------------------------------------------------------
+# rows of a multiple of 512 columns, where a wave has one row
+# ---------------------------------------------------------------------------
+
+PAIRS = [(a, b) for a in ("f32", "bf16", "f16") for b in ("f32", "bf16", "f16")]
+
+
+@pytest.mark.parametrize("cols", [512, 4096])
+@pytest.mark.parametrize("xt,ot", PAIRS)
+def test_dropout_of_whole_wave_rows(xt, ot, cols):
+    say(f"dropout 21x{cols} {xt}->{ot}")
+    g = np.random.default_rng(cols + len(xt))
+    for off, pad, res in ((0, 0, True), (1, 3, True), (5, 0, False)):
+        x = Mat(21, cols, xt, off, cols + pad, g.normal(size=(21, cols)))
+        r = Mat(21, cols, ot, off, cols + 2 * pad, g.normal(size=(21, cols))) if res else None
+        out = Mat(21, cols, ot, off, cols + pad)
+        d = drop_of(0.1, rows_at=2**32 - 30, step=2**32 - 1)
+        L.dropout(x.v, L_drop(d), residual=r.v if res else None, out=out.v)
+        xs, rs = x.f64(), r.f64() if res else None
+        close(out.v, OI.dropout(xs, d, rs), np.abs(xs) * OI.keep_scale(0.1) + (np.abs(rs) if res else 0), 5)
+        out.check()
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("dim", [512, 4096])
+@pytest.mark.parametrize("tt,ot", PAIRS)
+def test_lookup_of_whole_wave_rows(tt, ot, dim, p):
+    say(f"lookup 37 of 11x{dim} {tt}->{ot} p={p}")
+    g = np.random.default_rng(dim + len(ot))
+    table = Mat(11, dim, tt, 1, dim + 2, g.normal(size=(11, dim)))
+    pos = Mat(6, dim, tt, 3, dim, g.normal(size=(6, dim)))
+    ids, at = g.integers(-2, 13, size=37), g.integers(-1, 8, size=37)
+    ti, tp = torch.from_numpy(ids).cuda(), torch.from_numpy(at).cuda()
+    d = drop_of(p, rows_at=9) if p else None
+    for kw, okw in ((dict(), dict()),
+                    (dict(pos_table=pos.v, pos_period=7), dict(pos_table=pos.f64(), pos_period=7)),
+                    (dict(pos_table=pos.v, pos=tp), dict(pos_table=pos.f64(), pos=at))):
+        out = Mat(37, dim, ot, 1, dim + 1)
+        L.embedding(ti, table.v, scale=3.0, drop=L_drop(d), out=out.v, **kw)
+        want = OI.lookup(ids, table.f64(), scale=3.0, drop=d, **okw)
+        mag = dict(okw, **({"pos_table": np.abs(okw["pos_table"])} if okw else {}))
+        close(out.v, want, OI.lookup(ids, np.abs(table.f64()), scale=3.0, **mag) * OI.keep_scale(p), 5)
+        out.check()
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 513), (9, 512), (3, 2)])
+@pytest.mark.parametrize("xt,ot", PAIRS)
+def test_dropout_of_nothing_and_of_everything(rows, cols, xt, ot):
+    """p = 0 (and no drop) passes x on, p = 1 leaves the residual, bit for bit: one
+    fp32 addition, or none, and one rounding."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda").to(T[xt])
+    r = torch.randn(rows, cols, generator=g, device="cuda").to(T[ot])
+    for d in (None, L.Dropout(0.0), L.Dropout(2.0 ** -18)):
+        assert torch.equal(L.dropout(x, d, out_dtype=T[ot]), x.to(T[ot]))
+        assert torch.equal(L.dropout(x, d, residual=r), (x.float() + r.float()).to(T[ot]))
+    assert torch.equal(L.dropout(x, L.Dropout(1.0), residual=r), r)
+    assert not L.dropout(x, L.Dropout(1.0), out_dtype=T[ot]).any()

@@ -1,14 +1,17 @@
-"""The input layer's largest calls: more workgroups or threads than one launch holds.
+"""The input layer's largest calls: the lookup's form of two units a lane, and more
+workgroups, threads or units than one launch holds.
 
 HIP refuses a launch of 2^32 threads or more, and the launches here are divided
-or strided well below that; each test says how many it takes.  Values are small
-integers, whose fp32 sums are exact, so results are compared for equality.
+or strided well below that; each test says how many it takes.  Values of sums are
+small integers, whose fp32 sums are exact, so results are compared for equality.
 """
 import numpy as np
 import pytest
 import torch
 
 from gpu_harness import say
+from oracle import input_layer as OI
+from test_gpu_input_layer import PAIRS, T, close, drop_of
 from zero_sharded_mixed_plan_amd import input_layer as L
 
 pytestmark = pytest.mark.gpu
@@ -115,3 +118,85 @@ def test_element_kernels_beyond_one_launch():
     at = torch.tensor([n - 2, 5], device="cuda")
     L.embedding_grad(table, at, grad)
     assert torch.equal(grad[at], table) and _nonzero_rows(grad) == [5, n - 2]
+
+
+def _check_lookup_rows(out, lo, hi, ids, table, pos, period, drop, scale):
+    """Rows lo .. hi - 1 of a lookup against the oracle."""
+    at = np.arange(lo, hi) % period
+    i = ids[lo:hi].cpu().numpy()
+    ts, ps = table.cpu().double().numpy(), pos.cpu().double().numpy()
+    d = dict(drop, row0=drop["row0"] + lo) if drop else None
+    want = OI.lookup(i, ts, scale=scale, pos_table=ps, pos=at, drop=d)
+    mag = OI.lookup(i, np.abs(ts), scale=scale, pos_table=np.abs(ps), pos=at)
+    close(out[lo:hi], want, mag * OI.keep_scale(drop["p"] if drop else 0.0), 5, f"rows {lo} .. {hi}")
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("n,dim", [(16387, 4096), (41951, 1600), (86001, 777)])
+@pytest.mark.parametrize("tt,ot", PAIRS)
+def test_lookup_of_two_units_a_lane(tt, ot, n, dim, p):
+    """From 2^23 units of 8 columns on; one row a wave (4096), whole groups (1600) and
+    an odd width, each with a last wave in part.  Every element equals that of the same
+    rows looked up by halves, which take one unit a lane; some rows are checked
+    against the oracle."""
+    assert n * ((dim + 7) // 8) >= 1 << 23 > (n // 2 + 1) * ((dim + 7) // 8)
+    say(f"lookup {n} of 301x{dim} {tt}->{ot} p={p}")
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    flat = torch.randn(301 * dim + 3, generator=g, device="cuda").to(T[tt])
+    table = flat[3:].view(301, dim)
+    pos = torch.randn(97, dim, generator=g, device="cuda").to(T[tt])
+    ids = torch.randint(-2, 304, (n,), generator=g, device="cuda")
+    drop = drop_of(p, rows_at=70) if p else None
+    period, scale = 101, 1.5                            # positions 97 .. 100 have no row
+    whole = L.embedding(ids, table, scale=scale, pos_table=pos, pos_period=period,
+                        drop=L.Dropout(**drop) if p else None, out_dtype=T[ot])
+    half = n // 2
+    for lo, hi in ((0, half), (half, n)):
+        at = torch.arange(lo, hi, device="cuda") % period
+        part = L.embedding(ids[lo:hi], table, scale=scale, pos_table=pos, pos=at,
+                           drop=L.Dropout(**dict(drop, row0=70 + lo)) if p else None, out_dtype=T[ot])
+        assert torch.equal(whole[lo:hi], part)
+    for lo in (0, n // 3, n - 6):
+        _check_lookup_rows(whole, lo, lo + 6, ids, table, pos, period, drop, scale)
+    # without positions
+    whole = L.embedding(ids, table, scale=scale, drop=L.Dropout(**drop) if p else None, out_dtype=T[ot])
+    _check_lookup_rows(whole, n - 6, n, ids, table, torch.zeros_like(pos), period, drop, scale)
+
+
+def test_dropout_of_more_units_than_a_launch_holds():
+    """2^31 - 1 rows of one column in the first launch, the others in a second one."""
+    rows = (1 << 31) + 1000
+    x = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda")
+    for lo, hi in _parts(rows):
+        x[lo:hi, 0] = (torch.arange(lo, hi, device="cuda") % 251 - 125).to(torch.bfloat16)
+    say(f"dropout {rows} x 1")
+    d = drop_of(0.3, rows_at=5)
+    out = L.dropout(x, L.Dropout(**d))
+    for lo in (0, (1 << 31) - 51, rows - 100):
+        xs = x[lo:lo + 100].cpu().double().numpy()
+        close(out[lo:lo + 100], OI.dropout(xs, dict(d, row0=5 + lo)), np.abs(xs) * OI.keep_scale(0.3), 5, str(lo))
+    for lo, hi in _parts(rows):
+        assert torch.equal(L.dropout(x[lo:hi], L.Dropout(**dict(d, row0=5 + lo))), out[lo:hi]), lo
+    # in place
+    L.dropout(x, L.Dropout(**d), out=x)
+    for lo, hi in _parts(rows):
+        assert torch.equal(x[lo:hi], out[lo:hi]), lo
+
+
+def test_lookup_of_more_units_than_a_launch_holds():
+    """2^30 - 1 rows of two groups of columns in the first launch."""
+    n, dim, period, border = (1 << 30) + 1000, 9, 777, (1 << 30) - 1
+    g = torch.Generator(device="cuda").manual_seed(4)
+    table = torch.randn(50, dim, generator=g, device="cuda").bfloat16()
+    pos = torch.randn(period, dim, generator=g, device="cuda").bfloat16()
+    ids = torch.randint(-1, 51, (n,), generator=g, device="cuda", dtype=torch.int32)
+    say(f"lookup {n} of 50 x {dim}")
+    d = drop_of(0.25, rows_at=11)
+    out = L.embedding(ids, table, scale=2.0, pos_table=pos, pos_period=period, drop=L.Dropout(**d))
+    for lo in (0, border - 50, n - 100):
+        _check_lookup_rows(out, lo, lo + 100, ids, table, pos, period, d, 2.0)
+    for lo in (border - 100000, n - 100000):
+        at = (torch.arange(lo, lo + 100000, device="cuda") % period).int()
+        part = L.embedding(ids[lo:lo + 100000], table, scale=2.0, pos_table=pos, pos=at,
+                           drop=L.Dropout(**dict(d, row0=11 + lo)))
+        assert torch.equal(out[lo:lo + 100000], part[:n - lo]), lo
