@@ -610,7 +610,7 @@ typedef struct zero_embed_args {
 
 /*
  * out[t, :] = dropout(scale * table[ids[t] - id0, :] + pos_table[pos[t], :]),
- * in fp32 and rounded once to out_dtype.  An id outside [id0, id0 + rows) adds
+ * in fp32 and rounded once to out_dtype.  An id outside [id0, id0 + rows) reads
  * a row of zeros (padding ids; the rows of the other ranks where a table is split by
  * rows, whose outputs then add up), and so does a position outside [0, pos_rows).
  * The tables may sit anywhere in the gather buffer: element alignment suffices.

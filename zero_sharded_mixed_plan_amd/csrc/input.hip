@@ -371,7 +371,7 @@ __global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
     const u32 t = (u32)(i / a.dim), c = (u32)(i % a.dim);
     const u64 row = (u64)id_at(a.ids, a.id64, t) - (u64)a.id0;
     const int64_t col = (int64_t)c * one_bytes(tt);
-    float v = row < (u64)a.rows ? load_one(a.table + (int64_t)row * a.ld_table + col, tt) * a.scale : 0.0f;
+    float v = (row < (u64)a.rows ? load_one(a.table + (int64_t)row * a.ld_table + col, tt) : 0.0f) * a.scale;
     if (a.pos_table) {
       const int64_t pos = pos_at(a, t);
       v += (u64)pos < (u64)a.pos_rows ? load_one(a.pos_table + pos * a.ld_pos + col, tt) : 0.0f;
@@ -435,8 +435,7 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
   for (int i = 0; i < U; ++i)
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-#pragma unroll
-      for (u32& w : x[i][q].w) w = a.null_word;
+      x[i][q] = Raw<TT, W>{};
       y[i][q] = Raw<TT, W>{};
       dx[i][q] = dy[i][q] = 0;
       const int64_t col = (int64_t)(grp[i][q] * kGroup + piece_col<W>(lane)) * TT::bytes;

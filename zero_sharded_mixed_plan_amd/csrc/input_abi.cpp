@@ -229,7 +229,6 @@ int lookup(const zero_embed_args_t* args, void* stream) {
     // t < 2^31, so a longer period is none
     a.period = zk::fast_div((uint32_t)(with_pos && !A.pos ? std::min<int64_t>(A.pos_period, kMax31 - 1) : 1));
     a.scale = A.scale;
-    a.null_word = !std::signbit(A.scale) ? 0 : A.table_dtype == ZERO_F32 ? 0x80000000u : 0x80008000u;
     a.drop = k;
     if ((rc = zk::launch_lookup(a, A.table_dtype, A.out_dtype, stream))) return rc;
   }
