@@ -12,8 +12,10 @@
 // Results are stored non-temporally: they are read by another kernel, if at all,
 // and leave the L2 to what is read again (8192 x 1600 bf16, dropout with residual,
 // 13.6 us against 15.5; lookup of 32768 rows of 4096, 79 against 85).
-// Figures here are of one MI355X, calls back to back from a graph on four sets of inputs;
-// a plain streaming copy of 2 GiB moves 6.6 TB/s there.
+// Figures here are of one MI355X, calls back to back from a graph on four sets of inputs,
+// where not said otherwise; a plain streaming copy of 2 GiB moves 6.6 TB/s there.
+// "Vector units" is the share of the cycles in which a kernel runs that its vector
+// instructions take at four cycles each.
 // Arithmetic is IEEE fp32, one rounding per operation (the build disables
 // contraction); 16-bit results are rounded once, to nearest even.
 #include <hip/hip_runtime.h>
@@ -207,9 +209,9 @@ __device__ __forceinline__ Unit unit_at(u32 u0, u32 i, u32 first, const FastDiv&
 __device__ __forceinline__ u32 xor3(u32 a, u32 b, u32 c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
 
 // Philox4x32-10: ten rounds of two 32 x 32 -> 64 bit products (constants and
-// round as published, Salmon et al., SC'11).  On CDNA a product with both halves is
-// one quarter-rate instruction, so a call costs a wave about 10 * (2 * 16 + 4 * 4)
-// cycles for 8 elements per lane.
+// round as published, Salmon et al., SC'11).  A product with both halves is one
+// instruction.  A call costs a wave 205 cycles of its SIMD for 8 elements per lane
+// (measured with nothing else running; 124 with additions in the products' place).
 __device__ __forceinline__ void philox(u32 c0, u32 c1, u32 c2, u32 c3, u32 k0, u32 k1, u32 w[4]) {
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
@@ -297,8 +299,8 @@ __global__ void dropout_short_kernel(const DropoutLaunch a, int xt, int ot) {
 }
 
 // A unit is (row, 8-column group), numbered row by row; a wave takes 64 consecutive ones.
-// Bound by HBM: 8192 x 1600 bf16 with residual 13.0 us (6.0 TB/s), 16384 x 4097 fp32 92 us
-// (5.8 TB/s); the vector units are busy a third of the time.
+// Bound by HBM: 8192 x 1600 bf16 with residual 12.4 us (6.4 TB/s, vector units 69%),
+// 16384 x 4097 fp32 91 us (5.9 TB/s, 41%).
 template <class XT, class OT, bool DROP, bool ONE>
 __global__ __launch_bounds__(kInThreads) void dropout_kernel(const DropoutLaunch a) {
   constexpr int W = kWidth<XT, OT>, P = 8 / W;
@@ -385,8 +387,10 @@ __global__ void lookup_short_kernel(const LookupLaunch a, int tt, int ot) {
 // As above, with U times 64 units a wave, 256 apart, all loads before the arithmetic.
 // 32768 of 128256 rows of 4096 bf16: 66 us.  Its 371 MB would take 56 us at the copy's
 // rate; the eight L2 caches between them fetch the frequent rows again, 450 MB in all,
-// which it moves at 6.8 TB/s.  8192 x 1600 bf16 with positions and dropout: 11.8
-// us for 41 MB; there the random words' arithmetic and two dependent loads set the pace.
+// which it moves at 6.8 TB/s.  8192 x 1600 bf16 with positions and dropout: 10.7
+// us for 41 MB, bound by the vector units (95%): 212 instructions a wave, of which
+// the generator has about a quarter; the rest finds rows, columns and tails,
+// widens, scales and rounds.
 template <class TT, class OT, int U, bool DROP, bool ONE>
 __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a) {
   constexpr int W = kWidth<TT, OT>, P = 8 / W;
@@ -486,7 +490,7 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
 // 1. sort_kernel orders the positions t by row, equal rows by ascending t.  Each
 //    place of the order gets (t, row, its index within the row's run, the run's
 //    length); each row a flag that says whether it has any.
-// 2. grad_sum_kernel sums the runs in chunks of a.chunk places, so that a frequent id
+// 2. grad_sum_kernel sums the runs in chunks of 1 << a.lg_chunk places, so that a frequent id
 //    is shared by many waves.  A run of one chunk gives its row of the gradient,
 //    the chunks of longer ones give fp32 partial rows.  Further workgroups of the
 //    same launch zero the rows without an id.
@@ -495,10 +499,12 @@ __global__ __launch_bounds__(kInThreads) void lookup_kernel(const LookupLaunch a
 // The smallest calls take one launch instead (grad_once_kernel).
 //
 // The gradient is mostly a write: 8192 ids into 50257 x 1600 bf16 move 187 MB, of
-// which 161 MB are the result, and take 36.7 us, 28.4 at the copy's rate: 8.5 us order (39 MB
+// which 161 MB are the result, and take 36.4 us, 28.4 at the copy's rate: 9 us order (37.7 MB
 // of zero rows beside it), 24 us sums, 4 us joins.  65536 ids into 128256 x 4096 bf16
-// (1.59 GB): 316 us, 241 at the copy's rate: 45 us order (128 MB of zero rows), 260 us
-// sums at 5.7 TB/s, 9 us joins.
+// (1.59 GB): 316 us, 241 at the copy's rate: 41 us order (125.8 MB of zero rows), 265 us
+// sums at 5.6 TB/s, 9 us joins.  Added to what the gradient holds, where only the rows
+// with an id move, they take 29.8 us for 50 MB (8, 18.5 and 4) and 228 us for 883 MB
+// (25, 194 and 9.5).
 
 // The row of position t's id, or kNoRow.
 constexpr u32 kNoRow = ~0u;
@@ -537,7 +543,8 @@ __device__ __forceinline__ void zero_unit(const GradLaunch& a, char* p, u32 u) {
 // Wave w owns a contiguous range of positions; cnt[w][k] first counts its ids of
 // the class's row k, then holds the place of its next one.  The scan is a compare
 // and a ballot per 64 ids; the few own ones go to a list, and counting and placing
-// run over that.  8192 ids: 8 us, 65536: 25 us, bound by instruction issue.
+// run over that.  By itself 8 us for 8192 ids and 25 us for 65536 (vector units 33
+// and 55%).
 //   lds: cnt[kSortWaves][keys], start[keys] (the first place of row k), tot[keys] (its
 //        ids), lists [kSortWaves][a.list]
 // Calls counted(first place of the class, first place behind it) between the two
@@ -679,9 +686,10 @@ __device__ __forceinline__ void order_class(const GradLaunch& a, u32 cls, u32* c
   });
 }
 
-// One workgroup per class.  It reads little and takes 4 to 25 us, so further
-// workgroups of the launch zero the rows from a.early_row on meanwhile, whether
-// they have ids or not: those that do are written again by the launches that follow.
+// One workgroup per class.  That reads little and takes 8 to 25 us (8192 to 65536
+// ids), so further workgroups of the launch zero the rows from a.early_row on
+// meanwhile, whether they have ids or not: those that do are written again by the launches
+// that follow.  With them the launch takes 9 to 41 us.
 template <class GT>
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(const GradLaunch a) {
   if (blockIdx.x >> a.lg_classes) {
@@ -752,7 +760,7 @@ __device__ __forceinline__ uint4 order_at(const GradLaunch& a, u32 p) {
 }
 
 // Where the partial row of the chunk that begins at place p lies: at most one
-// full chunk and the shorter tail of one other run begin in an aligned a.chunk places.
+// full chunk and the shorter tail of one other run begin in 1 << a.lg_chunk aligned places.
 __device__ __forceinline__ u32 partial_slot(const GradLaunch& a, u32 p, bool tail) {
   return 2 * (p >> a.lg_chunk) + (tail ? 1 : 0);
 }
@@ -812,7 +820,7 @@ __device__ __forceinline__ void fill_rows(const GradLaunch& a, u32 r0) {
 template <bool DROP> constexpr int kSumBatch = DROP ? 4 : 8;
 
 // One wave per (window of a.window places, 512 columns): it sums the chunks that
-// begin in the window.  A chunk may end up to a.chunk - 1 places behind it.  The
+// begin in the window.  A chunk may end up to its length less one behind it.  The
 // workgroups that zero come after those that sum, and keep the memory busy while
 // the last of these wait for their rows.
 template <class DT, class GT, bool SORTED, bool DROP>

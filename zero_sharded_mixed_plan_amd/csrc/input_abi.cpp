@@ -321,7 +321,8 @@ int gradient(const zero_embed_grad_args_t* args, void* stream) {
   a.window = 1u << (a.lg_chunk - 1);
   a.windows = (uint32_t)((positions + a.window - 1) / a.window);
   a.slabs = (uint32_t)slabs_of(A.dim);
-  // without ids to sort (an empty batch) the period's form zeroes every row
+  // with an array of ids the sorted form, by period without one; either zeroes every
+  // row of an empty batch's gradient
   return zk::launch_embed_grad(a, A.dy_dtype, A.grad_dtype, stream);
 }
 
