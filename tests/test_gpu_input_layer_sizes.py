@@ -135,8 +135,8 @@ def _check_lookup_rows(out, lo, hi, ids, table, pos, period, drop, scale):
 @pytest.mark.parametrize("n,dim", [(16387, 4096), (41951, 1600), (86001, 777)])
 @pytest.mark.parametrize("tt,ot", PAIRS)
 def test_lookup_of_two_units_a_lane(tt, ot, n, dim, p):
-    """From 2^23 units of 8 columns on; one row a wave (4096), whole groups (1600) and
-    an odd width, each with a last wave in part.  Every element equals that of the same
+    """From 2^23 units of 8 columns on some types and forms take two; one row a wave (4096),
+    whole groups (1600) and an odd width, each with a last wave in part.  Every element equals that of the same
     rows looked up by halves, which take one unit a lane; some rows are checked
     against the oracle."""
     assert n * ((dim + 7) // 8) >= 1 << 23 > (n // 2 + 1) * ((dim + 7) // 8)

@@ -1085,11 +1085,27 @@ int launched(const char* what) {
   return fail(ZERO_EHIP, buf);
 }
 
-// Units per lane of a lookup: one, or two from this many units on.  Measured with
-// bf16 rows of 4096: 8192 ids (4.2M units) 17.5 us against 18.3, 32768 ids (16.8M)
-// 80 against 66.  A dropout is never faster with two (8192 x 1600 bf16 with residual
+// Units per lane of a lookup: one, or in some forms two from this many units on: bf16
+// rows of 4096, 8192 ids (4.2M units) 17.5 us with one against 18.3, 32768 ids (16.8M) 74.7
+// against 62.2.  A dropout is never faster with two (8192 x 1600 bf16 with residual
 // 13.4 against 13.9 us, 16384 x 4097 fp32 90.9 against 91.8).
 constexpr u32 kLookupUnits = 1u << 23;
+// The forms (us with one / with two; 42000 x 1600, and 32768 x 4096, where a wave has one
+// row; * takes one):
+//   16 to 16 bits    35.8 / 31.9, 74.7 / 62.2; with positions 39.8 / 39.9, 90.7 / 83.2;
+//                    with dropout 48.9 / 50.3 *, 98.7 / 93.5
+//   fp32 to 16 bits  59.7 / 53.9, 89.6 / 91.4 *; with positions 68.5 / 65.2, 114 / 120 *;
+//                    with dropout 74.7 / 74.7 *, 119 / 124 *
+//   16 bits to fp32  48.6 / 51.2 *, 105 / 106 *; with positions 60.8 / 57.4, 141 / 148 *;
+//                    with dropout 70.9 / 72.1 *, 145 / 153 *
+//   fp32 to fp32     76.6 / 75.0 *, 122 / 129 *; with positions 92.5 / 99.2 *, 162 / 178 *;
+//                    with dropout 96.1 / 96.3 *, 161 / 172 *
+template <class TT, class OT, bool DROP, bool ONE>
+constexpr bool kTwoUnits = kWidth<TT, OT> == 8 ? ONE || !DROP : !ONE && !DROP && TT::bytes != OT::bytes;
+template <class TT, class OT>
+bool two_units(const LookupLaunch& a) {
+  return a.units >= kLookupUnits && (TT::bytes >= OT::bytes || a.pos_table);
+}
 
 // calls f(drop, one row per wave) with constants
 template <class F>
@@ -1113,12 +1129,14 @@ void dropout_as(const DropoutLaunch& a, hipStream_t st) {
 template <class TT, class OT>
 void lookup_as(const LookupLaunch& a, hipStream_t st) {
   with_form(a.groups.d, a.drop.thr, [&](auto d, auto w) {
-    if (a.units < kLookupUnits)
-      hipLaunchKernelGGL((lookup_kernel<TT, OT, 1, decltype(d)::value, decltype(w)::value>), stream_grid(a.units, 1),
-                         dim3(kInThreads), 0, st, a);
-    else
-      hipLaunchKernelGGL((lookup_kernel<TT, OT, 2, decltype(d)::value, decltype(w)::value>), stream_grid(a.units, 2),
-                         dim3(kInThreads), 0, st, a);
+    constexpr bool DROP = decltype(d)::value, ONE = decltype(w)::value;
+    if constexpr (kTwoUnits<TT, OT, DROP, ONE>) {
+      if (two_units<TT, OT>(a)) {
+        hipLaunchKernelGGL((lookup_kernel<TT, OT, 2, DROP, ONE>), stream_grid(a.units, 2), dim3(kInThreads), 0, st, a);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((lookup_kernel<TT, OT, 1, DROP, ONE>), stream_grid(a.units, 1), dim3(kInThreads), 0, st, a);
   });
 }
 
