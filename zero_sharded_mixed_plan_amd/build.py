@@ -16,6 +16,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -86,19 +88,30 @@ def kernel_resources(remarks: str) -> dict:
     return out
 
 
-def build(verbose: bool = False) -> str:
-    """Compile the library; returns its path.  Always recompiles.  A kernel
-    that spills to scratch memory fails the build: every kernel here streams
-    from registers, and a spill has cost the step several percent."""
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
-           "-o", tmp, *SOURCES]
+def _run(cmd: list, verbose: bool) -> str:
+    """Run a compiler command; returns its messages."""
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
-    res = kernel_resources(r.stderr)
+    return r.stderr
+
+
+def build(verbose: bool = False) -> str:
+    """Compile the library; returns its path.  Always recompiles, the sources
+    side by side.  A kernel that spills to scratch memory fails the build:
+    every kernel here streams from registers, and a spill has cost the step
+    several percent."""
+    tmp = LIB + ".tmp"
+    include = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc")]
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            remarks = "".join(pool.map(
+                lambda so: _run([hipcc(), *FLAGS, *include, "-c", "-o", so[1], so[0]], verbose), zip(SOURCES, objects)))
+        _run([hipcc(), *FLAGS, "-o", tmp, *objects], verbose)
+    res = kernel_resources(remarks)
     with open(RESOURCES, "w") as f:
         for name in sorted(res):
             f.write(name + " " + " ".join(f"{k.replace(' ', '_')}={v}" for k, v in res[name].items()) + "\n")
