@@ -664,6 +664,189 @@ typedef struct zero_embed_grad_args {
 int64_t zero_embed_grad_ws_bytes(int64_t n_ids, int64_t rows, int64_t dim);
 int zero_embed_grad(const zero_embed_grad_args_t* args, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The pre-norm gated feed-forward sub-layer (device)                         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A [rows, cols] matrix held in 8 bits: blocks of 32 columns of a row (a row's last one
+ * may be shorter) share a scale 2^e, e the smallest whole number from -127 up
+ * with every finite magnitude of the block <= 448 * 2^e; an element is
+ * element / 2^e rounded to OCP e4m3 (to nearest, ties to even), so the largest ones
+ * keep 4 significant bits and none saturates.  Infinities and NaN are held as NaN and
+ * do not count towards the scale.  The values that codes and scales stand for
+ * are exact in bf16 and fp32 (down to their smallest numbers), and in fp16 where they
+ * lie in its range; magnitudes from 1.9375 * 2^127 up are held as 2^128, which reads as
+ * an infinity.
+ * codes [rows, cols]: one byte each, rows ld_codes bytes apart.  scales [rows,
+ * ceil(cols / 32)]: bytes e + 127 (OCP e8m0; never 255), rows ld_scales bytes apart.
+ */
+#define ZERO_HELD_BLOCK 32
+typedef struct zero_held {
+  void* codes;
+  int64_t ld_codes;
+  void* scales;
+  int64_t ld_scales;
+} zero_held_t;
+
+/*
+ * zero_pack8: x [rows, cols] of x_dtype, rows ld_x elements apart, held in 8 bits in
+ * *held.  zero_unpack8: the values that *held stands for, rounded once to out_dtype.
+ * Element alignment suffices; no overlaps.  1 <= cols < 2^31.  rows == 0: nothing to do.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
+ */
+int zero_pack8(const void* x, int64_t ld_x, zero_dtype_t x_dtype, int64_t rows, int64_t cols, const zero_held_t* held,
+               void* stream);
+int zero_unpack8(const zero_held_t* held, int64_t rows, int64_t cols, void* out, int64_t ld_out, zero_dtype_t out_dtype,
+                 void* stream);
+
+#define ZERO_NORM_MAX_COLS 8192
+
+/* Arguments of zero_rms_norm (host struct; pointers are device addresses). */
+typedef struct zero_rms_args {
+  const void* x;           /* [rows, cols], rows ld_x elements apart               */
+  int64_t ld_x;
+  zero_dtype_t x_dtype;
+  zero_dtype_t res_dtype;  /* of residual and total: x_dtype, or ZERO_F32          */
+  const void* residual;    /* or NULL: h = x                                       */
+  int64_t ld_res;
+  void* total;             /* h; given exactly where residual is                   */
+  int64_t ld_total;
+  const void* weight;      /* [cols], or NULL: ones                                */
+  zero_dtype_t weight_dtype;
+  zero_dtype_t out_dtype;
+  void* out;               /* y, or NULL where `held` is given                     */
+  int64_t ld_out;
+  const zero_held_t* held; /* y in 8 bits, or NULL                                 */
+  float* rstd;             /* [rows], or NULL                                      */
+  int64_t rows;
+  int64_t cols;            /* 1 <= cols <= ZERO_NORM_MAX_COLS                      */
+  double eps;              /* >= 0                                                 */
+} zero_rms_args_t;
+
+/*
+ * h = x + residual, rounded to res_dtype (without a residual h = x);
+ * rstd = 1 / sqrt(mean over the row of h^2 + eps); y = h * rstd * weight.
+ * The row's sum and y are computed in fp64; y is rounded to fp32, then to out_dtype, and from
+ * fp32 to the codes of `held`.  A row of zeros with eps == 0 gives NaN.
+ * total may be x (if the types are equal) or the residual, at the same address and
+ * stride; any other overlap of what is written is refused.  Element alignment suffices.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
+ */
+int zero_rms_norm(const zero_rms_args_t* args, void* stream);
+
+/* Arguments of zero_rms_norm_grad (host struct; pointers are device addresses). */
+typedef struct zero_rms_grad_args {
+  const void* dy;          /* [rows, cols], rows ld_dy elements apart              */
+  int64_t ld_dy;
+  zero_dtype_t dy_dtype;
+  zero_dtype_t h_dtype;    /* of h, dres and dh: dy_dtype, or ZERO_F32             */
+  const void* h;           /* what the norm was taken of, or NULL:                 */
+  int64_t ld_h;
+  const zero_held_t* held; /* the same held in 8 bits (exactly one is given)       */
+  const float* rstd;       /* [rows], of the forward pass                          */
+  const void* weight;      /* [cols], or NULL: ones                                */
+  zero_dtype_t weight_dtype;
+  zero_dtype_t dweight_dtype;
+  const void* dres;        /* the gradient that reaches h past the norm, or NULL   */
+  int64_t ld_dres;
+  void* dh;                /* [rows, cols]                                         */
+  int64_t ld_dh;
+  void* dweight;           /* [cols], or NULL                                      */
+  int32_t accumulate;      /* nonzero: add to what dweight holds                   */
+  int32_t reserved;        /* 0                                                    */
+  int64_t rows;
+  int64_t cols;            /* 1 <= cols <= ZERO_NORM_MAX_COLS                      */
+  void* ws;                /* zero_rms_grad_ws_bytes() bytes, 16-byte aligned      */
+  int64_t ws_bytes;        /* (may be NULL, 0 without dweight)                     */
+} zero_rms_grad_args_t;
+
+/*
+ * With n = h * rstd and s = weight * dy:
+ *   dh = rstd * (s - n * mean over the row of s * n) + dres, rounded to h_dtype;
+ *   dweight = sum over the rows of dy * n, written (zeros for rows == 0), or added to what it
+ *   holds and rounded once.
+ * Sums are fp32 within a workgroup's rows and fp64 beyond, in an order that the sizes
+ * alone give.  dh may be dy, h or dres of the same type at the same address and stride.
+ * dweight may sit anywhere in a flat gradient (element alignment).
+ * ws needs no initial content and must not be shared by calls that overlap in time.
+ * zero_rms_grad_ws_bytes: 0 if an argument is out of range; never falls as one grows.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
+ */
+int64_t zero_rms_grad_ws_bytes(int64_t rows, int64_t cols);
+int zero_rms_norm_grad(const zero_rms_grad_args_t* args, void* stream);
+
+typedef enum {
+  ZERO_SILU = 0,           /* g / (1 + exp(-g))                                    */
+  ZERO_GELU = 1            /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2    */
+} zero_act_t;
+
+/* Arguments of zero_gated and of the calls of its backward pass (host struct;
+ * pointers are device addresses).  tokens rows; x, dx [tokens, dim]; the weights and
+ * their gradients [hidden, dim]; everything else [tokens, hidden]; strides in elements.  A
+ * call reads the fields that it names below. */
+typedef struct zero_gated_args {
+  int64_t tokens, dim, hidden;  /* 0 <= tokens < 2^31, 1 <= dim, hidden < 2^31     */
+  zero_dtype_t dtype;      /* of everything but the weights' gradients             */
+  zero_act_t act;
+  const void* x;
+  int64_t ld_x;
+  const void* w_gate;
+  int64_t ld_w_gate;
+  const void* w_up;
+  int64_t ld_w_up;
+  void* a;
+  int64_t ld_a;
+  void* g;                 /* gate and up as tensors,                              */
+  int64_t ld_g;
+  void* u;
+  int64_t ld_u;
+  const zero_held_t* g8;   /* or held in 8 bits                                    */
+  const zero_held_t* u8;
+  const void* da;
+  int64_t ld_da;
+  void* dg;
+  int64_t ld_dg;
+  void* du;
+  int64_t ld_du;
+  void* dx;
+  int64_t ld_dx;
+  void* dw_gate;
+  int64_t ld_dw_gate;
+  void* dw_up;
+  int64_t ld_dw_up;
+  zero_dtype_t dw_dtype;
+  int32_t accumulate;      /* nonzero: add to what dw_gate and dw_up hold          */
+  void* ws;                /* zero_gated_ws_bytes() bytes, 16-byte aligned         */
+  int64_t ws_bytes;
+} zero_gated_args_t;
+
+/*
+ * zero_gated: g = x w_gate^T, u = x w_up^T, a = act(g) * u.  Reads x, w_gate, w_up;
+ *   writes a, and for the backward pass g and u (both or neither), as tensors or in
+ *   8 bits.  a, g, u and the codes are each rounded once from the fp32 sums.
+ * zero_gated_grad: dg = da * u * act'(g), du = da * act(g), and a once more (if not
+ *   NULL: the down projection's gradient needs it).  Reads da and g, u as tensors or in 8
+ *   bits; computes in fp32.  dg, du and a may be da, g or u at the same address and stride.
+ * zero_gated_input_grad: dx = dg w_gate + du w_up.
+ * zero_gated_weight_grad: dw_gate = dg^T x, dw_up = du^T x, written (zeros for
+ *   tokens == 0) or added to what they hold in fp32 and rounded once.  They may sit anywhere in
+ *   a flat gradient.
+ * Element alignment suffices; the matrix cores are fed fastest from addresses and strides that are
+ * multiples of 16 bytes.  Products of 16-bit types are exact and summed in fp32, in an
+ * order that the arguments' sizes, types and alignment alone give (no floating-point
+ * atomics).  Other overlaps of what a call writes are refused.  ws is used by the two
+ * product calls of the backward pass; it needs no initial content and must not be shared by
+ * calls that overlap in time.
+ * zero_gated_ws_bytes: 0 if an argument is out of range; never falls as one grows.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
+ */
+int64_t zero_gated_ws_bytes(int64_t tokens, int64_t dim, int64_t hidden);
+int zero_gated(const zero_gated_args_t* args, void* stream);
+int zero_gated_grad(const zero_gated_args_t* args, void* stream);
+int zero_gated_input_grad(const zero_gated_args_t* args, void* stream);
+int zero_gated_weight_grad(const zero_gated_args_t* args, void* stream);
+
 /*
  * A plain streaming copy of `bytes` bytes from src to dst (device pointers,
  * both 16-byte aligned, bytes a multiple of 16, no overlap), with the step's

@@ -14,7 +14,11 @@ from ._abi import (DTYPE_BYTES, DTYPE_CODES, EXPORTS, ZERO_BF16, ZERO_EALIGN, ZE
                    zero_plan_hash, zero_reduce_shard, zero_scaler_t, zero_shard_norm, zero_step_ctl_t,
                    zero_stream_copy, zero_version, ZERO_NOALLOC_SCRATCH_BYTES, zero_noalloc_max_shard,
                    zero_reduce_norm_noalloc, zero_drop_t, zero_dropout, zero_embed_args_t, zero_embed_grad,
-                   zero_embed_grad_args_t, zero_embed_grad_ws_bytes, zero_embed_lookup)
+                   zero_embed_grad_args_t, zero_embed_grad_ws_bytes, zero_embed_lookup,
+                   zero_held_t, zero_pack8, zero_unpack8, zero_rms_args_t, zero_rms_norm,
+                   zero_rms_grad_args_t, zero_rms_norm_grad, zero_rms_grad_ws_bytes,
+                   zero_gated_args_t, zero_gated, zero_gated_grad, zero_gated_input_grad,
+                   zero_gated_weight_grad, zero_gated_ws_bytes)
 
 __all__ = [
     "DTYPE_BYTES", "DTYPE_CODES", "EXPORTS", "ZERO_BF16", "ZERO_EALIGN", "ZERO_EHIP", "ZERO_EINVAL",
@@ -26,4 +30,8 @@ __all__ = [
     "zero_version", "ZERO_NOALLOC_SCRATCH_BYTES", "zero_noalloc_max_shard", "zero_reduce_norm_noalloc",
     "zero_drop_t", "zero_dropout", "zero_embed_args_t", "zero_embed_grad", "zero_embed_grad_args_t",
     "zero_embed_grad_ws_bytes", "zero_embed_lookup",
+    "zero_held_t", "zero_pack8", "zero_unpack8", "zero_rms_args_t", "zero_rms_norm",
+    "zero_rms_grad_args_t", "zero_rms_norm_grad", "zero_rms_grad_ws_bytes", "zero_gated_args_t",
+    "zero_gated", "zero_gated_grad", "zero_gated_input_grad", "zero_gated_weight_grad",
+    "zero_gated_ws_bytes",
 ]

@@ -32,6 +32,8 @@ EXPORTS = [
     "zero_adam_step", "zero_scaler_init", "zero_scaler_update", "zero_scaler_inv_scale", "zero_plan_hash",
     "zero_checkpoint_save", "zero_checkpoint_load", "zero_stream_copy", "zero_last_error", "zero_version",
     "zero_dropout", "zero_embed_lookup", "zero_embed_grad", "zero_embed_grad_ws_bytes",
+    "zero_pack8", "zero_unpack8", "zero_rms_norm", "zero_rms_norm_grad", "zero_rms_grad_ws_bytes",
+    "zero_gated", "zero_gated_grad", "zero_gated_input_grad", "zero_gated_weight_grad", "zero_gated_ws_bytes",
 ]
 
 
@@ -160,6 +162,105 @@ class zero_embed_grad_args_t(ctypes.Structure):
     ]
 
 
+class zero_held_t(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("ld_codes", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+        ("ld_scales", ctypes.c_int64),
+    ]
+
+
+class zero_rms_args_t(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64),
+        ("x_dtype", ctypes.c_int),
+        ("res_dtype", ctypes.c_int),
+        ("residual", ctypes.c_void_p),
+        ("ld_res", ctypes.c_int64),
+        ("total", ctypes.c_void_p),
+        ("ld_total", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("weight_dtype", ctypes.c_int),
+        ("out_dtype", ctypes.c_int),
+        ("out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("held", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("eps", ctypes.c_double),
+    ]
+
+
+class zero_rms_grad_args_t(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("ld_dy", ctypes.c_int64),
+        ("dy_dtype", ctypes.c_int),
+        ("h_dtype", ctypes.c_int),
+        ("h", ctypes.c_void_p),
+        ("ld_h", ctypes.c_int64),
+        ("held", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("weight_dtype", ctypes.c_int),
+        ("dweight_dtype", ctypes.c_int),
+        ("dres", ctypes.c_void_p),
+        ("ld_dres", ctypes.c_int64),
+        ("dh", ctypes.c_void_p),
+        ("ld_dh", ctypes.c_int64),
+        ("dweight", ctypes.c_void_p),
+        ("accumulate", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ws", ctypes.c_void_p),
+        ("ws_bytes", ctypes.c_int64),
+    ]
+
+
+class zero_gated_args_t(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("dtype", ctypes.c_int),
+        ("act", ctypes.c_int),
+        ("x", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64),
+        ("w_gate", ctypes.c_void_p),
+        ("ld_w_gate", ctypes.c_int64),
+        ("w_up", ctypes.c_void_p),
+        ("ld_w_up", ctypes.c_int64),
+        ("a", ctypes.c_void_p),
+        ("ld_a", ctypes.c_int64),
+        ("g", ctypes.c_void_p),
+        ("ld_g", ctypes.c_int64),
+        ("u", ctypes.c_void_p),
+        ("ld_u", ctypes.c_int64),
+        ("g8", ctypes.c_void_p),
+        ("u8", ctypes.c_void_p),
+        ("da", ctypes.c_void_p),
+        ("ld_da", ctypes.c_int64),
+        ("dg", ctypes.c_void_p),
+        ("ld_dg", ctypes.c_int64),
+        ("du", ctypes.c_void_p),
+        ("ld_du", ctypes.c_int64),
+        ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64),
+        ("dw_gate", ctypes.c_void_p),
+        ("ld_dw_gate", ctypes.c_int64),
+        ("dw_up", ctypes.c_void_p),
+        ("ld_dw_up", ctypes.c_int64),
+        ("dw_dtype", ctypes.c_int),
+        ("accumulate", ctypes.c_int32),
+        ("ws", ctypes.c_void_p),
+        ("ws_bytes", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -220,6 +321,16 @@ def load(path: str, required: bool = True) -> ctypes.CDLL:
         "zero_embed_lookup": (ctypes.c_int, [vp, vp]),
         "zero_embed_grad": (ctypes.c_int, [vp, vp]),
         "zero_embed_grad_ws_bytes": (i64, [i64, i64, i64]),
+        "zero_pack8": (ctypes.c_int, [vp, i64, ctypes.c_int, i64, i64, vp, vp]),
+        "zero_unpack8": (ctypes.c_int, [vp, i64, i64, vp, i64, ctypes.c_int, vp]),
+        "zero_rms_norm": (ctypes.c_int, [vp, vp]),
+        "zero_rms_norm_grad": (ctypes.c_int, [vp, vp]),
+        "zero_rms_grad_ws_bytes": (i64, [i64, i64]),
+        "zero_gated": (ctypes.c_int, [vp, vp]),
+        "zero_gated_grad": (ctypes.c_int, [vp, vp]),
+        "zero_gated_input_grad": (ctypes.c_int, [vp, vp]),
+        "zero_gated_weight_grad": (ctypes.c_int, [vp, vp]),
+        "zero_gated_ws_bytes": (i64, [i64, i64, i64]),
         "zero_last_error": (ctypes.c_char_p, []),
         "zero_version": (ctypes.c_char_p, []),
     }
@@ -493,6 +604,53 @@ def zero_embed_grad_ws_bytes(n_ids: int, rows: int, dim: int) -> int:
 
 def zero_embed_grad(args: zero_embed_grad_args_t, stream: int = 0) -> None:
     _check(lib().zero_embed_grad(ctypes.addressof(args), stream or None))
+
+
+# ---------------------------------------------------------------------------
+# the pre-norm gated feed-forward sub-layer
+# ---------------------------------------------------------------------------
+
+def zero_pack8(x: int, ld_x: int, x_dtype: int, rows: int, cols: int, held: zero_held_t, stream: int = 0) -> None:
+    _check(lib().zero_pack8(x or None, ld_x, x_dtype, rows, cols, ctypes.addressof(held), stream or None))
+
+
+def zero_unpack8(held: zero_held_t, rows: int, cols: int, out: int, ld_out: int, out_dtype: int,
+                 stream: int = 0) -> None:
+    _check(lib().zero_unpack8(ctypes.addressof(held), rows, cols, out or None, ld_out, out_dtype, stream or None))
+
+
+def zero_rms_norm(args: zero_rms_args_t, stream: int = 0) -> None:
+    _check(lib().zero_rms_norm(ctypes.addressof(args), stream or None))
+
+
+def zero_rms_grad_ws_bytes(rows: int, cols: int) -> int:
+    """Workspace bytes of zero_rms_norm_grad; 0 for sizes out of range."""
+    return int(lib().zero_rms_grad_ws_bytes(rows, cols))
+
+
+def zero_rms_norm_grad(args: zero_rms_grad_args_t, stream: int = 0) -> None:
+    _check(lib().zero_rms_norm_grad(ctypes.addressof(args), stream or None))
+
+
+def zero_gated_ws_bytes(tokens: int, dim: int, hidden: int) -> int:
+    """Workspace bytes of the gated block's product calls; 0 for sizes out of range."""
+    return int(lib().zero_gated_ws_bytes(tokens, dim, hidden))
+
+
+def zero_gated(args: zero_gated_args_t, stream: int = 0) -> None:
+    _check(lib().zero_gated(ctypes.addressof(args), stream or None))
+
+
+def zero_gated_grad(args: zero_gated_args_t, stream: int = 0) -> None:
+    _check(lib().zero_gated_grad(ctypes.addressof(args), stream or None))
+
+
+def zero_gated_input_grad(args: zero_gated_args_t, stream: int = 0) -> None:
+    _check(lib().zero_gated_input_grad(ctypes.addressof(args), stream or None))
+
+
+def zero_gated_weight_grad(args: zero_gated_args_t, stream: int = 0) -> None:
+    _check(lib().zero_gated_weight_grad(ctypes.addressof(args), stream or None))
 
 
 def adam_args(**kw) -> zero_adam_args_t:
