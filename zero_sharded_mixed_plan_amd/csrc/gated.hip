@@ -211,6 +211,276 @@ __global__ __launch_bounds__(256) void product_kernel(const ProductLaunch a, int
   }
 }
 
+// ---------------------------------------------------------------------------
+// 16-bit types at multiples of 16 bytes
+// ---------------------------------------------------------------------------
+
+// Tiles of TILE x TILE results (of gate and up in the forward pass TILE x TILE / 2 each),
+// 64 of k at a time, which go from global memory straight into LDS (16 bytes a lane,
+// no registers between) while the matrix cores work on the 64 before, from the other of
+// two buffers.  A wave has XB x 2 blocks of 32 x 32 results.
+//
+// LDS holds an operand as its rows lie in memory.  Rows of k ([row][64 k], 128 bytes): unit
+// (16 bytes) j of row i sits at j ^ (i % 8), so that the 16-byte reads of 8 lanes in
+// neighbouring rows meet every bank once.  Rows of the other index ([k][TILE]): unit j of
+// row k at j ^ 4 (k % 4), and the transposing read, in which 16 lanes fetch 4 rows of 16
+// columns, meets every bank once too.  The DMA writes LDS in lane order, so a lane fetches
+// the unit that belongs at its place.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+constexpr int kStep = 64;
+constexpr int kRounds = 4;  // 16 bytes a thread and round fill an operand's tile
+
+template <int TILE>
+constexpr int kTileThreads = TILE == 256 ? 512 : 256;
+
+// This thread's places in an operand's tile: byte offsets from the tile's first element.
+// i0, ni: the tile's first row (column) and the matrix's number of them, beyond which the last
+// ones stand in (what they give is not stored).
+template <int TILE, bool BY_K>
+__device__ __forceinline__ void places(u32 (&off)[kRounds], int round0, int rounds, int64_t ld, int64_t i0, int64_t ni) {
+  constexpr u32 kN = kTileThreads<TILE>;
+  const u32 t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q) {
+    if (q < round0 || q >= round0 + rounds) continue;
+    if constexpr (BY_K) {
+      const u32 row = (q - round0) * (kN / 8) + t / 8;
+      const u32 from = (u32)min((int64_t)row, ni - 1 - i0);
+      off[q] = from * (u32)ld + ((t % 8) ^ (t / 8 % 8)) * 16;
+    } else {
+      constexpr u32 kUnits = TILE / 8;
+      const u32 k = q * (kN / kUnits) + t / kUnits;
+      const u32 col = ((t % kUnits) ^ (4 * (k % 4))) * 8;
+      off[q] = k * (u32)ld + (u32)min((int64_t)col, ni - 8 - i0) * 2;
+    }
+  }
+}
+// Whether place q of the tile lies within the last `left` of k.
+template <int TILE, bool BY_K>
+__device__ __forceinline__ bool inside(int q, u32 left) {
+  constexpr u32 kN = kTileThreads<TILE>, kUnits = TILE / 8;
+  const u32 t = threadIdx.x;
+  return BY_K ? ((t % 8) ^ (t / 8 % 8)) * 8 < left : q * (kN / kUnits) + t / kUnits < left;
+}
+
+// Starts the copy of place q.  Beyond the end of k there are zeros.
+template <int TILE, bool BY_K>
+__device__ __forceinline__ void copy_place(char* lds, const char* from, u32 off, int q, u32 left) {
+  constexpr u32 kN = kTileThreads<TILE>;
+  char* const to = lds + (q * kN + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63u)) * 16;
+  if (left >= (u32)kStep || inside<TILE, BY_K>(q, left))
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) u32*)(from + off),
+                                     (__attribute__((address_space(3))) u32*)to, 16, 0, 0);
+  else
+    *reinterpret_cast<vec4*>(to + threadIdx.x % 64 * 16) = vec4{0, 0, 0, 0};
+}
+
+// A wave's 32 rows (columns) from i on, 16 of k from 16 s on: lane l has row l % 32, k 8 (l / 32) + 0 .. 7.
+template <int TILE, bool BY_K>
+__device__ __forceinline__ i16x8 fragment(const char* lds, u32 i, u32 s) {
+  const u32 lane = threadIdx.x & 63;
+  if constexpr (BY_K) {
+    const u32 row = i + lane % 32;
+    return *reinterpret_cast<const i16x8*>(lds + row * 128 + (((2 * s + lane / 32) ^ (row % 8)) * 16));
+  } else {
+    const u32 k = 16 * s + lane / 32 * 8 + lane % 16 / 4;
+    const u32 col = i + lane % 32 / 16 * 16 + lane % 4 * 4;
+    const char* const p = lds + k * (TILE * 2) + ((col / 8) ^ (4 * (lane % 16 / 4))) * 16 + col % 8 * 2;
+    typedef __attribute__((address_space(3))) i16x4* lds_ptr;
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * (TILE * 2)));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ f32x16 mfma32(i16x8 p, i16x8 q, f32x16 acc) {
+  if constexpr (std::is_same<T, BF16>::value)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), acc, 0, 0, 0);
+}
+
+// The copies have arrived, and every wave has read what it needs of the other buffer.
+__device__ __forceinline__ void turn() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The r-th and c-th tile of workgroup b.  Workgroups go round the eight XCDs; each
+// XCD takes a run of tiles of its own, down columns of `kTall` tiles, so that the
+// tiles that run on it at a time share rows and columns in its L2.
+constexpr u32 kTall = 4;
+__device__ __forceinline__ void tile_of(u32 b, u32 down, u32 across, u32& r, u32& c) {
+  const u32 n = down * across, xcd = b % 8, each = n / 8, more = n % 8;
+  const u32 i = xcd * each + min(xcd, more) + b / 8;
+  const u32 band = i / (kTall * across), in = i % (kTall * across);
+  const u32 tall = min(kTall, down - band * kTall);
+  r = band * kTall + in % tall;
+  c = in / tall;
+}
+
+template <class T, Product KIND, int TILE>
+__global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const ProductLaunch a, u32 down, u32 across) {
+  constexpr bool kQByK = KIND != kWeight, kPByK = KIND == kForward;
+  constexpr int WC = 2, WR = TILE == 256 ? 4 : 2;
+  constexpr int XB = TILE / WC / 32, YB = TILE / WR / 32;
+  constexpr u32 kCols = KIND == kForward ? TILE / 2 : TILE;  // columns of the results
+  __shared__ __attribute__((aligned(128))) char p0[TILE * kStep * 2], p1[TILE * kStep * 2], q0[TILE * kStep * 2],
+      q1[TILE * kStep * 2];
+  u32 tr, tc;
+  const u32 halves = KIND == kWeight ? 2 : 1;
+  tile_of(blockIdx.x, down * halves, across, tr, tc);
+  const int which = KIND == kWeight && tr >= down;
+  const int64_t r0 = (int64_t)(tr - which * down) * TILE, c0 = (int64_t)tc * kCols;
+  const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const u32 wc = wave % WC, wr = wave / WC;
+
+  u32 op[kRounds], oq[kRounds];
+  if constexpr (KIND == kForward) {  // gate's columns, then up's
+    places<TILE, kPByK>(op, 0, 2, a.ld_p[0], c0, a.cols);
+    places<TILE, kPByK>(op, 2, 2, a.ld_p[1], c0, a.cols);
+  } else {
+    places<TILE, kPByK>(op, 0, kRounds, a.ld_p[0], c0, a.cols);
+  }
+  places<TILE, kQByK>(oq, 0, kRounds, a.ld_q[which], r0, a.rows);
+
+  const u32 steps = (u32)((a.k + kStep - 1) / kStep), all = KIND == kInput ? 2 * steps : steps;
+  auto copy = [&](u32 s, char* sp, char* sq) {
+    const int part = KIND == kInput && s >= steps;
+    const int64_t k0 = (int64_t)(part ? s - steps : s) * kStep;
+    const u32 left = (u32)min(a.k - k0, (int64_t)kStep);
+    const int iq = KIND == kForward ? 0 : KIND == kInput ? part : which;
+    const char* const q = a.q[iq] + (kQByK ? r0 * a.ld_q[iq] + k0 * 2 : k0 * a.ld_q[iq] + r0 * 2);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int ip = KIND == kForward ? i / 2 : KIND == kInput ? part : 0;
+      const char* const p = a.p[ip] + (kPByK ? c0 * a.ld_p[ip] + k0 * 2 : k0 * a.ld_p[ip] + c0 * 2);
+      copy_place<TILE, kPByK>(sp, p, op[i], i, left);
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) copy_place<TILE, kQByK>(sq, q, oq[i], i, left);
+  };
+  f32x16 acc[XB][YB] = {};
+  auto work = [&](const char* sp, const char* sq) {
+#pragma unroll
+    for (u32 s = 0; s < kStep / 16; ++s) {
+      i16x8 p[XB], q[YB];
+#pragma unroll
+      for (int y = 0; y < YB; ++y) q[y] = fragment<TILE, kQByK>(sq, (wr * YB + y) * 32, s);
+#pragma unroll
+      for (int x = 0; x < XB; ++x) {
+        const u32 i = KIND == kForward ? x / (XB / 2) * (TILE / 2) + (wc * (XB / 2) + x % (XB / 2)) * 32 : (wc * XB + x) * 32;
+        p[x] = fragment<TILE, kPByK>(sp, i, s);
+      }
+#pragma unroll
+      for (int x = 0; x < XB; ++x)
+#pragma unroll
+        for (int y = 0; y < YB; ++y) acc[x][y] = mfma32<T>(p[x], q[y], acc[x][y]);
+    }
+  };
+  copy(0, p0, q0);
+  u32 s = 0;
+  for (; s + 2 <= all; s += 2) {
+    turn();
+    copy(s + 1, p1, q1);
+    work(p0, q0);
+    turn();
+    if (s + 2 < all) copy(s + 2, p0, q0);
+    work(p1, q1);
+  }
+  if (s < all) {
+    turn();
+    work(p0, q0);
+  }
+
+  const ProductLaunch& b = argument<ProductLaunch>();
+#pragma unroll
+  for (int y = 0; y < YB; ++y) {
+    const int64_t r = r0 + (wr * YB + y) * 32 + lane % 32;
+    if constexpr (KIND == kForward) {
+#pragma unroll
+      for (int x = 0; x < XB / 2; ++x) {
+        const int64_t c = c0 + (wc * (XB / 2) + x) * 32 + lane / 32 * 4;  // + 8 j: groups of four
+        u32 scale[2] = {0, 0};
+        if (b.held[0].codes) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            u32 top = 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j / 4 * 8 + j % 4 < b.cols) top = max(top, finite_magnitude(acc[x + i * (XB / 2)][y][j]));
+            top = max(top, (u32)__shfl_xor((int)top, 32, 64));
+            scale[i] = scale_of(top);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t at = c + 8 * j;
+          if (r >= b.rows || at >= b.cols) continue;
+          const u32 n = (u32)min(b.cols - at, (int64_t)4);
+          float v[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] = acc[x + i * (XB / 2)][y][4 * j + e];
+          finish_gated4<T>(b, r, at, v[0], v[1], n);
+          if (b.held[0].codes) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              store_codes4(b.held[i], r, at, v[i], scale[i], n);
+              if (at % kBlock == 0) b.held[i].scales[r * b.held[i].ld_scales + at / kBlock] = (char)scale[i];
+            }
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < XB; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t at = c0 + (wc * XB + x) * 32 + lane / 32 * 4 + 8 * j;
+          if (r >= b.rows || at >= b.cols) continue;
+          const float v[4] = {acc[x][y][4 * j], acc[x][y][4 * j + 1], acc[x][y][4 * j + 2], acc[x][y][4 * j + 3]};
+          finish4<T, KIND>(b, which, r, at, v, (u32)min(b.cols - at, (int64_t)4));
+        }
+    }
+  }
+}
+
+// Whether the copies of 16 bytes find whole units: addresses, strides, and the lengths
+// along which an operand's rows lie.  Offsets within a tile are 32 bits.
+bool tiles_fit(Product kind, const ProductLaunch& a) {
+  auto ok = [](const char* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && ld < (1 << 22); };
+  const int nq = kind == kForward ? 1 : 2, np = kind == kWeight ? 1 : 2;
+  for (int i = 0; i < nq; ++i)
+    if (!ok(a.q[i], a.ld_q[i])) return false;
+  for (int i = 0; i < np; ++i)
+    if (!ok(a.p[i], a.ld_p[i])) return false;
+  const bool q_by_k = kind != kWeight, p_by_k = kind == kForward;
+  if (a.k < 1 || a.ld_p[0] != a.ld_p[np - 1] || a.ld_q[0] != a.ld_q[nq - 1]) return false;
+  return (q_by_k ? a.k : a.rows) % 8 == 0 && (p_by_k ? a.k : a.cols) % 8 == 0;
+}
+
+template <class T, Product KIND, int TILE>
+int tiled_as(const ProductLaunch& a, hipStream_t s) {
+  constexpr int cols = KIND == kForward ? TILE / 2 : TILE;
+  const u32 down = (u32)((a.rows + TILE - 1) / TILE), across = (u32)((a.cols + cols - 1) / cols);
+  hipLaunchKernelGGL((tiled_kernel<T, KIND, TILE>), dim3(down * across * (KIND == kWeight ? 2 : 1)), dim3(kTileThreads<TILE>), 0,
+                     s, a, down, across);
+  return launched(KIND == kForward ? "gated projections" : KIND == kInput ? "gated input gradient" : "gated weight gradient");
+}
+
+template <class T, Product KIND>
+int tiled_of(const ProductLaunch& a, hipStream_t s) {
+  constexpr int64_t cols = KIND == kForward ? 128 : 256;
+  const int64_t big = (a.rows + 255) / 256 * ((a.cols + cols - 1) / cols) * (KIND == kWeight ? 2 : 1);
+  return big >= 192 ? tiled_as<T, KIND, 256>(a, s) : tiled_as<T, KIND, 128>(a, s);
+}
+
 template <class T, Product KIND>
 int product_as(const ProductLaunch& a, hipStream_t s) {
   const int64_t across = (a.cols + kT - 1) / kT;
@@ -222,6 +492,7 @@ int product_as(const ProductLaunch& a, hipStream_t s) {
 
 template <Product KIND>
 int product_of(const ProductLaunch& a, zero_dtype_t t, hipStream_t s) {
+  if (t != ZERO_F32 && tiles_fit(KIND, a)) return t == ZERO_BF16 ? tiled_of<BF16, KIND>(a, s) : tiled_of<F16, KIND>(a, s);
   switch (t) {
     case ZERO_F32: return product_as<F32, KIND>(a, s);
     case ZERO_BF16: return product_as<BF16, KIND>(a, s);
