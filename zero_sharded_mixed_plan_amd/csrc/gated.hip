@@ -215,66 +215,78 @@ __global__ __launch_bounds__(256) void product_kernel(const ProductLaunch a, int
 // 16-bit types at multiples of 16 bytes
 // ---------------------------------------------------------------------------
 
-// Tiles of TILE x TILE results (of gate and up in the forward pass TILE x TILE / 2 each),
-// 64 of k at a time, which go from global memory straight into LDS (16 bytes a lane,
-// no registers between) while the matrix cores work on the 64 before, from the other of
-// two buffers.  A wave has XB x 2 blocks of 32 x 32 results.
+// Tiles of TILE x TILE results (of gate and up in the forward pass TILE x TILE / 2 each).
+// A wave has XB x 2 blocks of 32 x 32 results.  The operands' tiles, 32 of k at a
+// time, go from global memory straight into LDS (16 bytes a lane, no registers between),
+// four steps ahead: under load a copy takes 2 us and more, two steps of matrix instructions.
 //
-// LDS holds an operand as its rows lie in memory.  Rows of k ([row][64 k], 128 bytes): unit
-// (16 bytes) j of row i sits at j ^ (i % 8), so that the 16-byte reads of 8 lanes in
-// neighbouring rows meet every bank once.  Rows of the other index ([k][TILE]): unit j of
-// row k at j ^ 4 (k % 4), and the transposing read, in which 16 lanes fetch 4 rows of 16
-// columns, meets every bank once too.  The DMA writes LDS in lane order, so a lane fetches
-// the unit that belongs at its place.
+// LDS holds an operand as its rows lie in memory.  Rows of k ([row][32 k], 64 bytes): unit
+// (16 bytes) j of row i sits at j ^ (i / 4 % 4), so that the 16-byte reads of 16 lanes in
+// neighbouring rows meet every bank once.  Rows of the other index ([k][TILE]) are read
+// transposed, 4 rows of 16 columns by 16 lanes: unit j of row k sits at j ^ 2 (k % 4) in
+// tiles of 128; in tiles of 256, whose kernels have no registers for the addresses that this
+// takes, at j ^ 2 (k % 2), and 64 bytes are left out behind every second row of an even
+// pair.  Either way the 4 rows lie in different banks.  The DMA writes LDS in lane
+// order, 1024 bytes a wave, so a lane fetches the unit that belongs at its place.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
-constexpr int kStep = 64;
-constexpr int kRounds = 4;  // 16 bytes a thread and round fill an operand's tile
+constexpr int kStep = 32;
+constexpr int kRounds = 2;  // 16 bytes a thread and round fill an operand's tile
 
 template <int TILE>
 constexpr int kTileThreads = TILE == 256 ? 512 : 256;
+template <int TILE, bool BY_K>
+constexpr int kTileBytes = TILE * kStep * 2 + (TILE == 256 && !BY_K ? 512 : 0);
+// Where the 1024 bytes of chunk c of a tile begin.
+template <int TILE, bool BY_K>
+__device__ __forceinline__ u32 chunk_at(u32 c) {
+  return c * 1024 + (TILE == 256 && !BY_K ? (c + 1) / 2 * 64 : 0);
+}
+template <int TILE>
+__device__ __forceinline__ u32 swizzle(u32 k) {
+  return TILE == 256 ? k % 2 * 2 : k % 4 * 2;
+}
 
-// This thread's places in an operand's tile: byte offsets from the tile's first element.
+// This thread's place of round q in an operand's tile: byte offset from the tile's first element.
 // i0, ni: the tile's first row (column) and the matrix's number of them, beyond which the last
 // ones stand in (what they give is not stored).
 template <int TILE, bool BY_K>
-__device__ __forceinline__ void places(u32 (&off)[kRounds], int round0, int rounds, int64_t ld, int64_t i0, int64_t ni) {
+__device__ __forceinline__ u32 place_of(int q, int64_t ld, int64_t i0, int64_t ni) {
   constexpr u32 kN = kTileThreads<TILE>;
   const u32 t = threadIdx.x;
-#pragma unroll
-  for (int q = 0; q < kRounds; ++q) {
-    if (q < round0 || q >= round0 + rounds) continue;
-    if constexpr (BY_K) {
-      const u32 row = (q - round0) * (kN / 8) + t / 8;
-      const u32 from = (u32)min((int64_t)row, ni - 1 - i0);
-      off[q] = from * (u32)ld + ((t % 8) ^ (t / 8 % 8)) * 16;
-    } else {
-      constexpr u32 kUnits = TILE / 8;
-      const u32 k = q * (kN / kUnits) + t / kUnits;
-      const u32 col = ((t % kUnits) ^ (4 * (k % 4))) * 8;
-      off[q] = k * (u32)ld + (u32)min((int64_t)col, ni - 8 - i0) * 2;
-    }
+  if constexpr (BY_K) {
+    const u32 row = q * (kN / 4) + t / 4;
+    return (u32)min((int64_t)row, ni - 1 - i0) * (u32)ld + ((t % 4) ^ (t / 16 % 4)) * 16;
+  } else {
+    constexpr u32 kUnits = TILE / 8;
+    const u32 k = q * (kN / kUnits) + t / kUnits;
+    const u32 col = ((t % kUnits) ^ swizzle<TILE>(k)) * 8;
+    return k * (u32)ld + (u32)min((int64_t)col, ni - 8 - i0) * 2;
   }
 }
-// Whether place q of the tile lies within the last `left` of k.
+// Whether it lies within the last `left` of k.
 template <int TILE, bool BY_K>
 __device__ __forceinline__ bool inside(int q, u32 left) {
   constexpr u32 kN = kTileThreads<TILE>, kUnits = TILE / 8;
-  const u32 t = threadIdx.x;
-  return BY_K ? ((t % 8) ^ (t / 8 % 8)) * 8 < left : q * (kN / kUnits) + t / kUnits < left;
+  u32 t = threadIdx.x;
+  asm volatile("" : "+v"(t));  // what this needs is not held in registers through the loop
+  return BY_K ? ((t % 4) ^ (t / 16 % 4)) * 8 < left : q * (kN / kUnits) + t / kUnits < left;
 }
 
-// Starts the copy of place q.  Beyond the end of k there are zeros.
-template <int TILE, bool BY_K>
+// Starts the copy of round q.  PART: the last of k, beyond whose `left` there are zeros.
+template <int TILE, bool BY_K, bool PART>
 __device__ __forceinline__ void copy_place(char* lds, const char* from, u32 off, int q, u32 left) {
   constexpr u32 kN = kTileThreads<TILE>;
-  char* const to = lds + (q * kN + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63u)) * 16;
-  if (left >= (u32)kStep || inside<TILE, BY_K>(q, left))
+  char* const to = lds + chunk_at<TILE, BY_K>(q * (kN / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64));
+  if (!PART || inside<TILE, BY_K>(q, left)) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) u32*)(from + off),
                                      (__attribute__((address_space(3))) u32*)to, 16, 0, 0);
-  else
-    *reinterpret_cast<vec4*>(to + threadIdx.x % 64 * 16) = vec4{0, 0, 0, 0};
+  } else {
+    u32 t = threadIdx.x, zero = 0;
+    asm volatile("" : "+v"(t), "+v"(zero));
+    *reinterpret_cast<vec4*>(to + t % 64 * 16) = vec4{zero, zero, zero, zero};
+  }
 }
 
 // A wave's 32 rows (columns) from i on, 16 of k from 16 s on: lane l has row l % 32, k 8 (l / 32) + 0 .. 7.
@@ -283,14 +295,22 @@ __device__ __forceinline__ i16x8 fragment(const char* lds, u32 i, u32 s) {
   const u32 lane = threadIdx.x & 63;
   if constexpr (BY_K) {
     const u32 row = i + lane % 32;
-    return *reinterpret_cast<const i16x8*>(lds + row * 128 + (((2 * s + lane / 32) ^ (row % 8)) * 16));
+    const u32 at = row * 64 + ((2 * s + lane / 32) ^ (lane / 4 % 4)) * 16;
+    return *reinterpret_cast<const i16x8*>(lds + at);
   } else {
-    const u32 k = 16 * s + lane / 32 * 8 + lane % 16 / 4;
-    const u32 col = i + lane % 32 / 16 * 16 + lane % 4 * 4;
-    const char* const p = lds + k * (TILE * 2) + ((col / 8) ^ (4 * (lane % 16 / 4))) * 16 + col % 8 * 2;
+    const u32 j = lane % 16 / 4, unit = lane % 32 / 16 * 2 + lane % 4 / 2;  // row of 4, unit of 32 columns
+    u32 p, p4;  // of rows 8 (l / 32) + j, and 4 behind them
+    if constexpr (TILE == 256) {
+      p = chunk_at<TILE, false>(8 * s) + lane / 32 * chunk_at<TILE, false>(4) + j / 2 * chunk_at<TILE, false>(1) + j % 2 * 512 +
+          i * 2 + (unit ^ swizzle<TILE>(j)) * 16 + lane % 2 * 8;
+      p4 = p + chunk_at<TILE, false>(2);
+    } else {
+      p = (16 * s + lane / 32 * 8 + j) * (TILE * 2) + ((i / 8 + unit) ^ swizzle<TILE>(j)) * 16 + lane % 2 * 8;
+      p4 = p + 4 * (TILE * 2);
+    }
     typedef __attribute__((address_space(3))) i16x4* lds_ptr;
-    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
-    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * (TILE * 2)));
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + p));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + p4));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 }
@@ -303,11 +323,28 @@ __device__ __forceinline__ f32x16 mfma32(i16x8 p, i16x8 q, f32x16 acc) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), acc, 0, 0, 0);
 }
 
-// The copies have arrived, and every wave has read what it needs of the other buffer.
+// All but the newest LATER copies have arrived, for every wave, and every wave's reads are done.
+template <int LATER>
 __device__ __forceinline__ void turn() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  static_assert(LATER < 16, "the field's low bits");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x70 | LATER);  // vmcnt(LATER) lgkmcnt(0), known to the compiler, which adds no others
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Orders the scheduling region: one matrix instruction, one of the copies, EACH reads of LDS, and so on.
+template <int MFMA, int COPIES, int READS, int EACH>
+__device__ __forceinline__ void interleave() {
+  if constexpr (MFMA > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (COPIES > 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS < EACH ? READS : EACH, 0);
+    interleave<MFMA - 1, (COPIES > 0 ? COPIES - 1 : 0), (READS > EACH ? READS - EACH : 0), EACH>();
+  }
 }
 
 // The r-th and c-th tile of workgroup b.  Workgroups go round the eight XCDs; each
@@ -329,8 +366,11 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   constexpr int WC = 2, WR = TILE == 256 ? 4 : 2;
   constexpr int XB = TILE / WC / 32, YB = TILE / WR / 32;
   constexpr u32 kCols = KIND == kForward ? TILE / 2 : TILE;  // columns of the results
-  __shared__ __attribute__((aligned(128))) char p0[TILE * kStep * 2], p1[TILE * kStep * 2], q0[TILE * kStep * 2],
-      q1[TILE * kStep * 2];
+  // Names of their own, so that the compiler sees that reads of one and copies to another do not
+  // meet, and waits for none of them; it tells seven apart.
+  constexpr int kP = kTileBytes<TILE, kPByK>, kQ = kTileBytes<TILE, kQByK>;
+  __shared__ __attribute__((aligned(128))) char p1[kP], p2[kP], p3[kP], q1[kQ], q2[kQ], q3[kQ], first[kP + kQ];
+  char *const p0 = first, *const q0 = first + kP;
   u32 tr, tc;
   const u32 halves = KIND == kWeight ? 2 : 1;
   tile_of(blockIdx.x, down * halves, across, tr, tc);
@@ -340,61 +380,99 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   const u32 wc = wave % WC, wr = wave / WC;
 
   u32 op[kRounds], oq[kRounds];
-  if constexpr (KIND == kForward) {  // gate's columns, then up's
-    places<TILE, kPByK>(op, 0, 2, a.ld_p[0], c0, a.cols);
-    places<TILE, kPByK>(op, 2, 2, a.ld_p[1], c0, a.cols);
-  } else {
-    places<TILE, kPByK>(op, 0, kRounds, a.ld_p[0], c0, a.cols);
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {  // in the forward pass gate's columns, then up's
+    op[i] = place_of<TILE, kPByK>(KIND == kForward ? 0 : i, a.ld_p[0], c0, a.cols);
+    oq[i] = place_of<TILE, kQByK>(i, a.ld_q[0], r0, a.rows);
   }
-  places<TILE, kQByK>(oq, 0, kRounds, a.ld_q[which], r0, a.rows);
-
-  const u32 steps = (u32)((a.k + kStep - 1) / kStep), all = KIND == kInput ? 2 * steps : steps;
-  auto copy = [&](u32 s, char* sp, char* sq) {
-    const int part = KIND == kInput && s >= steps;
-    const int64_t k0 = (int64_t)(part ? s - steps : s) * kStep;
-    const u32 left = (u32)min(a.k - k0, (int64_t)kStep);
-    const int iq = KIND == kForward ? 0 : KIND == kInput ? part : which;
-    const char* const q = a.q[iq] + (kQByK ? r0 * a.ld_q[iq] + k0 * 2 : k0 * a.ld_q[iq] + r0 * 2);
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int ip = KIND == kForward ? i / 2 : KIND == kInput ? part : 0;
-      const char* const p = a.p[ip] + (kPByK ? c0 * a.ld_p[ip] + k0 * 2 : k0 * a.ld_p[ip] + c0 * 2);
-      copy_place<TILE, kPByK>(sp, p, op[i], i, left);
-    }
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) copy_place<TILE, kQByK>(sq, q, oq[i], i, left);
-  };
   f32x16 acc[XB][YB] = {};
-  auto work = [&](const char* sp, const char* sq) {
-#pragma unroll
-    for (u32 s = 0; s < kStep / 16; ++s) {
-      i16x8 p[XB], q[YB];
-#pragma unroll
-      for (int y = 0; y < YB; ++y) q[y] = fragment<TILE, kQByK>(sq, (wr * YB + y) * 32, s);
-#pragma unroll
-      for (int x = 0; x < XB; ++x) {
-        const u32 i = KIND == kForward ? x / (XB / 2) * (TILE / 2) + (wc * (XB / 2) + x % (XB / 2)) * 32 : (wc * XB + x) * 32;
-        p[x] = fragment<TILE, kPByK>(sp, i, s);
-      }
-#pragma unroll
-      for (int x = 0; x < XB; ++x)
-#pragma unroll
-        for (int y = 0; y < YB; ++y) acc[x][y] = mfma32<T>(p[x], q[y], acc[x][y]);
-    }
+  struct Fragments {
+    i16x8 p[kStep / 16][XB], q[kStep / 16][YB];
   };
-  copy(0, p0, q0);
-  u32 s = 0;
-  for (; s + 2 <= all; s += 2) {
-    turn();
-    copy(s + 1, p1, q1);
-    work(p0, q0);
-    turn();
-    if (s + 2 < all) copy(s + 2, p0, q0);
-    work(p1, q1);
-  }
-  if (s < all) {
-    turn();
-    work(p0, q0);
+  const u32 steps = (u32)((a.k + kStep - 1) / kStep);
+  for (int part = 0; part < (KIND == kInput ? 2 : 1); ++part) {
+    const int iq = KIND == kWeight ? which : part;
+    auto copy = [&](u32 s, char* sp, char* sq, auto whole) {
+      const int64_t k0 = (int64_t)s * kStep;
+      const u32 left = (u32)min(a.k - k0, (int64_t)kStep);
+      const char* const q = a.q[iq] + (kQByK ? r0 * a.ld_q[0] + k0 * 2 : k0 * a.ld_q[0] + r0 * 2);
+      auto start = [&](auto is_part) {
+        constexpr bool kPart = decltype(is_part)::value;
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+          const int ip = KIND == kForward ? i : KIND == kInput ? part : 0;
+          const char* const p = a.p[ip] + (kPByK ? c0 * a.ld_p[0] + k0 * 2 : k0 * a.ld_p[0] + c0 * 2);
+          copy_place<TILE, kPByK, kPart>(sp, p, op[i], i, left);
+        }
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) copy_place<TILE, kQByK, kPart>(sq, q, oq[i], i, left);
+      };
+      if (decltype(whole)::value || left == kStep) start(std::false_type{});
+      else start(std::true_type{});
+    };
+    auto read = [&](const char* sp, const char* sq, Fragments& f) {
+#pragma unroll
+      for (u32 s = 0; s < kStep / 16; ++s) {
+#pragma unroll
+        for (int y = 0; y < YB; ++y) f.q[s][y] = fragment<TILE, kQByK>(sq, (wr * YB + y) * 32, s);
+#pragma unroll
+        for (int x = 0; x < XB; ++x) {
+          const u32 i = KIND == kForward ? x / (XB / 2) * (TILE / 2) + (wc * (XB / 2) + x % (XB / 2)) * 32 : (wc * XB + x) * 32;
+          f.p[s][x] = fragment<TILE, kPByK>(sp, i, s);
+        }
+      }
+    };
+    // Step s multiplies fragments that are in registers, while those of step s + 1 are read and the
+    // copies of steps s + 2 to s + 4 are under way, the last of them into the buffer that step s was read from.
+    auto multiply_and_read = [&](const Fragments& f, const char* sp, const char* sq, Fragments& next) {
+      read(sp, sq, next);
+#pragma unroll
+      for (u32 s = 0; s < kStep / 16; ++s)
+#pragma unroll
+        for (int x = 0; x < XB; ++x)
+#pragma unroll
+          for (int y = 0; y < YB; ++y) acc[x][y] = mfma32<T>(f.p[s][x], f.q[s][y], acc[x][y]);
+      // a few reads behind each matrix instruction, so that neither waits for the other
+      constexpr int kReads = kStep / 16 * ((kPByK ? 1 : 2) * XB + (kQByK ? 1 : 2) * YB);
+      constexpr int kMfma = kStep / 16 * XB * YB;
+      constexpr int kEach = (kReads + kMfma - 3) / (kMfma - 2);
+      interleave<kMfma, 2 * kRounds, kReads, kEach>();
+    };
+    auto step = [&](u32 s, const Fragments& f, Fragments& next, char* p, char* q, const char* from_p, const char* from_q) {
+      copy(s + 4, p, q, std::true_type{});
+      multiply_and_read(f, from_p, from_q, next);
+      turn<4 * kRounds>();
+    };
+    auto last_steps = [&](u32 s, const Fragments& f, Fragments& next, char* p, char* q, const char* from_p,
+                          const char* from_q) {
+      if (s >= steps) return;
+      if (s + 4 < steps) copy(s + 4, p, q, std::false_type{});
+      multiply_and_read(f, from_p, from_q, next);
+      turn<0>();
+    };
+    Fragments f, g;
+    copy(0, p0, q0, std::false_type{});
+    if (1 < steps) copy(1, p1, q1, std::false_type{});
+    if (2 < steps) copy(2, p2, q2, std::false_type{});
+    if (3 < steps) copy(3, p3, q3, std::false_type{});
+    if (steps > 4) turn<4 * kRounds>();
+    else turn<0>();
+    read(p0, q0, f);
+    turn<4 * kRounds>();
+    u32 s = 0;
+    for (; s + 8 < steps; s += 4) {  // copies of whole steps only
+      step(s, f, g, p0, q0, p1, q1);
+      step(s + 1, g, f, p1, q1, p2, q2);
+      step(s + 2, f, g, p2, q2, p3, q3);
+      step(s + 3, g, f, p3, q3, p0, q0);
+    }
+#pragma unroll 1
+    for (; s < steps; s += 4) {
+      last_steps(s, f, g, p0, q0, p1, q1);
+      last_steps(s + 1, g, f, p1, q1, p2, q2);
+      last_steps(s + 2, f, g, p2, q2, p3, q3);
+      last_steps(s + 3, g, f, p3, q3, p0, q0);
+    }
   }
 
   const ProductLaunch& b = argument<ProductLaunch>();
