@@ -216,28 +216,34 @@ __global__ __launch_bounds__(256) void product_kernel(const ProductLaunch a, int
 // ---------------------------------------------------------------------------
 
 // Tiles of TILE x TILE results (of gate and up in the forward pass TILE x TILE / 2 each).
-// A wave has XB x 2 blocks of 32 x 32 results.  The operands' tiles, 32 of k at a
-// time, go from global memory straight into LDS (16 bytes a lane, no registers between),
-// four steps ahead: under load a copy takes 2 us and more, two steps of matrix instructions.
+// A wave has XB x 2 blocks of 32 x 32 results.  The operands' tiles go from global memory
+// straight into LDS (16 bytes a lane, no registers between), two to four steps of 32 of k
+// before they are used: under load a copy takes a microsecond and more, a step of matrix
+// instructions 0.6.
 //
-// LDS holds an operand as its rows lie in memory.  Rows of k ([row][32 k], 64 bytes): unit
-// (16 bytes) j of row i sits at j ^ (i / 4 % 4), so that the 16-byte reads of 16 lanes in
-// neighbouring rows meet every bank once.  Rows of the other index ([k][TILE]) are read
-// transposed, 4 rows of 16 columns by 16 lanes: unit j of row k sits at j ^ 2 (k % 4) in
-// tiles of 128; in tiles of 256, whose kernels have no registers for the addresses that this
-// takes, at j ^ 2 (k % 2), and 64 bytes are left out behind every second row of an even
-// pair.  Either way the 4 rows lie in different banks.  The DMA writes LDS in lane
-// order, 1024 bytes a wave, so a lane fetches the unit that belongs at its place.
+// LDS holds an operand as its rows lie in memory.  Rows of k are copied 64 of k at a time,
+// 128 bytes, whole lines of the L2 (with half lines its requests doubled, and the
+// forward pass took 1626 us in place of FWD_US): unit (16 bytes) j of row i sits at
+// j ^ (i / 2 % 8), so that the 16-byte reads of 16 lanes in neighbouring rows meet every bank once.
+// Rows of the other index ([32 k][TILE]) are read transposed, 4 rows of 16 columns by 16
+// lanes: unit j of row k sits at j ^ 2 (k % 4) in tiles of 128; in tiles of 256, whose kernels
+// have no registers for the addresses that this takes, at j ^ 2 (k % 2), with 64 bytes
+// left out before every odd pair of rows.  Either way the 4 rows lie in different banks.
+// The DMA writes LDS in lane order, 1024 bytes a wave, so a lane fetches the unit that belongs
+// at its place.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 constexpr int kStep = 32;
-constexpr int kRounds = 2;  // 16 bytes a thread and round fill an operand's tile
+template <bool BY_K>
+constexpr int kDeep = BY_K ? 2 * kStep : kStep;  // of k, copied at a time
+template <bool BY_K>
+constexpr int kRounds = BY_K ? 4 : 2;            // 16 bytes a thread and round
 
 template <int TILE>
 constexpr int kTileThreads = TILE == 256 ? 512 : 256;
 template <int TILE, bool BY_K>
-constexpr int kTileBytes = TILE * kStep * 2 + (TILE == 256 && !BY_K ? 512 : 0);
+constexpr int kTileBytes = TILE * kDeep<BY_K> * 2 + (TILE == 256 && !BY_K ? 512 : 0);
 // Where the 1024 bytes of chunk c of a tile begin.
 template <int TILE, bool BY_K>
 __device__ __forceinline__ u32 chunk_at(u32 c) {
@@ -256,8 +262,8 @@ __device__ __forceinline__ u32 place_of(int q, int64_t ld, int64_t i0, int64_t n
   constexpr u32 kN = kTileThreads<TILE>;
   const u32 t = threadIdx.x;
   if constexpr (BY_K) {
-    const u32 row = q * (kN / 4) + t / 4;
-    return (u32)min((int64_t)row, ni - 1 - i0) * (u32)ld + ((t % 4) ^ (t / 16 % 4)) * 16;
+    const u32 row = q * (kN / 8) + t / 8;
+    return (u32)min((int64_t)row, ni - 1 - i0) * (u32)ld + ((t % 8) ^ (t / 16 % 8)) * 16;
   } else {
     constexpr u32 kUnits = TILE / 8;
     const u32 k = q * (kN / kUnits) + t / kUnits;
@@ -267,21 +273,26 @@ __device__ __forceinline__ u32 place_of(int q, int64_t ld, int64_t i0, int64_t n
 }
 // Whether it lies within the last `left` of k.
 template <int TILE, bool BY_K>
-__device__ __forceinline__ bool inside(int q, u32 left) {
+__device__ __forceinline__ bool inside(int q, int left) {
   constexpr u32 kN = kTileThreads<TILE>, kUnits = TILE / 8;
   u32 t = threadIdx.x;
   asm volatile("" : "+v"(t));  // what this needs is not held in registers through the loop
-  return BY_K ? ((t % 4) ^ (t / 16 % 4)) * 8 < left : q * (kN / kUnits) + t / kUnits < left;
+  return (int)(BY_K ? ((t % 8) ^ (t / 16 % 8)) * 8 : q * (kN / kUnits) + t / kUnits) < left;
+}
+
+// What copies read from: bytes from p on, by 32-bit offsets.  A buffer descriptor costs a copy no vector
+// instruction and no register for its address.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const char* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, 0x7fffffff, 0x00020000);
 }
 
 // Starts the copy of round q.  PART: the last of k, beyond whose `left` there are zeros.
 template <int TILE, bool BY_K, bool PART>
-__device__ __forceinline__ void copy_place(char* lds, const char* from, u32 off, int q, u32 left) {
+__device__ __forceinline__ void copy_place(char* lds, __amdgpu_buffer_rsrc_t from, u32 off, int q, int left) {
   constexpr u32 kN = kTileThreads<TILE>;
   char* const to = lds + chunk_at<TILE, BY_K>(q * (kN / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64));
   if (!PART || inside<TILE, BY_K>(q, left)) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) u32*)(from + off),
-                                     (__attribute__((address_space(3))) u32*)to, 16, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
   } else {
     u32 t = threadIdx.x, zero = 0;
     asm volatile("" : "+v"(t), "+v"(zero));
@@ -295,7 +306,7 @@ __device__ __forceinline__ i16x8 fragment(const char* lds, u32 i, u32 s) {
   const u32 lane = threadIdx.x & 63;
   if constexpr (BY_K) {
     const u32 row = i + lane % 32;
-    const u32 at = row * 64 + ((2 * s + lane / 32) ^ (lane / 4 % 4)) * 16;
+    const u32 at = row * 128 + ((2 * s + lane / 32) ^ (lane / 2 % 8)) * 16;
     return *reinterpret_cast<const i16x8*>(lds + at);
   } else {
     const u32 j = lane % 16 / 4, unit = lane % 32 / 16 * 2 + lane % 4 / 2;  // row of 4, unit of 32 columns
@@ -367,10 +378,12 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   constexpr int XB = TILE / WC / 32, YB = TILE / WR / 32;
   constexpr u32 kCols = KIND == kForward ? TILE / 2 : TILE;  // columns of the results
   // Names of their own, so that the compiler sees that reads of one and copies to another do not
-  // meet, and waits for none of them; it tells seven apart.
+  // meet, and waits for none of them; it tells seven apart.  An operand has two deep tiles, or four.
   constexpr int kP = kTileBytes<TILE, kPByK>, kQ = kTileBytes<TILE, kQByK>;
-  __shared__ __attribute__((aligned(128))) char p1[kP], p2[kP], p3[kP], q1[kQ], q2[kQ], q3[kQ], first[kP + kQ];
-  char *const p0 = first, *const q0 = first + kP;
+  constexpr bool kEight = !kPByK && !kQByK;
+  __shared__ __attribute__((aligned(128))) char p1[kP], p2[kPByK ? 16 : kP], p3[kPByK ? 16 : kP];
+  __shared__ __attribute__((aligned(128))) char q1[kQ], q2[kQByK ? 16 : kQ], q3[kQByK ? 16 : kQ];
+  __shared__ __attribute__((aligned(128))) char p0[kEight ? kP + kQ : kP], q0[kEight ? 16 : kQ];
   u32 tr, tc;
   const u32 halves = KIND == kWeight ? 2 : 1;
   tile_of(blockIdx.x, down * halves, across, tr, tc);
@@ -379,53 +392,87 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const u32 wc = wave % WC, wr = wave / WC;
 
-  u32 op[kRounds], oq[kRounds];
+  constexpr int kRP = kRounds<kPByK>, kRQ = kRounds<kQByK>;
+  u32 op[kRP], oq[kRQ];
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {  // in the forward pass gate's columns, then up's
-    op[i] = place_of<TILE, kPByK>(KIND == kForward ? 0 : i, a.ld_p[0], c0, a.cols);
-    oq[i] = place_of<TILE, kQByK>(i, a.ld_q[0], r0, a.rows);
-  }
+  for (int i = 0; i < kRP; ++i)  // in the forward pass gate's columns, then up's
+    op[i] = place_of<TILE, kPByK>(KIND == kForward ? i % (kRP / 2) : i, a.ld_p[0], c0, a.cols);
+#pragma unroll
+  for (int i = 0; i < kRQ; ++i) oq[i] = place_of<TILE, kQByK>(i, a.ld_q[0], r0, a.rows);
   f32x16 acc[XB][YB] = {};
   struct Fragments {
     i16x8 p[kStep / 16][XB], q[kStep / 16][YB];
   };
-  const u32 steps = (u32)((a.k + kStep - 1) / kStep);
+  const u32 steps = (u32)((a.k + kStep - 1) / kStep), whole = (u32)(a.k / kStep);
   for (int part = 0; part < (KIND == kInput ? 2 : 1); ++part) {
-    const int iq = KIND == kWeight ? which : part;
-    auto copy = [&](u32 s, char* sp, char* sq, auto whole) {
-      const int64_t k0 = (int64_t)s * kStep;
-      const u32 left = (u32)min(a.k - k0, (int64_t)kStep);
-      const char* const q = a.q[iq] + (kQByK ? r0 * a.ld_q[0] + k0 * 2 : k0 * a.ld_q[0] + r0 * 2);
+    const int iq = KIND == kWeight ? which : part, ip = KIND == kInput ? part : 0;
+    // where the next copies begin, how far a copy goes, and what is left of k there
+    const char* next_q = a.q[iq] + (kQByK ? r0 * a.ld_q[0] : r0 * 2);
+    const char* next_p[2] = {a.p[ip] + (kPByK ? c0 * a.ld_p[0] : c0 * 2), KIND == kForward ? a.p[1] + c0 * a.ld_p[0] : nullptr};
+    const int64_t far_q = kDeep<kQByK> * (kQByK ? 2 : a.ld_q[0]), far_p = kDeep<kPByK> * (kPByK ? 2 : a.ld_p[0]);
+    int left_p = (int)a.k, left_q = (int)a.k;
+    auto copy_p = [&](char* to, auto all_whole) {
       auto start = [&](auto is_part) {
-        constexpr bool kPart = decltype(is_part)::value;
 #pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-          const int ip = KIND == kForward ? i : KIND == kInput ? part : 0;
-          const char* const p = a.p[ip] + (kPByK ? c0 * a.ld_p[0] + k0 * 2 : k0 * a.ld_p[0] + c0 * 2);
-          copy_place<TILE, kPByK, kPart>(sp, p, op[i], i, left);
-        }
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) copy_place<TILE, kQByK, kPart>(sq, q, oq[i], i, left);
+        for (int i = 0; i < kRP; ++i)
+          copy_place<TILE, kPByK, decltype(is_part)::value>(to, buffer_at(next_p[KIND == kForward ? i / (kRP / 2) : 0]), op[i], i,
+                                                            left_p);
       };
-      if (decltype(whole)::value || left == kStep) start(std::false_type{});
+      if (decltype(all_whole)::value || left_p >= kDeep<kPByK>) start(std::false_type{});
       else start(std::true_type{});
+      next_p[0] += far_p;
+      if constexpr (KIND == kForward) next_p[1] += far_p;
+      left_p -= kDeep<kPByK>;
     };
-    auto read = [&](const char* sp, const char* sq, Fragments& f) {
+    auto copy_q = [&](char* to, auto all_whole) {
+      auto start = [&](auto is_part) {
+#pragma unroll
+        for (int i = 0; i < kRQ; ++i) copy_place<TILE, kQByK, decltype(is_part)::value>(to, buffer_at(next_q), oq[i], i, left_q);
+      };
+      if (decltype(all_whole)::value || left_q >= kDeep<kQByK>) start(std::false_type{});
+      else start(std::true_type{});
+      next_q += far_q;
+      left_q -= kDeep<kQByK>;
+    };
+    // Steps go round J = 0 .. 3.  The tile of step J, or of steps J and J + 1 (J even) where it is deep:
+    auto tile_p = [&](auto j) -> char* {
+      constexpr int J = decltype(j)::value & 3;
+      if constexpr (kPByK) return J < 2 ? p0 : p1;
+      else return J == 0 ? p0 : J == 1 ? p1 : J == 2 ? p2 : p3;
+    };
+    auto tile_q = [&](auto j) -> char* {
+      constexpr int J = decltype(j)::value & 3;
+      if constexpr (kQByK) return J < 2 ? q0 : q1;
+      else return J == 0 ? (kEight ? p0 + kP : q0) : J == 1 ? q1 : J == 2 ? q2 : q3;
+    };
+    auto read = [&](auto j, Fragments& f) {
+      constexpr u32 J = decltype(j)::value & 3;
 #pragma unroll
       for (u32 s = 0; s < kStep / 16; ++s) {
 #pragma unroll
-        for (int y = 0; y < YB; ++y) f.q[s][y] = fragment<TILE, kQByK>(sq, (wr * YB + y) * 32, s);
+        for (int y = 0; y < YB; ++y)
+          f.q[s][y] = fragment<TILE, kQByK>(tile_q(j), (wr * YB + y) * 32, s + (kQByK ? J % 2 * 2 : 0));
 #pragma unroll
         for (int x = 0; x < XB; ++x) {
           const u32 i = KIND == kForward ? x / (XB / 2) * (TILE / 2) + (wc * (XB / 2) + x % (XB / 2)) * 32 : (wc * XB + x) * 32;
-          f.p[s][x] = fragment<TILE, kPByK>(sp, i, s);
+          f.p[s][x] = fragment<TILE, kPByK>(tile_p(j), i, s + (kPByK ? J % 2 * 2 : 0));
         }
       }
     };
-    // Step s multiplies fragments that are in registers, while those of step s + 1 are read and the
-    // copies of steps s + 2 to s + 4 are under way, the last of them into the buffer that step s was read from.
-    auto multiply_and_read = [&](const Fragments& f, const char* sp, const char* sq, Fragments& next) {
-      read(sp, sq, next);
+    // A step multiplies fragments that are in registers, while those of the next one are read, and starts
+    // the copies that fit into what it was itself read from: a step's tile four steps ahead, or
+    // with its second step a deep tile three steps ahead.
+    auto copies = [&](auto j, u32 s, auto all_whole) {
+      constexpr int J = decltype(j)::value;
+      const bool small = decltype(all_whole)::value || s + 4 < steps, deep = decltype(all_whole)::value || s + 3 < steps;
+      if constexpr (!kPByK || J % 2 == 1)
+        if (kPByK ? deep : small) copy_p(tile_p(j), all_whole);
+      if constexpr (!kQByK || J % 2 == 1)
+        if (kQByK ? deep : small) copy_q(tile_q(j), all_whole);
+    };
+    auto multiply_and_read = [&](auto j, const Fragments& f, Fragments& next) {
+      constexpr int J = decltype(j)::value;
+      read(std::integral_constant<int, J + 1>{}, next);
 #pragma unroll
       for (u32 s = 0; s < kStep / 16; ++s)
 #pragma unroll
@@ -436,42 +483,55 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
       constexpr int kReads = kStep / 16 * ((kPByK ? 1 : 2) * XB + (kQByK ? 1 : 2) * YB);
       constexpr int kMfma = kStep / 16 * XB * YB;
       constexpr int kEach = (kReads + kMfma - 3) / (kMfma - 2);
-      interleave<kMfma, 2 * kRounds, kReads, kEach>();
+      interleave<kMfma, (!kPByK || J % 2 ? kRP : 0) + (!kQByK || J % 2 ? kRQ : 0), kReads, kEach>();
     };
-    auto step = [&](u32 s, const Fragments& f, Fragments& next, char* p, char* q, const char* from_p, const char* from_q) {
-      copy(s + 4, p, q, std::true_type{});
-      multiply_and_read(f, from_p, from_q, next);
-      turn<4 * kRounds>();
+    constexpr int kSmall = (kPByK ? 0 : kRP) + (kQByK ? 0 : kRQ);  // copies started by an even step
+    auto step = [&](auto j, const Fragments& f, Fragments& next) {
+      constexpr int J = decltype(j)::value;
+      copies(j, 0, std::true_type{});
+      multiply_and_read(j, f, next);
+      // what the next step reads has arrived: deep tiles started by the step before an even one; tiles of
+      // one step started two before
+      turn<(kPByK || kQByK) && J % 2 == 0 ? kSmall : 8>();
     };
-    auto last_steps = [&](u32 s, const Fragments& f, Fragments& next, char* p, char* q, const char* from_p,
-                          const char* from_q) {
+    auto last_steps = [&](auto j, u32 s, const Fragments& f, Fragments& next) {
       if (s >= steps) return;
-      if (s + 4 < steps) copy(s + 4, p, q, std::false_type{});
-      multiply_and_read(f, from_p, from_q, next);
+      copies(j, s, std::false_type{});
+      multiply_and_read(j, f, next);
       turn<0>();
     };
+    using J0 = std::integral_constant<int, 0>;
+    using J1 = std::integral_constant<int, 1>;
+    using J2 = std::integral_constant<int, 2>;
+    using J3 = std::integral_constant<int, 3>;
     Fragments f, g;
-    copy(0, p0, q0, std::false_type{});
-    if (1 < steps) copy(1, p1, q1, std::false_type{});
-    if (2 < steps) copy(2, p2, q2, std::false_type{});
-    if (3 < steps) copy(3, p3, q3, std::false_type{});
-    if (steps > 4) turn<4 * kRounds>();
+    copy_p(tile_p(J0{}), std::false_type{});
+    copy_q(tile_q(J0{}), std::false_type{});
+    if (!kPByK && 1 < steps) copy_p(tile_p(J1{}), std::false_type{});
+    if (!kQByK && 1 < steps) copy_q(tile_q(J1{}), std::false_type{});
+    if (2 < steps) {
+      copy_p(tile_p(J2{}), std::false_type{});
+      copy_q(tile_q(J2{}), std::false_type{});
+    }
+    if (!kPByK && 3 < steps) copy_p(tile_p(J3{}), std::false_type{});
+    if (!kQByK && 3 < steps) copy_q(tile_q(J3{}), std::false_type{});
+    if (whole >= 4) turn<8>();  // the second four steps' copies may still be under way
     else turn<0>();
-    read(p0, q0, f);
-    turn<4 * kRounds>();
+    read(J0{}, f);
+    turn<8>();
     u32 s = 0;
-    for (; s + 8 < steps; s += 4) {  // copies of whole steps only
-      step(s, f, g, p0, q0, p1, q1);
-      step(s + 1, g, f, p1, q1, p2, q2);
-      step(s + 2, f, g, p2, q2, p3, q3);
-      step(s + 3, g, f, p3, q3, p0, q0);
+    for (; s + 8 <= whole; s += 4) {  // copies of whole steps only
+      step(J0{}, f, g);
+      step(J1{}, g, f);
+      step(J2{}, f, g);
+      step(J3{}, g, f);
     }
 #pragma unroll 1
     for (; s < steps; s += 4) {
-      last_steps(s, f, g, p0, q0, p1, q1);
-      last_steps(s + 1, g, f, p1, q1, p2, q2);
-      last_steps(s + 2, f, g, p2, q2, p3, q3);
-      last_steps(s + 3, g, f, p3, q3, p0, q0);
+      last_steps(J0{}, s, f, g);
+      last_steps(J1{}, s + 1, g, f);
+      last_steps(J2{}, s + 2, f, g);
+      last_steps(J3{}, s + 3, g, f);
     }
   }
 
