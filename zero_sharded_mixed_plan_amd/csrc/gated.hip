@@ -300,25 +300,37 @@ __device__ __forceinline__ void copy_place(char* lds, __amdgpu_buffer_rsrc_t fro
   }
 }
 
-// A wave's 32 rows (columns) from i on, 16 of k from 16 s on: lane l has row l % 32, k 8 (l / 32) + 0 .. 7.
-template <int TILE, bool BY_K>
-__device__ __forceinline__ i16x8 fragment(const char* lds, u32 i, u32 s) {
+// This lane's offsets of the blocks of 32 rows (columns) from i0, i0 + 32 .. on.  The compiler has to
+// see an LDS address as one sum, or it loses which tile it lies in.
+template <int TILE, bool BY_K, int N>
+__device__ __forceinline__ void block_offsets(u32 (&at)[N], u32 i0) {
   const u32 lane = threadIdx.x & 63;
-  if constexpr (BY_K) {
-    const u32 row = i + lane % 32;
-    const u32 at = row * 128 + ((2 * s + lane / 32) ^ (lane / 2 % 8)) * 16;
-    return *reinterpret_cast<const i16x8*>(lds + at);
-  } else {
-    const u32 j = lane % 16 / 4, unit = lane % 32 / 16 * 2 + lane % 4 / 2;  // row of 4, unit of 32 columns
-    u32 p, p4;  // of rows 8 (l / 32) + j, and 4 behind them
-    if constexpr (TILE == 256) {
-      p = chunk_at<TILE, false>(8 * s) + lane / 32 * chunk_at<TILE, false>(4) + j / 2 * chunk_at<TILE, false>(1) + j % 2 * 512 +
-          i * 2 + (unit ^ swizzle<TILE>(j)) * 16 + lane % 2 * 8;
-      p4 = p + chunk_at<TILE, false>(2);
-    } else {
-      p = (16 * s + lane / 32 * 8 + j) * (TILE * 2) + ((i / 8 + unit) ^ swizzle<TILE>(j)) * 16 + lane % 2 * 8;
-      p4 = p + 4 * (TILE * 2);
+  const u32 j = lane % 16 / 4, unit = lane % 32 / 16 * 2 + lane % 4 / 2;  // row of 4, unit of 32 columns
+  constexpr bool kOne = BY_K || TILE == 256;  // the others lie a fixed way behind the first
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    if (kOne && x > 0) {
+      at[x] = at[0] + x * (BY_K ? 32 * 128 : 64);
+      continue;
     }
+    const u32 i = i0 + 32 * x;
+    if constexpr (BY_K) at[x] = (i + lane % 32) * 128 + ((lane / 32) ^ (lane / 2 % 8)) * 16;
+    else if constexpr (TILE == 256)
+      at[x] = lane / 32 * chunk_at<TILE, false>(4) + j / 2 * chunk_at<TILE, false>(1) + j % 2 * 512 + i * 2 +
+              (unit ^ swizzle<TILE>(j)) * 16 + lane % 2 * 8;
+    else at[x] = (lane / 32 * 8 + j) * (TILE * 2) + ((i / 8 + unit) ^ swizzle<TILE>(j)) * 16 + lane % 2 * 8;
+    if constexpr (!BY_K) asm("" : "+v"(at[x]));
+  }
+}
+
+// 16 of k from 16 s on of a block: lane l has row (column) l % 32, k 8 (l / 32) + 0 .. 7.
+template <int TILE, bool BY_K>
+__device__ __forceinline__ i16x8 fragment(const char* lds, u32 at, u32 s) {
+  if constexpr (BY_K) {
+    return *reinterpret_cast<const i16x8*>(lds + (at ^ (s * 32)));
+  } else {
+    const u32 p = at + (TILE == 256 ? chunk_at<TILE, false>(8 * s) : 16 * s * (TILE * 2));
+    const u32 p4 = p + (TILE == 256 ? chunk_at<TILE, false>(2) : 4 * (TILE * 2));  // 4 rows on
     typedef __attribute__((address_space(3))) i16x4* lds_ptr;
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + p));
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + p4));
@@ -399,6 +411,16 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
     op[i] = place_of<TILE, kPByK>(KIND == kForward ? i % (kRP / 2) : i, a.ld_p[0], c0, a.cols);
 #pragma unroll
   for (int i = 0; i < kRQ; ++i) oq[i] = place_of<TILE, kQByK>(i, a.ld_q[0], r0, a.rows);
+  u32 at_p[XB], at_q[YB];
+  block_offsets<TILE, kQByK>(at_q, wr * YB * 32);
+  if constexpr (KIND == kForward) {  // blocks of gate, then of up
+    u32 gate[XB / 2];
+    block_offsets<TILE, kPByK>(gate, wc * (XB / 2) * 32);
+#pragma unroll
+    for (int x = 0; x < XB; ++x) at_p[x] = gate[x % (XB / 2)] + x / (XB / 2) * (TILE / 2) * 128;
+  } else {
+    block_offsets<TILE, kPByK>(at_p, wc * XB * 32);
+  }
   f32x16 acc[XB][YB] = {};
   struct Fragments {
     i16x8 p[kStep / 16][XB], q[kStep / 16][YB];
@@ -451,12 +473,10 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
       for (u32 s = 0; s < kStep / 16; ++s) {
 #pragma unroll
         for (int y = 0; y < YB; ++y)
-          f.q[s][y] = fragment<TILE, kQByK>(tile_q(j), (wr * YB + y) * 32, s + (kQByK ? J % 2 * 2 : 0));
+          f.q[s][y] = fragment<TILE, kQByK>(tile_q(j), at_q[y], s + (kQByK ? J % 2 * 2 : 0));
 #pragma unroll
-        for (int x = 0; x < XB; ++x) {
-          const u32 i = KIND == kForward ? x / (XB / 2) * (TILE / 2) + (wc * (XB / 2) + x % (XB / 2)) * 32 : (wc * XB + x) * 32;
-          f.p[s][x] = fragment<TILE, kPByK>(tile_p(j), i, s + (kPByK ? J % 2 * 2 : 0));
-        }
+        for (int x = 0; x < XB; ++x)
+          f.p[s][x] = fragment<TILE, kPByK>(tile_p(j), at_p[x], s + (kPByK ? J % 2 * 2 : 0));
       }
     };
     // A step multiplies fragments that are in registers, while those of the next one are read, and starts
