@@ -8,6 +8,7 @@ namespace zk {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -27,14 +28,19 @@ __device__ __forceinline__ void finish4(const ProductLaunch& a, int which, int64
     store4<T>(a.out[0] + r * a.ld_out[0] + c * T::bytes, v, n);
   } else {
     char* const p = a.out[which] + r * a.ld_out[which] + c * one_bytes(a.out_type);
-    float s[4];
+    float s[4] = {v[0], v[1], v[2], v[3]};
+    if (a.accumulate) {
+      float old[4];
+      load4_as(p, a.out_type, n, old);
 #pragma unroll
-    for (u32 j = 0; j < 4; ++j) {
-      s[j] = v[j];
-      if (a.accumulate && j < n) s[j] += load_one(p + j * one_bytes(a.out_type), a.out_type);
+      for (int j = 0; j < 4; ++j) s[j] += old[j];
     }
     store4_as(p, a.out_type, s, n);
   }
+}
+
+__device__ __forceinline__ float gated_value(int32_t act, float g, float u) {
+  return g * (act == kSilu ? gate_of<kSilu>(g).p : gate_of<kGelu>(g).p) * u;
 }
 
 // The same of the forward pass: gate and up.
@@ -43,8 +49,7 @@ __device__ __forceinline__ void finish_gated4(const ProductLaunch& a, int64_t r,
                                               u32 n) {
   float v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] = g[j] * (a.act == kSilu ? gate_of<kSilu>(g[j]).p : gate_of<kGelu>(g[j]).p) * u[j];
+  for (int j = 0; j < 4; ++j) v[j] = gated_value(a.act, g[j], u[j]);
   store4<T>(a.out[0] + r * a.ld_out[0] + c * T::bytes, v, n);
   if (a.kept[0]) {
     store4<T>(a.kept[0] + r * a.ld_kept[0] + c * T::bytes, g, n);
@@ -212,6 +217,119 @@ __global__ __launch_bounds__(256) void product_kernel(const ProductLaunch a, int
 }
 
 // ---------------------------------------------------------------------------
+// results by way of LDS
+// ---------------------------------------------------------------------------
+
+// 32 rows of a wave, each of WIDE 16-bit results, 32 fp32 ones or WIDE codes, 16 bytes apart from the next
+// row so that the lanes' rows begin in different banks.  In a block of 32 x 32 results lane l
+// has row l % 32, columns 8 j + 4 (l / 32) + 0 .. 3.
+constexpr u32 kStageBytes = 32 * 144;
+
+template <class T, int WIDE>
+__device__ __forceinline__ void stage_bits(char* s, u32 col, const float v[4]) {
+  const u32 lane = threadIdx.x & 63;
+  const vec2 w = {bits_of<T>(v[0]) | bits_of<T>(v[1]) << 16, bits_of<T>(v[2]) | bits_of<T>(v[3]) << 16};
+  *reinterpret_cast<vec2*>(s + lane % 32 * (WIDE * 2 + 16) + (col + lane / 32 * 4) * 2) = w;
+}
+// Writes what is staged to rows from r on, columns from c on.
+template <class T, int WIDE>
+__device__ __forceinline__ void flush_bits(const char* s, char* out, int64_t ld, int64_t r, int64_t rows, int64_t c,
+                                           int64_t cols) {
+  constexpr u32 kLanes = WIDE / 8;  // of a row
+  const u32 lane = threadIdx.x & 63;
+  const int64_t col = c + lane % kLanes * 8;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (u32 i = 0; i < 32; i += 64 / kLanes) {
+    const u32 row = i + lane / kLanes;
+    const vec4 q = *reinterpret_cast<const vec4*>(s + row * (WIDE * 2 + 16) + lane % kLanes * 16);
+    if (r + row >= rows || col >= cols) continue;
+    char* const p = out + (r + row) * ld + col * T::bytes;
+    const u32 n = (u32)min(cols - col, (int64_t)8);
+    if (n == 8) {
+      *reinterpret_cast<vec4_any*>(p) = q;
+    } else {
+      u32 w[4] = {q[0], q[1], q[2], q[3]};
+      store_bits<T::bytes, 4>(p, w, n);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ void stage_floats(char* s, u32 col, f32x4 v) {
+  const u32 lane = threadIdx.x & 63;
+  *reinterpret_cast<f32x4*>(s + lane % 32 * 144 + (col + lane / 32 * 4) * 4) = v;
+}
+// The weight gradient's results, added to what is there where asked.
+__device__ __forceinline__ void flush_floats(const char* s, const ProductLaunch& a, int which, int64_t r, int64_t c) {
+  const u32 lane = threadIdx.x & 63;
+  const int64_t col = c + lane % 8 * 4;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (u32 i = 0; i < 32; i += 8) {
+    const u32 row = i + lane / 8;
+    const f32x4 q = *reinterpret_cast<const f32x4*>(s + row * 144 + lane % 8 * 16);
+    if (r + row >= a.rows || col >= a.cols) continue;
+    const float v[4] = {q[0], q[1], q[2], q[3]};
+    finish4<BF16, kWeight>(a, which, r + row, col, v, (u32)min(a.cols - col, (int64_t)4));
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Stages a block's codes and stores its scales.  The block's columns begin at c, at `at` of what is staged.
+template <int WIDE>
+__device__ __forceinline__ void hold_block(char* s, const Held& h, const f32x16& v, int64_t r, int64_t rows, int64_t c, u32 at,
+                                           int64_t cols) {
+  const u32 lane = threadIdx.x & 63;
+  float f[16];
+  const int64_t left = cols - c - lane / 32 * 4;  // columns beyond the last hold what the tile read there
+  u32 top = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    f[j] = j / 4 * 8 + j % 4 < left ? v[j] : 0.0f;
+    top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+  }
+  if (__builtin_amdgcn_ballot_w64(top >= 0x7f800000u)) {  // infinities and NaN
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      top = max(top, finite_magnitude(f[j]));
+      f[j] = held_input(f[j]);
+    }
+  }
+  top = max(top, (u32)__shfl_xor((int)top, 32, 64));
+  const u32 scale = scale_of(top);
+  const float inv = inverse_scale(scale);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<u32*>(s + lane % 32 * (WIDE + 16) + at + 8 * j + lane / 32 * 4) = codes4_finite(f + 4 * j, inv);
+  if (lane < 32 && r + lane < rows && c < cols) h.scales[(r + lane) * h.ld_scales + c / kBlock] = (char)scale;
+}
+template <int WIDE>
+__device__ __forceinline__ void flush_codes(const char* s, const Held& h, int64_t r, int64_t rows, int64_t c, int64_t cols) {
+  constexpr u32 kLanes = WIDE / 16;
+  const u32 lane = threadIdx.x & 63;
+  const int64_t col = c + lane % kLanes * 16;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (u32 i = 0; i < 32; i += 64 / kLanes) {
+    const u32 row = i + lane / kLanes;
+    if (row >= 32) continue;
+    const vec4 q = *reinterpret_cast<const vec4*>(s + row * (WIDE + 16) + lane % kLanes * 16);
+    if (r + row >= rows || col >= cols) continue;
+    char* const p = h.codes + (r + row) * h.ld_codes + col;
+    const u32 n = (u32)min(cols - col, (int64_t)16);
+    if (n == 16) {
+      *reinterpret_cast<vec4_byte*>(p) = q;
+    } else {
+      u32 w[4] = {q[0], q[1], q[2], q[3]};
+      store_bits<1, 8>(p, w, n);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+// ---------------------------------------------------------------------------
 // 16-bit types at multiples of 16 bytes
 // ---------------------------------------------------------------------------
 
@@ -231,7 +349,6 @@ __global__ __launch_bounds__(256) void product_kernel(const ProductLaunch a, int
 // left out before every odd pair of rows.  Either way the 4 rows lie in different banks.
 // The DMA writes LDS in lane order, 1024 bytes a wave, so a lane fetches the unit that belongs
 // at its place.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 constexpr int kStep = 32;
@@ -401,7 +518,7 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   tile_of(blockIdx.x, down * halves, across, tr, tc);
   const int which = KIND == kWeight && tr >= down;
   const int64_t r0 = (int64_t)(tr - which * down) * TILE, c0 = (int64_t)tc * kCols;
-  const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const u32 wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const u32 wc = wave % WC, wr = wave / WC;
 
   constexpr int kRP = kRounds<kPByK>, kRQ = kRounds<kQByK>;
@@ -555,56 +672,72 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
     }
   }
 
-  const ProductLaunch& b = argument<ProductLaunch>();
+  // A block's results lie across the lanes by rows, four columns a lane: stored as they are, each store of
+  // a wave would touch 32 rows by 16 bytes.  They go through LDS, where the copies no longer need it, and
+  // leave by whole rows of the wave's columns.
+  constexpr u32 kOf = kPByK ? 2 : 4, kEach = WC * WR / kOf;
+  const u32 slot = wave / kEach;
+  char* at_slot = slot == 0 ? p0 : p1;
+  if constexpr (!kPByK) at_slot = slot == 2 ? p2 : slot == 3 ? p3 : at_slot;
+  char* const mine = at_slot + wave % kEach * kStageBytes;
 #pragma unroll
   for (int y = 0; y < YB; ++y) {
-    const int64_t r = r0 + (wr * YB + y) * 32 + lane % 32;
+    const int64_t r = r0 + (wr * YB + y) * 32;
+    const ProductLaunch& b = argument<ProductLaunch>();
     if constexpr (KIND == kForward) {
+      constexpr int XG = XB / 2, kWide = XG * 32;
+      const int64_t c = c0 + wc * kWide;
 #pragma unroll
-      for (int x = 0; x < XB / 2; ++x) {
-        const int64_t c = c0 + (wc * (XB / 2) + x) * 32 + lane / 32 * 4;  // + 8 j: groups of four
-        u32 scale[2] = {0, 0};
-        if (b.held[0].codes) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            u32 top = 0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j / 4 * 8 + j % 4 < b.cols) top = max(top, finite_magnitude(acc[x + i * (XB / 2)][y][j]));
-            top = max(top, (u32)__shfl_xor((int)top, 32, 64));
-            scale[i] = scale_of(top);
-          }
-        }
+      for (int x = 0; x < XG; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int64_t at = c + 8 * j;
-          if (r >= b.rows || at >= b.cols) continue;
-          const u32 n = (u32)min(b.cols - at, (int64_t)4);
-          float v[2][4];
+          float v[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = acc[x + i * (XB / 2)][y][4 * j + e];
-          finish_gated4<T>(b, r, at, v[0], v[1], n);
-          if (b.held[0].codes) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              store_codes4(b.held[i], r, at, v[i], scale[i], n);
-              if (at % kBlock == 0) b.held[i].scales[r * b.held[i].ld_scales + at / kBlock] = (char)scale[i];
-            }
-          }
+          for (int e = 0; e < 4; ++e) v[e] = gated_value(b.act, acc[x][y][4 * j + e], acc[x + XG][y][4 * j + e]);
+          stage_bits<T, kWide>(mine, x * 32 + 8 * j, v);
         }
+      flush_bits<T, kWide>(mine, b.out[0], b.ld_out[0], r, b.rows, c, b.cols);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const ProductLaunch& b = argument<ProductLaunch>();
+        if (b.kept[0]) {
+#pragma unroll
+          for (int x = 0; x < XG; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float v[4] = {acc[x + i * XG][y][4 * j], acc[x + i * XG][y][4 * j + 1], acc[x + i * XG][y][4 * j + 2],
+                                  acc[x + i * XG][y][4 * j + 3]};
+              stage_bits<T, kWide>(mine, x * 32 + 8 * j, v);
+            }
+          flush_bits<T, kWide>(mine, b.kept[i], b.ld_kept[i], r, b.rows, c, b.cols);
+        }
+        if (b.held[0].codes) {
+#pragma unroll
+          for (int x = 0; x < XG; ++x) hold_block<kWide>(mine, b.held[i], acc[x + i * XG][y], r, b.rows, c + 32 * x, 32 * x, b.cols);
+          flush_codes<kWide>(mine, b.held[i], r, b.rows, c, b.cols);
+        }
+      }
+    } else if constexpr (KIND == kInput) {
+      constexpr int kWide = 64;
+#pragma unroll
+      for (int x = 0; x < XB; x += 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float v[4] = {acc[x + i][y][4 * j], acc[x + i][y][4 * j + 1], acc[x + i][y][4 * j + 2], acc[x + i][y][4 * j + 3]};
+            stage_bits<T, kWide>(mine, i * 32 + 8 * j, v);
+          }
+        flush_bits<T, kWide>(mine, b.out[0], b.ld_out[0], r, b.rows, c0 + (wc * XB + x) * 32, b.cols);
       }
     } else {
 #pragma unroll
-      for (int x = 0; x < XB; ++x)
+      for (int x = 0; x < XB; ++x) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t at = c0 + (wc * XB + x) * 32 + lane / 32 * 4 + 8 * j;
-          if (r >= b.rows || at >= b.cols) continue;
-          const float v[4] = {acc[x][y][4 * j], acc[x][y][4 * j + 1], acc[x][y][4 * j + 2], acc[x][y][4 * j + 3]};
-          finish4<T, KIND>(b, which, r, at, v, (u32)min(b.cols - at, (int64_t)4));
-        }
+        for (int j = 0; j < 4; ++j)
+          stage_floats(mine, 8 * j, f32x4{acc[x][y][4 * j], acc[x][y][4 * j + 1], acc[x][y][4 * j + 2], acc[x][y][4 * j + 3]});
+        flush_floats(mine, b, which, r, c0 + (wc * XB + x) * 32);
+      }
     }
   }
 }

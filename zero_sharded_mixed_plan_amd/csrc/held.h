@@ -10,6 +10,7 @@ namespace zk {
 namespace {
 
 typedef vec2 vec2_byte __attribute__((aligned(1)));  // at any address
+typedef vec4 vec4_byte __attribute__((aligned(1)));
 
 typedef u32 u32_byte __attribute__((aligned(1)));
 typedef uint16_t u16_byte __attribute__((aligned(1)));
@@ -64,6 +65,22 @@ __device__ __forceinline__ void values8(const Raw8<T>& r, u32 n, float v[8]) {
   for (int i = 0; i < 2 * T::bytes; ++i) x.w[i] = r.w[i];
   widen<T, 8>(x, v);
   clear_tail(v, n);
+}
+
+// The first n of 4 elements at p, of a type known when the kernel runs; zeros behind them.
+__device__ __forceinline__ void load4_as(const char* p, int type, u32 n, float v[4]) {
+  if (n < 4) {
+#pragma unroll
+    for (u32 j = 0; j < 4; ++j) v[j] = j < n ? load_one(p + j * one_bytes(type), type) : 0.0f;
+  } else if (type == ZERO_F32) {
+    const vec4 q = *reinterpret_cast<const vec4_any*>(p);
+    const Raw<F32, 4> r = {{q[0], q[1], q[2], q[3]}};
+    widen<F32, 4>(r, v);
+  } else {
+    const vec2 q = *reinterpret_cast<const vec2_any*>(p);
+    if (type == ZERO_BF16) widen<BF16, 4>(Raw<BF16, 4>{{q[0], q[1]}}, v);
+    else widen<F16, 4>(Raw<F16, 4>{{q[0], q[1]}}, v);
+  }
 }
 
 // The first n < 2 K elements of the N words w, by the bits K, K / 2 .. 1 of n.
@@ -193,24 +210,41 @@ __device__ __forceinline__ u32 finite_magnitude(float v) {
 __device__ __forceinline__ float held_input(float v) {
   return finite_bits(__float_as_uint(v)) ? v : __uint_as_float(0x7fc00000u);
 }
-// four codes; the conversion rounds to nearest, ties to even, and nothing is past 448
+// Four codes of values that are finite or NaN.  The conversion rounds to nearest, ties to even, and nothing is past 448.
+__device__ __forceinline__ u32 codes4_finite(const float* v, float inv) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+  return (u32)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
+}
+// Four codes of any values.
 __device__ __forceinline__ u32 codes4(const float* v, float inv) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(held_input(v[0]) * inv, held_input(v[1]) * inv, 0, false);
-  return (u32)__builtin_amdgcn_cvt_pk_fp8_f32(held_input(v[2]) * inv, held_input(v[3]) * inv, w, true);
+  const float f[4] = {held_input(v[0]), held_input(v[1]), held_input(v[2]), held_input(v[3])};
+  return codes4_finite(f, inv);
 }
 
 // Holds 8 columns of a row; the four lanes of a quad have one block's 32 columns, and
 // all of them take part.  Values behind the n-th are zeros.
-__device__ __forceinline__ void hold8(const Held& h, int64_t row, u32 group, const float v[8], u32 n) {
+__device__ __forceinline__ void hold8(const Held& h, int64_t row, u32 group, const float x[8], u32 n) {
   u32 top = 0;
+  float v[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, finite_magnitude(v[j]));
+  for (int j = 0; j < 8; ++j) {
+    v[j] = x[j];
+    top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  }
+  if (__builtin_amdgcn_ballot_w64(top >= 0x7f800000u)) {  // infinities and NaN
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top = max(top, finite_magnitude(v[j]));
+      v[j] = held_input(v[j]);
+    }
+  }
   top = max(top, (u32)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xF, 0xF, true));  // quad_perm [1, 0, 3, 2]
   top = max(top, (u32)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xF, 0xF, true));  // quad_perm [2, 3, 0, 1]
   if (n == 0) return;
   const u32 s = scale_of(top);
   const float inv = inverse_scale(s);
-  const u32 lo = codes4(v, inv), hi = codes4(v + 4, inv);
+  const u32 lo = codes4_finite(v, inv), hi = codes4_finite(v + 4, inv);
   char* p = h.codes + row * h.ld_codes + (int64_t)group * 8;
   if (n == 8) {
     const vec2 q = {lo, hi};
