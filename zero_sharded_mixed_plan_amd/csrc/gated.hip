@@ -742,6 +742,171 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   }
 }
 
+// ---------------------------------------------------------------------------
+// a few tokens
+// ---------------------------------------------------------------------------
+
+// Every weight is read once, and what counts is the bytes in flight and that all CUs have a like share
+// of them.  A workgroup has COLS columns of gate and of up, 16 or 32 (a block, where they are held in 8 bits); its waves take turns of 64 of k and work alone: each copies its
+// turns' weights and tokens into LDS, whole lines, RING turns ahead, and waits for no other wave before its
+// sums are added to theirs.  Weights loaded straight into the registers that the matrix
+// instructions take them from, 16 bytes of every row a lane, reached half of the bandwidth: each
+// lane of such a load is a line of its own to the L1.  TOKENS: a multiple of 16.
+template <class T>
+__device__ __forceinline__ f32x4 mfma16(i16x8 p, i16x8 q, f32x4 acc) {
+  if constexpr (std::is_same<T, BF16>::value)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), acc, 0, 0, 0);
+}
+
+template <class T, int TOKENS, int COLS, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void few_kernel(const ProductLaunch a) {
+  constexpr int N = TOKENS / 16, H = COLS / 16, kRing = N <= 2 ? 3 : 2;
+  constexpr int kTurnBytes = (2 * COLS + TOKENS) * 128;  // rows of gate, of up, of tokens
+  constexpr int kCopies = kTurnBytes / 1024;
+  __shared__ __attribute__((aligned(128))) char s0[WAVES * kTurnBytes], s1[WAVES * kTurnBytes],
+      s2[kRing > 2 ? WAVES * kTurnBytes : 16];
+  const u32 lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t c0 = (int64_t)blockIdx.x * COLS;
+  // Chunk i of 8 rows: lane l fetches the unit of row 8 i + l / 8 whose place is l % 8 (unit j of row r at
+  // j ^ (r / 2 % 8)).  Rows beyond the last stand for it.
+  u32 off[COLS / 8], off_x[2 * N];
+#pragma unroll
+  for (u32 i = 0; i < COLS / 8; ++i)
+    off[i] = (u32)min((int64_t)(8 * i + lane / 8), a.cols - 1 - c0) * (u32)a.ld_p[0] + ((lane % 8) ^ ((4 * i + lane / 16) % 8)) * 16;
+#pragma unroll
+  for (u32 i = 0; i < 2 * N; ++i)
+    off_x[i] = (u32)min((int64_t)(8 * i + lane / 8), a.rows - 1) * (u32)a.ld_q[0] + ((lane % 8) ^ ((4 * i + lane / 16) % 8)) * 16;
+  u32 at = wave * kTurnBytes + lane % 16 * 128 + ((lane / 16) ^ (lane / 2 % 8)) * 16;  // 16 rows further: + 2048
+  asm("" : "+v"(at));
+
+  auto copy = [&](char* slot, int64_t u) {
+    const int64_t left = a.k - u * 64;
+    auto start = [&](auto is_part) {
+      auto one = [&](__amdgpu_buffer_rsrc_t from, u32 from_off, u32 i, u32 chunk) {
+        char* const to = slot + wave * kTurnBytes + chunk * 1024;
+        if (!decltype(is_part)::value || (int64_t)(((lane % 8) ^ ((4 * i + lane / 16) % 8)) * 8) < left)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, from_off, 0, 0, 0);
+        else
+          *reinterpret_cast<vec4*>(to + lane * 16) = vec4{0, 0, 0, 0};  // beyond the end of k
+      };
+#pragma unroll
+      for (u32 m = 0; m < 2; ++m)
+#pragma unroll
+        for (u32 i = 0; i < COLS / 8; ++i) one(buffer_at(a.p[m] + c0 * a.ld_p[0] + u * 128), off[i], i, COLS / 8 * m + i);
+#pragma unroll
+      for (u32 i = 0; i < 2 * N; ++i) one(buffer_at(a.q[0] + u * 128), off_x[i], i, COLS / 4 + i);
+    };
+    if (left >= 64) start(std::false_type{});
+    else start(std::true_type{});
+  };
+  f32x4 acc[2][H][N] = {};
+  // this wave's turns are 64 of k from 64 (wave + WAVES i) on
+  const int64_t all = (a.k + 63) / 64, turns = (all - wave + WAVES - 1) / WAVES;
+  const int64_t whole = (a.k / 64 - wave + WAVES - 1) / WAVES;  // of them without an end of k inside
+  auto turn = [&](char* slot, int64_t i) {
+    if (i >= turns) return;
+    // the ring's other turns may be under way still; one with an end of k inside starts fewer copies
+    if (i + kRing - 1 < whole) __builtin_amdgcn_s_waitcnt(0x70 | ((kRing - 1) * kCopies & 15) | ((kRing - 1) * kCopies >> 4) << 14);
+    else __builtin_amdgcn_s_waitcnt(0x70);
+    i16x8 w[2][H][2], x[N][2];
+#pragma unroll
+    for (u32 s = 0; s < 2; ++s) {
+#pragma unroll
+      for (u32 m = 0; m < 2; ++m)
+#pragma unroll
+        for (u32 h = 0; h < H; ++h) w[m][h][s] = *reinterpret_cast<const i16x8*>(slot + ((at ^ (s * 64)) + (H * m + h) * 2048));
+#pragma unroll
+      for (int t = 0; t < N; ++t) x[t][s] = *reinterpret_cast<const i16x8*>(slot + ((at ^ (s * 64)) + (2 * H + t) * 2048));
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what was read may be written over
+    asm volatile("" ::: "memory");
+    if (i + kRing < turns) copy(slot, wave + WAVES * (i + kRing));
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < N; ++t)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int h = 0; h < H; ++h) acc[m][h][t] = mfma16<T>(w[m][h][s], x[t][s], acc[m][h][t]);
+  };
+  if (0 < turns) copy(s0, wave);
+  if (1 < turns) copy(s1, wave + WAVES);
+  if (kRing > 2 && 2 < turns) copy(s2, wave + 2 * WAVES);
+#pragma unroll 1
+  for (int64_t i = 0; i < turns; i += kRing) {
+    turn(s0, i);
+    turn(s1, i + 1);
+    if constexpr (kRing > 2) turn(s2, i + 2);
+  }
+
+  // sums [wave][gate or up][token][column]
+  static_assert(2 * TOKENS * COLS * 4 <= kTurnBytes, "the sums fit where the copies were");
+  float* const sums = reinterpret_cast<float*>(s0);
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        *reinterpret_cast<f32x4*>(sums + ((wave * 2 + m) * TOKENS + 16 * t + lane % 16) * COLS + 16 * h + lane / 16 * 4) = acc[m][h][t];
+  __syncthreads();
+  // four columns a thread
+#pragma unroll 1
+  for (u32 e = threadIdx.x; e < TOKENS * (COLS / 4); e += WAVES * 64) {
+    const u32 t = e / (COLS / 4), col = e % (COLS / 4) * 4;
+    const int64_t c = c0 + col;
+    const u32 n = c < a.cols ? (u32)min(a.cols - c, (int64_t)4) : 0;
+    float v[2][4];
+#pragma unroll
+    for (u32 m = 0; m < 2; ++m) {
+      f32x4 f = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (u32 k = 0; k < WAVES; ++k) f += *reinterpret_cast<const f32x4*>(sums + ((k * 2 + m) * TOKENS + t) * COLS + col);
+#pragma unroll
+      for (u32 j = 0; j < 4; ++j) v[m][j] = j < n ? f[j] : 0.0f;
+    }
+    if (COLS == kBlock && a.held[0].codes) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        u32 top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, finite_magnitude(v[m][j]));
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) top = max(top, (u32)__shfl_xor((int)top, d, 64));
+        if (t >= a.rows || n == 0) continue;
+        const u32 scale = scale_of(top);
+        store_codes4(a.held[m], t, c, v[m], scale, n);
+        if (col == 0) a.held[m].scales[t * a.held[m].ld_scales + c / kBlock] = (char)scale;
+      }
+    }
+    if (t < a.rows && n > 0) finish_gated4<T>(a, t, c, v[0], v[1], n);
+  }
+}
+
+template <class T, int TOKENS>
+int few_as(const ProductLaunch& a, hipStream_t s) {
+  auto go = [&](auto columns, auto waves) {
+    constexpr int C = decltype(columns)::value, W = decltype(waves)::value;
+    hipLaunchKernelGGL((few_kernel<T, TOKENS, C, W>), dim3((u32)((a.cols + C - 1) / C)), dim3(W * 64), 0, s, a);
+  };
+  using Two = std::integral_constant<int, 2>;
+  using Four = std::integral_constant<int, 4>;
+  const bool many = a.cols > 16 * 512;  // more than two workgroups a CU
+  // With 64 tokens their rows are more than the weights' of 16 columns (64 tokens, 4096 x 14336
+  // 58 us with 32 columns, 69 with 16; 16 tokens 48 and 47, 4096 x 11008 45 and 37.5).
+  if (TOKENS == 64 || a.held[0].codes) {
+    a.cols > 32 * 256 ? go(std::integral_constant<int, 32>{}, Two{}) : go(std::integral_constant<int, 32>{}, Four{});
+  } else if constexpr (TOKENS < 64) {
+    many ? go(std::integral_constant<int, 16>{}, Two{}) : go(std::integral_constant<int, 16>{}, Four{});
+  }
+  return launched("gated projections");
+}
+
 // Whether the copies of 16 bytes find whole units: addresses, strides, and the lengths
 // along which an operand's rows lie.  Offsets within a tile are 32 bits.
 bool tiles_fit(Product kind, const ProductLaunch& a) {
@@ -767,6 +932,11 @@ int tiled_as(const ProductLaunch& a, hipStream_t s) {
 
 template <class T, Product KIND>
 int tiled_of(const ProductLaunch& a, hipStream_t s) {
+  if constexpr (KIND == kForward) {
+    if (a.rows <= 16) return few_as<T, 16>(a, s);
+    if (a.rows <= 32) return few_as<T, 32>(a, s);
+    if (a.rows <= 64) return few_as<T, 64>(a, s);
+  }
   constexpr int64_t cols = KIND == kForward ? 128 : 256;
   const int64_t big = (a.rows + 255) / 256 * ((a.cols + cols - 1) / cols) * (KIND == kWeight ? 2 : 1);
   return big >= 192 ? tiled_as<T, KIND, 256>(a, s) : tiled_as<T, KIND, 128>(a, s);
