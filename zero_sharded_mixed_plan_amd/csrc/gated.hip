@@ -276,6 +276,20 @@ __device__ __forceinline__ void flush_floats(const char* s, const ProductLaunch&
   __builtin_amdgcn_wave_barrier();
 }
 
+// A split's sums, dense, `out` at row r; cols is a multiple of 8.
+__device__ __forceinline__ void flush_partial(const char* s, float* out, int64_t r, int64_t rows, int64_t c, int64_t cols) {
+  const u32 lane = threadIdx.x & 63;
+  const int64_t col = c + lane % 8 * 4;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (u32 i = 0; i < 32; i += 8) {
+    const u32 row = i + lane / 8;
+    const f32x4 q = *reinterpret_cast<const f32x4*>(s + row * 144 + lane % 8 * 16);
+    if (r + row < rows && col < cols) *reinterpret_cast<f32x4*>(out + row * cols + col) = q;
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Stages a block's codes and stores its scales.  The block's columns begin at c, at `at` of what is staged.
 template <int WIDE>
 __device__ __forceinline__ void hold_block(char* s, const Held& h, const f32x16& v, int64_t r, int64_t rows, int64_t c, u32 at,
@@ -501,7 +515,7 @@ __device__ __forceinline__ void tile_of(u32 b, u32 down, u32 across, u32& r, u32
 }
 
 template <class T, Product KIND, int TILE>
-__global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const ProductLaunch a, u32 down, u32 across) {
+__global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const ProductLaunch a, u32 down, u32 across, u32 splits) {
   constexpr bool kQByK = KIND != kWeight, kPByK = KIND == kForward;
   constexpr int WC = 2, WR = TILE == 256 ? 4 : 2;
   constexpr int XB = TILE / WC / 32, YB = TILE / WR / 32;
@@ -515,7 +529,8 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   __shared__ __attribute__((aligned(128))) char p0[kEight ? kP + kQ : kP], q0[kEight ? 16 : kQ];
   u32 tr, tc;
   const u32 halves = KIND == kWeight ? 2 : 1;
-  tile_of(blockIdx.x, down * halves, across, tr, tc);
+  const u32 split = KIND == kForward ? 0 : blockIdx.x / (down * halves * across);
+  tile_of(KIND == kForward ? blockIdx.x : blockIdx.x % (down * halves * across), down * halves, across, tr, tc);
   const int which = KIND == kWeight && tr >= down;
   const int64_t r0 = (int64_t)(tr - which * down) * TILE, c0 = (int64_t)tc * kCols;
   const u32 wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -542,14 +557,23 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   struct Fragments {
     i16x8 p[kStep / 16][XB], q[kStep / 16][YB];
   };
-  const u32 steps = (u32)((a.k + kStep - 1) / kStep), whole = (u32)(a.k / kStep);
-  for (int part = 0; part < (KIND == kInput ? 2 : 1); ++part) {
-    const int iq = KIND == kWeight ? which : part, ip = KIND == kInput ? part : 0;
+  // a split has a run of the 64s of k, in the input gradient of gate's and then up's
+  constexpr u32 kParts = KIND == kInput ? 2 : 1;
+  const u32 units = (u32)((a.k + 63) / 64);
+  const u32 from = (u32)((u64)units * kParts * split / splits), to = (u32)((u64)units * kParts * (split + 1) / splits);
+  for (u32 part = 0; part < kParts; ++part) {
+    const u32 lo = max(from, part * units) - part * units, hi = min(to, (part + 1) * units) - part * units;
+    if (KIND != kForward && (from >= (part + 1) * units || to <= part * units)) continue;
+    const int64_t k_lo = KIND == kForward ? 0 : (int64_t)lo * 64;
+    const int k = (int)((KIND == kForward ? a.k : min(a.k, (int64_t)hi * 64)) - k_lo);
+    const u32 steps = (u32)(k + kStep - 1) / kStep, whole = (u32)k / kStep;
+    const u32 iq = KIND == kWeight ? which : part, ip = KIND == kInput ? part : 0;
     // where the next copies begin, how far a copy goes, and what is left of k there
-    const char* next_q = a.q[iq] + (kQByK ? r0 * a.ld_q[0] : r0 * 2);
-    const char* next_p[2] = {a.p[ip] + (kPByK ? c0 * a.ld_p[0] : c0 * 2), KIND == kForward ? a.p[1] + c0 * a.ld_p[0] : nullptr};
+    const char* next_q = a.q[iq] + (kQByK ? r0 * a.ld_q[0] + k_lo * 2 : k_lo * a.ld_q[0] + r0 * 2);
+    const char* next_p[2] = {a.p[ip] + (kPByK ? c0 * a.ld_p[0] + k_lo * 2 : k_lo * a.ld_p[0] + c0 * 2),
+                             KIND == kForward ? a.p[1] + c0 * a.ld_p[0] : nullptr};
     const int64_t far_q = kDeep<kQByK> * (kQByK ? 2 : a.ld_q[0]), far_p = kDeep<kPByK> * (kPByK ? 2 : a.ld_p[0]);
-    int left_p = (int)a.k, left_q = (int)a.k;
+    int left_p = k, left_q = k;
     auto copy_p = [&](char* to, auto all_whole) {
       auto start = [&](auto is_part) {
 #pragma unroll
@@ -716,6 +740,15 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
           for (int x = 0; x < XG; ++x) hold_block<kWide>(mine, b.held[i], acc[x + i * XG][y], r, b.rows, c + 32 * x, 32 * x, b.cols);
           flush_codes<kWide>(mine, b.held[i], r, b.rows, c, b.cols);
         }
+      }
+    } else if (splits > 1) {  // fp32, for join_kernel
+      const int64_t at = ((int64_t)(split * halves + which) * b.rows + r) * b.cols;
+#pragma unroll
+      for (int x = 0; x < XB; ++x) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          stage_floats(mine, 8 * j, f32x4{acc[x][y][4 * j], acc[x][y][4 * j + 1], acc[x][y][4 * j + 2], acc[x][y][4 * j + 3]});
+        flush_partial(mine, b.ws + at, r, b.rows, c0 + (wc * XB + x) * 32, b.cols);
       }
     } else if constexpr (KIND == kInput) {
       constexpr int kWide = 64;
@@ -921,12 +954,66 @@ bool tiles_fit(Product kind, const ProductLaunch& a) {
   return (q_by_k ? a.k : a.rows) % 8 == 0 && (p_by_k ? a.k : a.cols) % 8 == 0;
 }
 
+// Adds the splits' sums, four columns a thread, in their order.
+template <class T, Product KIND>
+__global__ __launch_bounds__(256) void join_kernel(const ProductLaunch a, u32 splits) {
+  const int64_t each = a.rows * a.cols, all = each * (KIND == kWeight ? 2 : 1);
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all; i += (int64_t)gridDim.x * 1024) {
+    const int which = i >= each;
+    const int64_t r = (i - which * each) / a.cols, c = (i - which * each) % a.cols;
+    f32x4 sum = *reinterpret_cast<const f32x4*>(a.ws + i);
+#pragma unroll 4
+    for (u32 s = 1; s < splits; ++s) sum += *reinterpret_cast<const f32x4*>(a.ws + s * all + i);
+    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    finish4<T, KIND>(a, which, r, c, v, 4);
+  }
+}
+
+// The size of the tiles and the number of splits of k.  Few tiles leave CUs without work; splits of a long k
+// give it to them, at the price of fp32 partial results that are written and read once more.  The
+// estimate is of microseconds, from these measurements: 64 of k take a tile of 256 1.5, of
+// 128 0.4 alone on a CU and 0.95 where two share it (the 8192 x 4096 x 14336 forward pass 1498 us with
+// tiles of 256, 1873 with 128); a tile begins and ends in 8 and 5; partial results move at 5 TB/s,
+// and another launch takes 3.
+struct TilePlan {
+  int tile;
+  u32 splits;
+};
+constexpr u32 kMaxSplits = 16;
+constexpr int64_t kMaxPartialBytes = int64_t(64) << 20;
+
+TilePlan tile_plan(Product kind, const ProductLaunch& a) {
+  const int64_t halves = kind == kWeight ? 2 : 1, units = (a.k + 63) / 64 * (kind == kInput ? 2 : 1);
+  const int64_t bytes = halves * a.rows * a.cols * 4;
+  TilePlan best{128, 1};
+  double least = 1e300;
+  for (int tile : {128, 256}) {
+    const int64_t cols = kind == kForward ? tile / 2 : tile;
+    const int64_t tiles = (a.rows + tile - 1) / tile * ((a.cols + cols - 1) / cols) * halves;
+    for (u32 n = 1; n <= kMaxSplits; ++n) {
+      if (n > 1 && (kind == kForward || units / n < 4 || bytes > kMaxPartialBytes / n || a.cols % 8 != 0)) break;
+      const int64_t groups = tiles * n;
+      double each, begin, rounds;
+      if (tile == 256) each = 1.5, begin = 8.0, rounds = (double)((groups + 255) / 256);
+      else if (groups <= 256) each = 0.4, begin = 5.0, rounds = 1.0;
+      else each = 0.95, begin = 5.0, rounds = (double)((groups + 511) / 512);
+      double t = rounds * (each * (double)units / n + begin);
+      if (n > 1) t += 3.0 + 2.0 * n * (double)bytes / 5e6;
+      if (t < least) {
+        least = t;
+        best = TilePlan{tile, n};
+      }
+    }
+  }
+  return best;
+}
+
 template <class T, Product KIND, int TILE>
-int tiled_as(const ProductLaunch& a, hipStream_t s) {
+int tiled_as(const ProductLaunch& a, u32 splits, hipStream_t s) {
   constexpr int cols = KIND == kForward ? TILE / 2 : TILE;
   const u32 down = (u32)((a.rows + TILE - 1) / TILE), across = (u32)((a.cols + cols - 1) / cols);
-  hipLaunchKernelGGL((tiled_kernel<T, KIND, TILE>), dim3(down * across * (KIND == kWeight ? 2 : 1)), dim3(kTileThreads<TILE>), 0,
-                     s, a, down, across);
+  hipLaunchKernelGGL((tiled_kernel<T, KIND, TILE>), dim3(down * across * (KIND == kWeight ? 2 : 1) * splits),
+                     dim3(kTileThreads<TILE>), 0, s, a, down, across, splits);
   return launched(KIND == kForward ? "gated projections" : KIND == kInput ? "gated input gradient" : "gated weight gradient");
 }
 
@@ -937,9 +1024,17 @@ int tiled_of(const ProductLaunch& a, hipStream_t s) {
     if (a.rows <= 32) return few_as<T, 32>(a, s);
     if (a.rows <= 64) return few_as<T, 64>(a, s);
   }
-  constexpr int64_t cols = KIND == kForward ? 128 : 256;
-  const int64_t big = (a.rows + 255) / 256 * ((a.cols + cols - 1) / cols) * (KIND == kWeight ? 2 : 1);
-  return big >= 192 ? tiled_as<T, KIND, 256>(a, s) : tiled_as<T, KIND, 128>(a, s);
+  const TilePlan plan = tile_plan(KIND, a);
+  if (int rc = plan.tile == 256 ? tiled_as<T, KIND, 256>(a, plan.splits, s) : tiled_as<T, KIND, 128>(a, plan.splits, s)) return rc;
+  if constexpr (KIND != kForward) {
+    if (plan.splits > 1) {
+      const int64_t all = a.rows * a.cols * (KIND == kWeight ? 2 : 1);
+      hipLaunchKernelGGL((join_kernel<T, KIND>), dim3((u32)std::min<int64_t>((all + 1023) / 1024, 4096)), dim3(256), 0, s, a,
+                         plan.splits);
+      return launched("gated products (join)");
+    }
+  }
+  return ZERO_OK;
 }
 
 template <class T, Product KIND>
@@ -963,7 +1058,10 @@ int product_of(const ProductLaunch& a, zero_dtype_t t, hipStream_t s) {
 
 }  // namespace
 
-int64_t product_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
+int64_t product_ws_bytes(int64_t tokens, int64_t dim, int64_t hidden) {
+  const double most = 4.0 * kMaxSplits * (double)dim * (double)std::max(tokens, 2 * hidden);
+  return most < (double)kMaxPartialBytes ? (int64_t)most : kMaxPartialBytes;
+}
 
 int launch_product(Product kind, const ProductLaunch& a, zero_dtype_t t, void* stream) {
   switch (kind) {
