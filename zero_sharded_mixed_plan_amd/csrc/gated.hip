@@ -750,19 +750,25 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
           stage_floats(mine, 8 * j, f32x4{acc[x][y][4 * j], acc[x][y][4 * j + 1], acc[x][y][4 * j + 2], acc[x][y][4 * j + 3]});
         flush_partial(mine, b.ws + at, r, b.rows, c0 + (wc * XB + x) * 32, b.cols);
       }
-    } else if constexpr (KIND == kInput) {
+    } else if (KIND == kInput || (b.out_type != ZERO_F32 && !b.accumulate)) {  // rounded once, to 16 bits
       constexpr int kWide = 64;
+      auto store = [&](auto type) {
+        using O = decltype(type);
 #pragma unroll
-      for (int x = 0; x < XB; x += 2) {
+        for (int x = 0; x < XB; x += 2) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float v[4] = {acc[x + i][y][4 * j], acc[x + i][y][4 * j + 1], acc[x + i][y][4 * j + 2], acc[x + i][y][4 * j + 3]};
-            stage_bits<T, kWide>(mine, i * 32 + 8 * j, v);
-          }
-        flush_bits<T, kWide>(mine, b.out[0], b.ld_out[0], r, b.rows, c0 + (wc * XB + x) * 32, b.cols);
-      }
+            for (int j = 0; j < 4; ++j) {
+              const float v[4] = {acc[x + i][y][4 * j], acc[x + i][y][4 * j + 1], acc[x + i][y][4 * j + 2], acc[x + i][y][4 * j + 3]};
+              stage_bits<O, kWide>(mine, i * 32 + 8 * j, v);
+            }
+          flush_bits<O, kWide>(mine, b.out[which], b.ld_out[which], r, b.rows, c0 + (wc * XB + x) * 32, b.cols);
+        }
+      };
+      if constexpr (KIND == kInput) store(T{});
+      else if (b.out_type == ZERO_BF16) store(BF16{});
+      else store(F16{});
     } else {
 #pragma unroll
       for (int x = 0; x < XB; ++x) {
