@@ -12,15 +12,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// The kernel's first argument, read again where this stands: fields that only the end of
-// a kernel needs are not held in scalar registers through its loop.
-template <class L>
-__device__ __forceinline__ const L& argument() {
-  auto p = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return *(const L*)(const __attribute__((address_space(4))) L*)p;
-}
-
 // A result's four values of consecutive columns c .. c + 3 in row r; n of them exist.
 template <class T, Product KIND>
 __device__ __forceinline__ void finish4(const ProductLaunch& a, int which, int64_t r, int64_t c, const float v[4], u32 n) {

@@ -15,6 +15,15 @@ typedef vec4 vec4_byte __attribute__((aligned(1)));
 typedef u32 u32_byte __attribute__((aligned(1)));
 typedef uint16_t u16_byte __attribute__((aligned(1)));
 
+// The kernel's first argument, read again where this stands: fields that only the end of
+// a kernel needs are not held in scalar registers through its loop.
+template <class L>
+__device__ __forceinline__ const L& argument() {
+  auto p = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const L*)(const __attribute__((address_space(4))) L*)p;
+}
+
 // 8 elements of a row, raw
 template <class T>
 struct Raw8 {
@@ -24,12 +33,13 @@ struct Raw8 {
 // The n <= 8 elements at p that exist in the row; behind them anything.  Vectors where
 // 8 elements lie before `end`, the end of the tensor, else (its last few
 // elements, and tensors shorter than 8) one by one.
+// `inside`: a whole wave's answer that every vector lies before the end.
 template <class T>
-__device__ __forceinline__ void load8(const char* p, const char* end, u32 n, Raw8<T>& r) {
+__device__ __forceinline__ void load8(const char* p, const char* end, u32 n, Raw8<T>& r, bool inside = false) {
 #pragma unroll
   for (int i = 0; i < 2 * T::bytes; ++i) r.w[i] = 0;
   if (n == 0) return;
-  if (end - p >= 8 * T::bytes) {
+  if (inside || end - p >= 8 * T::bytes) {
 #pragma unroll
     for (int i = 0; i < T::bytes / 2; ++i) {
       const vec4 q = reinterpret_cast<const vec4_any*>(p)[i];
@@ -108,16 +118,25 @@ __device__ __forceinline__ void store_bits(char* p, u32 (&w)[N], u32 n) {
   if constexpr (K > 1) store_bits<BYTES, K / 2>(p, w, n);
 }
 
+// 8 values rounded to a type
+template <class T>
+__device__ __forceinline__ Raw8<T> round8(const float v[8]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < 2 * T::bytes; ++i) {
+    if constexpr (T::bytes == 4) r.w[i] = bits_of<T>(v[i]);
+    else r.w[i] = bits_of<T>(v[2 * i]) | bits_of<T>(v[2 * i + 1]) << 16;
+  }
+  return r;
+}
+
 // Stores n <= 8 values, not to be read again soon.
 template <class T>
-__device__ __forceinline__ void store8(char* p, const float v[8], u32 n) {
+__device__ __forceinline__ void store8(char* p, const Raw8<T>& r, u32 n) {
   constexpr int N = 2 * T::bytes;
   u32 w[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if constexpr (T::bytes == 4) w[i] = bits_of<T>(v[i]);
-    else w[i] = bits_of<T>(v[2 * i]) | bits_of<T>(v[2 * i + 1]) << 16;
-  }
+  for (int i = 0; i < N; ++i) w[i] = r.w[i];
   if (n == 8) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
@@ -128,6 +147,11 @@ __device__ __forceinline__ void store8(char* p, const float v[8], u32 n) {
     asm volatile("" : "+v"(n));
     store_bits<T::bytes, 4>(p, w, n);
   }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(char* p, const float v[8], u32 n) {
+  store8<T>(p, round8<T>(v), n);
 }
 
 // Stores the first n of 4 values.
@@ -261,11 +285,11 @@ __device__ __forceinline__ void hold8(const Held& h, int64_t row, u32 group, con
 struct RawHeld {
   u32 lo, hi, scale;
 };
-__device__ __forceinline__ void load_held(const Held& h, int64_t row, u32 group, u32 n, RawHeld& r) {
+__device__ __forceinline__ void load_held(const Held& h, int64_t row, u32 group, u32 n, RawHeld& r, bool inside = false) {
   r.lo = r.hi = r.scale = 0;
   if (n == 0) return;
   const char* p = h.codes + row * h.ld_codes + (int64_t)group * 8;
-  if (h.codes_end - p >= 8) {
+  if (inside || h.codes_end - p >= 8) {
     const vec2 q = *reinterpret_cast<const vec2_byte*>(p);
     r.lo = q.x;
     r.hi = q.y;

@@ -39,7 +39,7 @@ struct RmsLaunch {
   int64_t rows;
   uint32_t cols;
   int32_t weight_type, y_type;
-  double eps;
+  double eps, per_col;    // per_col: 1 / cols
 };
 
 struct RmsGradLaunch {

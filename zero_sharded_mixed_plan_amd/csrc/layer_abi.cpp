@@ -189,6 +189,7 @@ int rms(const zero_rms_args_t* args, void* stream) {
   a.rows = A.rows;
   a.cols = (uint32_t)A.cols;
   a.eps = A.eps;
+  a.per_col = 1.0 / (double)A.cols;
   return zk::launch_rms(a, A.x_dtype, res ? A.res_dtype : A.x_dtype, stream);
 }
 

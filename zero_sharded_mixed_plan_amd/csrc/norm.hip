@@ -5,10 +5,11 @@
 //   y = h * rstd * weight
 //
 // Bound by HBM: each element is read once and written once, a row's values wait in
-// registers for the row's sum.  The sum and y are computed in fp64, which on this
-// card costs a vector instruction no more than fp32 does: the 8-bit codes, where a last bit decides
-// which of two values 2^-4 apart is stored, then do not hang on the order of a
-// row's sum, and so not on how a row is split over lanes and waves.
+// registers for the row's sum.  In 8-bit codes a last bit decides which of two values 2^-4 apart is
+// stored, so rstd and y must not hang on how a row is split over lanes and waves: squares are summed in
+// fp64, and y is computed in pairs of fp32 numbers (good to 2^-44), rounded once to
+// fp32.  All in fp64, whose conversions are slow, 8192 x 4096 bf16 took 62 us with a
+// residual and codes, 36 without.
 #include <algorithm>
 
 #include "held.h"
@@ -16,85 +17,117 @@
 namespace zk {
 namespace {
 
-// A row is WAVES waves of C groups of 8 columns a lane.  Rows of one wave share a
-// workgroup of four, so that a workgroup's four waves never wait for each other there.
+// A row is WAVES waves of C times 8 columns a lane.  Short rows share a workgroup of four waves.
 constexpr int rms_threads(int waves) { return waves < 4 ? 256 : waves * 64; }
+
+// 1 / sqrt(x): the hardware's estimate and two of Newton's steps, each of which squares its error;
+// infinity for 0, 0 for infinity.
+__device__ __forceinline__ double inverse_root(double x) {
+  const double first = __builtin_amdgcn_rsq(x), half = -0.5 * x;
+  double r = first;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = __builtin_fma(r * 0.5, __builtin_fma(half * r, r + r, 1.0), r);
+  return x == 0.0 || first == 0.0 ? first : r;
+}
 
 template <class XT, class RT, int WAVES, int C, bool HELD>
 __global__ __launch_bounds__(rms_threads(WAVES)) void rms_kernel(const RmsLaunch a) {
   constexpr u32 kRow = WAVES * 64;
   constexpr u32 kRows = rms_threads(WAVES) / kRow;
-  const u32 t = threadIdx.x % kRow;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow; row < a.rows; row += (int64_t)gridDim.x * kRows) {
+  // a wave's row is a number of the wave, so that its addresses cost no vector instructions
+  const u32 t = kRows == 1 ? threadIdx.x : threadIdx.x % kRow;
+  const u32 mine = kRows == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kRow);
+  u32 n[C];
+  Raw8<F32> rw[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const u32 col = (c * kRow + t) * 8;
+    n[c] = col < a.cols ? min(a.cols - col, 8u) : 0;
+    if (a.weight) load8_as(a.weight + (int64_t)col * one_bytes(a.weight_type), a.weight_end, a.weight_type, n[c], rw[c]);
+  }
+  const int64_t stride = (int64_t)gridDim.x * kRows;
+  struct Row {
     Raw8<XT> x[C];
     Raw8<RT> r[C];
-    u32 n[C];
+  } next;
+  auto load = [&](int64_t row) {
+    if (row >= a.rows) return;
+    const bool inside = row + 1 < a.rows && a.cols >= 8;  // what follows a row is the next one
+    const char* const x = a.x + row * a.ld_x;
+    const char* const r = a.res + row * a.ld_res;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const u32 col = (c * kRow + t) * 8;
-      n[c] = col < a.cols ? min(a.cols - col, 8u) : 0;
-      asm volatile("" : "+v"(n[c]));  // no lane masks of it are kept across rows, in scalar registers
-      load8<XT>(a.x + row * a.ld_x + (int64_t)col * XT::bytes, a.x_end, n[c], x[c]);
-    }
-    if (a.res) {
+    for (int c = 0; c < C; ++c) load8<XT>(x + (c * kRow + t) * 8 * XT::bytes, a.x_end, n[c], next.x[c], inside);
+    if (!a.res) return;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const u32 col = (c * kRow + t) * 8;
-        load8<RT>(a.res + row * a.ld_res + (int64_t)col * RT::bytes, a.res_end, n[c], r[c]);
-      }
-    }
+    for (int c = 0; c < C; ++c) load8<RT>(r + (c * kRow + t) * 8 * RT::bytes, a.res_end, n[c], next.r[c], inside);
+  };
+  load((int64_t)blockIdx.x * kRows + mine);
+  u32 turn = 0;
+  // of several rows at a time, all go through the loop as often, for they meet at the barrier
+  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows; row0 += stride, ++turn) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(n[c]));  // no lane masks of it are kept across rows, in scalar registers
+    const int64_t row = row0 + mine;
+    const bool exists = kRows == 1 || row < a.rows;
+    const Row now = next;
+    load(row + stride);
     float h[C][8];
     double sum = 0.0;
+    if (exists) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      values8<XT>(x[c], n[c], h[c]);
-      if (a.res) {
-        float q[8];
-        values8<RT>(r[c], n[c], q);
+      for (int c = 0; c < C; ++c) {
+        values8<XT>(now.x[c], n[c], h[c]);
+        if (a.res) {
+          float q[8];
+          values8<RT>(now.r[c], n[c], q);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const u32 b = bits_of<RT>(h[c][j] + q[j]);
-          if constexpr (RT::bytes == 4) h[c][j] = __uint_as_float(b);
-          else if constexpr (std::is_same<RT, BF16>::value) h[c][j] = __uint_as_float(b << 16);
-          else h[c][j] = (float)__builtin_bit_cast(_Float16, (uint16_t)b);
+          for (int j = 0; j < 8; ++j) h[c][j] += q[j];
+          const Raw8<RT> total = round8<RT>(h[c]);
+          store8<RT>(a.total + row * a.ld_total + (c * kRow + t) * 8 * RT::bytes, total, n[c]);
+          values8<RT>(total, 8, h[c]);
         }
-        const u32 col = (c * kRow + t) * 8;
-        store8<RT>(a.total + row * a.ld_total + (int64_t)col * RT::bytes, h[c], n[c]);
-      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)h[c][j], (double)h[c][j], sum);
+        for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)h[c][j], (double)h[c][j], sum);
+      }
     }
     sum = wave_sum(sum);
     if constexpr (WAVES > 1) {
-      __shared__ double part[2][WAVES];  // two, for a wave may be a row ahead
-      const u32 which = (u32)((row / gridDim.x) & 1);
-      if (t % 64 == 0) part[which][t / 64] = sum;
+      __shared__ double part[2][kRows][WAVES];  // two, for a wave may be a row ahead
+      const u32 which = turn & 1;
+      if (t % 64 == 0) part[which][mine][t / 64] = sum;
       __syncthreads();
       sum = 0.0;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) sum += part[which][w];
+      for (int w = 0; w < WAVES; ++w) sum += part[which][mine][w];
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(n[c]));
-    const double rstd = 1.0 / __builtin_sqrt(sum / a.cols + a.eps);
-    if (a.rstd && t == 0) a.rstd[row] = (float)rstd;
+    if (!exists) continue;
+    const RmsLaunch& b = argument<RmsLaunch>();
+    const double rstd = inverse_root(sum * b.per_col + b.eps);
+    const float r_hi = (float)rstd, r_lo = (float)(rstd - (double)r_hi);
+    if (b.rstd && t == 0) b.rstd[row] = r_hi;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const u32 col = (c * kRow + t) * 8;
-      float y[8], w[8];
+      float y[8];
       if (a.weight) {
-        Raw8<F32> q;
-        load8_as(a.weight + (int64_t)col * one_bytes(a.weight_type), a.weight_end, a.weight_type, n[c], q);
-        values8_as(q, a.weight_type, n[c], w);
-      }
+        float w[8];
+        values8_as(rw[c], a.weight_type, 8, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double v = (double)h[c][j] * rstd;
-        y[j] = (float)(a.weight ? v * (double)w[j] : v);
+        for (int j = 0; j < 8; ++j) {
+          const float s = w[j] * r_hi;
+          const float s_lo = __builtin_fmaf(w[j], r_lo, __builtin_fmaf(w[j], r_hi, -s));
+          const float p = h[c][j] * s;
+          y[j] = p + __builtin_fmaf(h[c][j], s_lo, __builtin_fmaf(h[c][j], s, -p));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float p = h[c][j] * r_hi;
+          y[j] = p + __builtin_fmaf(h[c][j], r_lo, __builtin_fmaf(h[c][j], r_hi, -p));
+        }
       }
       clear_tail(y, n[c]);  // infinity times the zeros there
-      if (a.y) store8_as(a.y + row * a.ld_y + (int64_t)col * one_bytes(a.y_type), a.y_type, y, n[c]);
-      if constexpr (HELD) hold8(a.held, row, c * kRow + t, y, n[c]);
+      if (b.y) store8_as(b.y + row * b.ld_y + (int64_t)((c * kRow + t) * 8) * one_bytes(b.y_type), b.y_type, y, n[c]);
+      if constexpr (HELD) hold8(b.held, row, c * kRow + t, y, n[c]);
     }
   }
 }
@@ -102,18 +135,20 @@ __global__ __launch_bounds__(rms_threads(WAVES)) void rms_kernel(const RmsLaunch
 template <class XT, class RT, bool HELD>
 void rms_as(const RmsLaunch& a, hipStream_t s) {
   auto go = [&](auto waves, auto groups) {
-    constexpr int W = decltype(waves)::value, C = decltype(groups)::value;
-    constexpr int rows = rms_threads(W) / (W * 64);
-    const u32 grid = (u32)std::min<int64_t>((a.rows + rows - 1) / rows, kMaxGroups);
+    constexpr int W = decltype(waves)::value, C = decltype(groups)::value, rows = rms_threads(W) / (W * 64);
+    // as many workgroups as fit the card at once; each loads its next row while it works on one
+    const u32 grid = (u32)std::min<int64_t>((a.rows + rows - 1) / rows, 256 * 16 / std::max(W, 4));
     hipLaunchKernelGGL((rms_kernel<XT, RT, W, C, HELD>), dim3(grid), dim3(rms_threads(W)), 0, s, a);
   };
-#define ZK_SHAPE(w, c) go(std::integral_constant<int, w>{}, std::integral_constant<int, c>{})
-  if (a.cols <= 512) ZK_SHAPE(1, 1);
-  else if (a.cols <= 1024) ZK_SHAPE(1, 2);
-  else if (a.cols <= 2048) ZK_SHAPE(4, 1);
-  else if (a.cols <= 4096) ZK_SHAPE(4, 2);
-  else ZK_SHAPE(8, 2);
-#undef ZK_SHAPE
+  // 16 bytes of a row a lane and vector: two groups of 16-bit columns (8192 x 4096 bf16 without a residual 29 us,
+  // with one 33), one of fp32 (4096 x 4096 24 us, with two 30)
+  constexpr int C = XT::bytes == 4 ? 1 : 2;
+  using Groups = std::integral_constant<int, C>;
+  if (a.cols <= 512) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  else if (a.cols <= 1024) go(std::integral_constant<int, 2 / C>{}, Groups{});
+  else if (a.cols <= 2048) go(std::integral_constant<int, 4 / C>{}, Groups{});
+  else if (a.cols <= 4096) go(std::integral_constant<int, 8 / C>{}, Groups{});
+  else go(std::integral_constant<int, 16 / C>{}, Groups{});
 }
 
 }  // namespace
