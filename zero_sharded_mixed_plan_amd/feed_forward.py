@@ -30,7 +30,7 @@ from typing import NamedTuple, Optional, Tuple, Union
 import torch
 
 from . import _abi
-from .input_layer import _call, _code, _device, _no_history, _rows
+from .input_layer import _call, _code, _no_history, _rows
 
 # as in input_layer: the calls' argument structs are packed in one go
 _RMS = struct.Struct("@PqiiPqPqPiiPqPPqqd")
@@ -82,6 +82,15 @@ def packed8_empty(shape, device="cuda") -> Packed8:
     return Packed8(codes, torch.empty((*lead, (cols + BLOCK - 1) // BLOCK), dtype=torch.float8_e8m0fnu, device=device))
 
 
+def _packed8(shape, like: torch.Tensor) -> Packed8:
+    """packed8_empty beside a tensor."""
+    if like.shape == shape:  # a quicker call
+        codes = torch.empty_like(like, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+    else:
+        codes = like.new_empty(shape, dtype=torch.float8_e4m3fn)
+    return Packed8(codes, like.new_empty((*shape[:-1], (shape[-1] + BLOCK - 1) // BLOCK), dtype=torch.float8_e8m0fnu))
+
+
 def _held(p: Packed8, rows: int, cols: int, shape, what: str) -> _abi.zero_held_t:
     """The C struct of a Packed8 of this shape."""
     codes, scales = p
@@ -100,31 +109,34 @@ def _is_packed(t) -> bool:
     return isinstance(t, Packed8)
 
 
-def _tensors(*ts):
-    """The tensors among tensors, Packed8s and None."""
-    for t in ts:
+def _one_device(first: torch.Tensor, *others) -> int:
+    """The index of the one GPU of tensors, Packed8s and Nones."""
+    dev = first.get_device()
+    history, stranger = first.requires_grad, None
+    for t in others:
         if t is None:
             continue
         if isinstance(t, Packed8):
-            yield t.codes
-            yield t.scales
-        else:
-            yield t
-
-
-def _one_device(*ts) -> int:
-    ts = list(_tensors(*ts))
-    for t in ts:
-        if t.requires_grad:
-            _no_history()
-            break
-    return _device(*ts)
+            _one_device(first, *t)
+            continue
+        if t.get_device() != dev:
+            stranger = t
+        history = history or t.requires_grad
+    if history:
+        _no_history()
+    if dev < 0 or (stranger is not None and not stranger.is_cuda):
+        raise ValueError("tensors must be on the GPU")
+    if stranger is not None:
+        raise ValueError("tensors are on different devices")
+    return dev
 
 
 def _result(out: Optional[torch.Tensor], shape, dtype: torch.dtype, like: torch.Tensor, what: str):
     """A given result, checked, or a new one: (tensor, stride between rows)."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device), shape[-1]
+        if like.shape == shape:  # a quicker call
+            return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format), shape[-1]
+        return like.new_empty(shape, dtype=dtype), shape[-1]
     if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"{what} must be {list(shape)} of {dtype}")
     return out, _rows(out, what)[2]
@@ -143,7 +155,7 @@ def pack8(x: torch.Tensor, *, out: Optional[Packed8] = None) -> Packed8:
     """x [..., cols] held in 8 bits: a checkpoint of about a byte an element."""
     n, cols, ld = _rows(x, "x")
     code = _code(x.dtype)
-    p = packed8_empty(x.shape, x.device) if out is None else out
+    p = _packed8(x.shape, x) if out is None else out
     held = _held(p, n, cols, x.shape, "out")
     dev = _one_device(x, p)
     if n and cols:
@@ -158,7 +170,7 @@ def unpack8(p: Packed8, dtype: Optional[torch.dtype] = None, *, out: Optional[to
     n, cols, _ = _rows(p.codes, "codes")
     held = _held(p, n, cols, p.codes.shape, "p")
     out, ld = _result(out, p.codes.shape, dtype, p.codes, "out")
-    dev = _one_device(p, out)
+    dev = _one_device(out, p)
     if n and cols:
         _call(_abi.lib().zero_unpack8, dev, ctypes.addressof(held), n, cols, out.data_ptr(), ld, code)
     return out
@@ -205,13 +217,13 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
         ptr_y, yc = y.data_ptr(), _code(dt)
     held = keep = None
     if packed is not False:
-        keep = packed8_empty(shape, x.device) if packed is True else packed
+        keep = _packed8(shape, x) if packed is True else packed
         held = _held(keep, n, cols, shape, "packed")
     if y is None and keep is None:
         raise ValueError("neither out nor packed is asked for")
     scale = None
     if rstd is not False:
-        scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device) if rstd is True else rstd
+        scale = x.new_empty(shape[:-1], dtype=torch.float32) if rstd is True else rstd
         if scale.shape != shape[:-1] or scale.dtype != torch.float32 or not scale.is_contiguous():
             raise ValueError("rstd must be contiguous fp32 of x's shape without the columns")
     dev = _one_device(x, residual, total, weight, y, keep, scale)
@@ -232,7 +244,7 @@ def rms_norm_grad_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor
 
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return like.new_empty(nbytes, dtype=torch.uint8)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     return workspace
@@ -339,9 +351,9 @@ def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, act: str
     gate = up = None
     if isinstance(keep, str):
         if keep == "packed":
-            gate, up = packed8_empty(shape, x.device), packed8_empty(shape, x.device)
+            gate, up = _packed8(shape, x), _packed8(shape, x)
         elif keep == "tensors":
-            gate, up = (torch.empty(shape, dtype=x.dtype, device=x.device) for _ in range(2))
+            gate, up = x.new_empty(shape), x.new_empty(shape)
         else:
             raise ValueError("keep must be 'tensors', 'packed' or a pair of either")
     elif keep is not None:
