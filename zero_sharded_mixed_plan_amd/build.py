@@ -23,7 +23,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libzero_shard.so")
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("kernels.hip", "abi.cpp", "plan.cpp", "runtime.cpp", "noalloc.hip",
-                                                   "input.hip", "input_abi.cpp", "norm.hip", "norm_grad.hip", "held.hip", "gated.hip", "layer_abi.cpp")]
+                                                   "input.hip", "input_abi.cpp", "norm.hip", "norm_grad.hip", "held.hip", "gated.hip",
+                                                   "gated_any.hip", "layer_abi.cpp")]
 ARCH = "gfx950"
 
 FLAGS = [
