@@ -5,7 +5,7 @@ sharded step.
 Error bounds (u = half a step of a type relative to the value, e = 2^-24; SUB = half the
 smallest subnormal of the result's type):
   codes, totals, unpacked values   equal bits
-  y           computed in fp64 (its error of some 2^-50 is covered by 1.01), rounded to
+  y           computed in pairs of fp32 (an error of some 2^-44, covered by 1.01), rounded to
               fp32, then to its type: (e + u) |y|
   dh          s = w dy and n = h rstd: 1 rounding each; their products' sum over a row is made of at
               most 16 terms a lane, 6 steps over the lanes, 8 waves: 30 additions on any path, each
@@ -653,6 +653,126 @@ def test_products_empty_and_special():
     dx = F.gated_input_grad(dg, du, v, w)
     ok = [c for c in range(40) if c != 7]
     assert torch.equal(dx[:, ok], clean[:, ok]) and not torch.isfinite(dx[:, 7]).any()
+
+
+# Every variant that a rule on sizes chooses, with whole numbers on the GPU: dense and padded operands,
+# aligned ones and others.
+def on_gpu(gen, rows, cols, dt, off=0, pad=0, most=2):
+    """Whole numbers of -most .. most in a padded matrix; NaN in the padding."""
+    flat = torch.full((off + rows * (cols + pad),), float("nan"), dtype=T[dt], device="cuda")
+    v = flat[off:].view(rows, cols + pad)[:, :cols]
+    v.copy_(torch.randint(-most, most + 1, (rows, cols), generator=gen, device="cuda", dtype=torch.int8))
+    return v
+
+
+FORMS = [  # tokens, dim, hidden, type, offset, padding
+    (4000, 200, 2040, "bf16", 0, 0), (4001, 72, 2041, "f16", 0, 8), (2100, 136, 1000, "bf16", 0, 0), (65, 328, 9000, "bf16", 0, 0),
+    (16384, 64, 520, "bf16", 0, 0),
+    (1, 840, 8300, "bf16", 0, 0), (5, 64, 8200, "f16", 0, 0), (17, 136, 8300, "bf16", 0, 0), (32, 72, 200, "bf16", 0, 0),
+    (33, 840, 300, "f16", 0, 0), (64, 200, 8300, "bf16", 0, 0), (64, 8, 31, "f16", 0, 0),
+    (1, 841, 8301, "bf16", 0, 0), (2, 63, 33, "f16", 1, 0), (17, 137, 300, "bf16", 0, 1), (33, 300, 77, "f32", 1, 3),
+    (64, 129, 1000, "f16", 3, 0), (64, 7, 65, "bf16", 0, 0), (12, 1000, 500, "f32", 0, 0), (29, 260, 200, "f32", 0, 0),
+    (65, 9, 31, "bf16", 0, 0), (300, 515, 190, "bf16", 0, 0), (1025, 191, 333, "f16", 5, 3), (257, 512, 640, "f32", 0, 0),
+    (129, 31, 65, "f32", 1, 1), (130, 64, 66, "bf16", 4, 0),
+    (3, 16, (1 << 18) + 40, "bf16", 0, 0), ((1 << 18) + 5, 8, 16, "f16", 0, 0), (3, 5, (1 << 18) + 33, "f32", 0, 0),
+]
+
+
+@pytest.mark.parametrize("t,d,f,dt,off,pad", FORMS)
+def test_gated_forms(t, d, f, dt, off, pad):
+    say(f"gated {t}x{d}x{f} {dt} off {off} pad {pad}")
+    gen = torch.Generator(device="cuda").manual_seed(t + d + f)
+    x = on_gpu(gen, t, d, dt, off, pad)
+    wg, wu = (on_gpu(gen, f, d, dt, off, pad) for _ in range(2))
+    gate, up = ((x.float() @ w.float().t()).contiguous() for w in (wg, wu))  # exact
+    kept = F.gated(x, wg, wu, act="gelu", keep="tensors")
+    assert torch.equal(kept.gate, gate.to(T[dt])) and torch.equal(kept.up, up.to(T[dt]))
+    held = F.gated(x, wg, wu, act="gelu", keep="packed")
+    for got, v in ((held.gate, gate), (held.up, up)):
+        want = F.pack8(v)
+        assert torch.equal(got.codes.view(torch.uint8), want.codes.view(torch.uint8))
+        assert torch.equal(got.scales.view(torch.uint8), want.scales.view(torch.uint8))
+    lean = F.gated(x, wg, wu, act="gelu").a
+    assert torch.equal(lean, kept.a) and torch.equal(lean, held.a)
+    # a = g p u with p = 1 / (1 + exp(-z)): z off by 6 e |z| moves p by p (1 - p) 6 e |z|, the rest by 8 e p (or
+    # p reads 0 below 2^-126); the two products and what else is rounded 3 e
+    g, u = gate.double(), up.double()
+    z = 2 * 0.7978845608028654 * (g + 0.044715 * g ** 3)
+    p = 1 / (1 + torch.exp(-z))
+    want = g * p * u
+    err = (6 * z.abs() * (1 - p) + 11) * E * want.abs() + 2.0 ** -126 * (g * u).abs()
+    tol = 1.01 * (err + torch.finfo(T[dt]).eps / 2 * want.abs()) + SUB[T[dt]]
+    fits = want.abs() <= 65000 if dt == "f16" else torch.ones_like(want, dtype=torch.bool)
+    assert ((lean.double() - want).abs() <= tol)[fits].all()
+
+
+PRODUCT_FORMS = [  # tokens, dim, hidden, type, offset, padding
+    (4096, 4096, 72, "bf16", 0, 0), (4100, 2048, 200, "f16", 0, 8), (100, 4096, 2048, "bf16", 0, 0), (100, 4096, 2048, "f16", 0, 0),
+    (300, 512, 5000, "bf16", 0, 0), (9000, 136, 72, "bf16", 0, 0), (9000, 136, 72, "f16", 0, 8), (1, 512, 5000, "bf16", 0, 0),
+    (1, 513, 5001, "bf16", 0, 0), (1, 300, 700, "f32", 0, 0), (9001, 137, 71, "bf16", 0, 0), (9001, 66, 130, "f16", 1, 0),
+    (2500, 100, 60, "f32", 0, 0), (2501, 130, 129, "f32", 3, 1), (700, 260, 390, "bf16", 4, 0), (3, 5, 4099, "f16", 0, 3),
+    (64, 7, 33, "bf16", 0, 0), (129, 3, 1000, "bf16", 0, 0), (40, 1000, 6, "f32", 0, 0), (63, 129, 127, "f16", 0, 0),
+    (65, 8, 8, "bf16", 0, 0), (1, 1, 1, "f16", 0, 0),
+    ((1 << 18) + 9, 8, 16, "bf16", 0, 0), (5, (1 << 18) + 8, 16, "bf16", 0, 0), (5, 8, (1 << 18) + 24, "f16", 0, 0),
+    (6, (1 << 18) + 7, 5, "f32", 0, 0),
+]
+
+
+@pytest.mark.parametrize("t,d,f,dt,off,pad", PRODUCT_FORMS)
+def test_product_forms(t, d, f, dt, off, pad):
+    say(f"products {t}x{d}x{f} {dt} off {off} pad {pad}")
+    gen = torch.Generator(device="cuda").manual_seed(t + d + f)
+    x, dg, du = (on_gpu(gen, t, c, dt, off, pad) for c in (d, f, f))
+    wg, wu = (on_gpu(gen, f, d, dt, off, pad) for _ in range(2))
+    dx = F.gated_input_grad(dg, du, wg, wu)
+    want = dg.double() @ wg.double() + du.double() @ wu.double()
+    assert torch.equal(dx, want.float().to(T[dt]))
+    for wt in ("f32", "bf16", "f16"):
+        sums = [(v.double().t() @ x.double()).float() for v in (dg, du)]
+        grads = [Mat(f, d, wt, off, d + pad) for _ in range(2)]
+        F.gated_weight_grad(dg, du, x, grads[0].v, grads[1].v)
+        for m, w in zip(grads, sums):
+            assert torch.equal(m.v, w.to(T[wt])), wt
+            m.v.fill_(3.0)
+        F.gated_weight_grad(dg, du, x, grads[0].v, grads[1].v, accumulate=True)
+        for m, w in zip(grads, sums):
+            assert torch.equal(m.v, (w + 3.0).to(T[wt])), wt
+            m.check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_products_keep_apart_what_is_not_finite(dt):
+    """NaN and infinities reach the results whose sums they are part of, in every form: aligned tiles,
+    others, few tokens, split sums."""
+    for t, d, f in ((300, 136, 200), (300, 137, 201), (5, 136, 200), (5, 137, 201), (2049, 72, 72), (2049, 71, 73)):
+        say(f"not finite {t}x{d}x{f} {dt}")
+        gen = torch.Generator(device="cuda").manual_seed(t + d)
+        x, dg, du = (on_gpu(gen, t, c, dt) for c in (d, f, f))
+        wg, wu = (on_gpu(gen, f, d, dt) for _ in range(2))
+        clean = F.gated(x, wg, wu, keep="tensors")
+        y, v = x.clone(), wg.clone()
+        y[-1, -1] = float("nan")
+        v[-1, 0] = float("inf")
+        got = F.gated(y, wg, wu, keep="tensors")
+        for a, b in zip(got, clean):
+            assert torch.isnan(a[-1]).all() and torch.equal(a[:-1], b[:-1])
+        got = F.gated(x, v, wu, keep="tensors")
+        assert torch.equal(got.a[:, :-1], clean.a[:, :-1]) and torch.equal(got.gate[:, :-1], clean.gate[:, :-1])
+        assert torch.equal(got.up, clean.up) and not torch.isfinite(got.gate[:, -1]).any()
+        dx = F.gated_input_grad(dg, du, wg, wu)
+        bad = du.clone()
+        bad[-1, -1] = float("nan")
+        got = F.gated_input_grad(dg, bad, wg, wu)
+        assert torch.isnan(got[-1]).all() and torch.equal(got[:-1], dx[:-1])
+        v = wu.clone()
+        v[-1, -1] = float("nan")
+        got = F.gated_input_grad(dg, du, wg, v)
+        assert torch.isnan(got[:, -1]).all() and torch.equal(got[:, :-1], dx[:, :-1])
+        one, two = ([torch.empty(f, d, device="cuda") for _ in range(2)] for _ in range(2))
+        F.gated_weight_grad(dg, du, x, *one)
+        F.gated_weight_grad(dg, bad, y, *two)
+        assert torch.isnan(two[1][-1]).all() and torch.isnan(two[0][:, -1]).all()
+        assert torch.equal(two[0][:, :-1], one[0][:, :-1]) and torch.equal(two[1][:-1, :-1], one[1][:-1, :-1])
 
 
 # ---------------------------------------------------------------------------
