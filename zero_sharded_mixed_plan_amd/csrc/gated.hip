@@ -19,6 +19,9 @@ namespace {
 //
 // Rows of k are copied 64 of k at a time, whole lines of the L2 (with half lines its
 // requests doubled, and the 8192 x 4096 x 14336 forward pass took 1626 us in place of 1525).
+// A deep tile can be refilled only when both of its steps have been read, two steps before it is
+// needed; where both operands have them, the second has a third one, which fills the 160 KB of a CU:
+// 1530 us with two and two, 1436 with three (1339 TFLOP/s).
 // The DMA writes LDS in lane order, 1024 bytes a wave, so a lane fetches the unit that belongs
 // at its place.
 template <int TILE>
@@ -95,6 +98,13 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
+// f(0), f(1) .. f(N - 1), as constants
+template <int N, int J = 0, class F>
+__device__ __forceinline__ void each_step(F&& f) {
+  f(std::integral_constant<int, J>{});
+  if constexpr (J + 1 < N) each_step<N, J + 1>(f);
+}
+
 template <class T, Product KIND, int TILE>
 __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const ProductLaunch a, u32 down, u32 across, u32 splits) {
   constexpr bool kQByK = KIND != kWeight, kPByK = KIND == kForward;
@@ -102,11 +112,13 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   constexpr int XB = TILE / WC / 32, YB = TILE / WR / 32;
   constexpr u32 kCols = KIND == kForward ? TILE / 2 : TILE;  // columns of the results
   // Names of their own, so that the compiler sees that reads of one and copies to another do not
-  // meet, and waits for none of them; it tells seven apart.  An operand has two deep tiles, or four.
+  // meet, and waits for none of them; it tells seven apart.  An operand has two deep tiles (of the forward
+  // pass's two the second has three), or four.
   constexpr int kP = kTileBytes<TILE, kPByK>, kQ = kTileBytes<TILE, kQByK>;
   constexpr bool kEight = !kPByK && !kQByK;
+  constexpr bool kThree = kPByK && kQByK;
   __shared__ __attribute__((aligned(128))) char p1[kP], p2[kPByK ? 16 : kP], p3[kPByK ? 16 : kP];
-  __shared__ __attribute__((aligned(128))) char q1[kQ], q2[kQByK ? 16 : kQ], q3[kQByK ? 16 : kQ];
+  __shared__ __attribute__((aligned(128))) char q1[kQ], q2[kThree || !kQByK ? kQ : 16], q3[kQByK ? 16 : kQ];
   __shared__ __attribute__((aligned(128))) char p0[kEight ? kP + kQ : kP], q0[kEight ? 16 : kQ];
   u32 tr, tc;
   const u32 halves = KIND == kWeight ? 2 : 1;
@@ -178,15 +190,16 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
       next_q += far_q;
       left_q -= kDeep<kQByK>;
     };
-    // Steps go round J = 0 .. 3.  The tile of step J, or of steps J and J + 1 (J even) where it is deep:
+    // Steps go round J = 0 .. kRound - 1.  The tile of step J, or of steps J and J + 1 (J even) where it is deep:
     auto tile_p = [&](auto j) -> char* {
       constexpr int J = decltype(j)::value & 3;
       if constexpr (kPByK) return J < 2 ? p0 : p1;
       else return J == 0 ? p0 : J == 1 ? p1 : J == 2 ? p2 : p3;
     };
     auto tile_q = [&](auto j) -> char* {
-      constexpr int J = decltype(j)::value & 3;
-      if constexpr (kQByK) return J < 2 ? q0 : q1;
+      constexpr int J = kThree ? decltype(j)::value / 2 % 3 : decltype(j)::value & 3;
+      if constexpr (kThree) return J == 0 ? q0 : J == 1 ? q1 : q2;
+      else if constexpr (kQByK) return J < 2 ? q0 : q1;
       else return J == 0 ? (kEight ? p0 + kP : q0) : J == 1 ? q1 : J == 2 ? q2 : q3;
     };
     auto read = [&](auto j, Fragments& f) {
@@ -203,14 +216,17 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
     };
     // A step multiplies fragments that are in registers, while those of the next one are read, and starts
     // the copies that fit into what it was itself read from: a step's tile four steps ahead, or
-    // with its second step a deep tile three steps ahead.
+    // with its second step a deep tile three steps ahead; into the third deep tile four steps ahead.
     auto copies = [&](auto j, u32 s, auto all_whole) {
       constexpr int J = decltype(j)::value;
       const bool small = decltype(all_whole)::value || s + 4 < steps, deep = decltype(all_whole)::value || s + 3 < steps;
       if constexpr (!kPByK || J % 2 == 1)
         if (kPByK ? deep : small) copy_p(tile_p(j), all_whole);
-      if constexpr (!kQByK || J % 2 == 1)
+      if constexpr (kThree) {
+        if (J % 2 == 0 && small) copy_q(tile_q(std::integral_constant<int, J + 4>{}), all_whole);
+      } else if constexpr (!kQByK || J % 2 == 1) {
         if (kQByK ? deep : small) copy_q(tile_q(j), all_whole);
+      }
     };
     auto multiply_and_read = [&](auto j, const Fragments& f, Fragments& next) {
       constexpr int J = decltype(j)::value;
@@ -225,9 +241,9 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
       constexpr int kReads = kStep / 16 * ((kPByK ? 1 : 2) * XB + (kQByK ? 1 : 2) * YB);
       constexpr int kMfma = kStep / 16 * XB * YB;
       constexpr int kEach = (kReads + kMfma - 3) / (kMfma - 2);
-      interleave<kMfma, (!kPByK || J % 2 ? kRP : 0) + (!kQByK || J % 2 ? kRQ : 0), kReads, kEach>();
+      interleave<kMfma, (!kPByK || J % 2 ? kRP : 0) + (!kQByK || J % 2 == (kThree ? 0 : 1) ? kRQ : 0), kReads, kEach>();
     };
-    constexpr int kSmall = (kPByK ? 0 : kRP) + (kQByK ? 0 : kRQ);  // copies started by an even step
+    constexpr int kSmall = (kPByK ? 0 : kRP) + (kQByK && !kThree ? 0 : kRQ);  // copies started by an even step
     auto step = [&](auto j, const Fragments& f, Fragments& next) {
       constexpr int J = decltype(j)::value;
       copies(j, 0, std::true_type{});
@@ -246,6 +262,7 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
     using J1 = std::integral_constant<int, 1>;
     using J2 = std::integral_constant<int, 2>;
     using J3 = std::integral_constant<int, 3>;
+    constexpr int kRound = kThree ? 12 : 4;
     Fragments f, g;
     copy_p(tile_p(J0{}), std::false_type{});
     copy_q(tile_q(J0{}), std::false_type{});
@@ -262,19 +279,17 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
     read(J0{}, f);
     turn<8>();
     u32 s = 0;
-    for (; s + 8 <= whole; s += 4) {  // copies of whole steps only
-      step(J0{}, f, g);
-      step(J1{}, g, f);
-      step(J2{}, f, g);
-      step(J3{}, g, f);
-    }
+    for (; s + kRound + 4 <= whole; s += kRound)  // copies of whole steps only
+      each_step<kRound>([&](auto j) {
+        if constexpr (decltype(j)::value % 2 == 0) step(j, f, g);
+        else step(j, g, f);
+      });
 #pragma unroll 1
-    for (; s < steps; s += 4) {
-      last_steps(J0{}, s, f, g);
-      last_steps(J1{}, s + 1, g, f);
-      last_steps(J2{}, s + 2, f, g);
-      last_steps(J3{}, s + 3, g, f);
-    }
+    for (; s < steps; s += kRound)
+      each_step<kRound>([&](auto j) {
+        if constexpr (decltype(j)::value % 2 == 0) last_steps(j, s + decltype(j)::value, f, g);
+        else last_steps(j, s + decltype(j)::value, g, f);
+      });
   }
 
   // the results leave by way of LDS, where the copies no longer need it
