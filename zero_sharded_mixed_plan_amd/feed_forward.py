@@ -36,6 +36,7 @@ from .input_layer import _call, _code, _no_history, _rows
 _RMS = struct.Struct("@PqiiPqPqPiiPqPPqqd")
 _RMS_GRAD = struct.Struct("@PqiiPqPPPiiPqPqPiiqqPq")
 _GATED = struct.Struct("@qqqii" + "Pq" * 6 + "PP" + "Pq" * 6 + "iiPq")
+_ZEROS = tuple((0,) * n for n in range(17))  # what a call leaves out
 assert _RMS.size == ctypes.sizeof(_abi.zero_rms_args_t)
 assert _RMS_GRAD.size == ctypes.sizeof(_abi.zero_rms_grad_args_t)
 assert _GATED.size == ctypes.sizeof(_abi.zero_gated_args_t)
@@ -318,18 +319,27 @@ def _act(act: str) -> int:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, not {act!r}") from None
 
 
-def _pack_gated(tokens=0, dim=0, hidden=0, dtype=0, act=0, x=(0, 0), w_gate=(0, 0), w_up=(0, 0), a=(0, 0), g=(0, 0),
-                u=(0, 0), g8=0, u8=0, da=(0, 0), dg=(0, 0), du=(0, 0), dx=(0, 0), dw_gate=(0, 0), dw_up=(0, 0),
-                dw_dtype=0, accumulate=0, ws=(0, 0)) -> bytes:
-    return _GATED.pack(tokens, dim, hidden, dtype, act, *x, *w_gate, *w_up, *a, *g, *u, g8, u8, *da, *dg, *du, *dx,
-                       *dw_gate, *dw_up, dw_dtype, accumulate, *ws)
+def _kept(gate, up, n: int, hidden: int, shape, like: torch.Tensor):
+    """The arguments g, ld_g, u, ld_u, g8, u8 of a pair of tensors or Packed8s, or of none, and what
+    holds the structs."""
+    if gate is None:
+        return 0, 0, 0, 0, 0, 0, None
+    if isinstance(gate, Packed8) != isinstance(up, Packed8):
+        raise ValueError("gate and up must be of one form")
+    if isinstance(gate, Packed8):
+        held = _held(gate, n, hidden, shape, "gate"), _held(up, n, hidden, shape, "up")
+        return 0, 0, 0, 0, ctypes.addressof(held[0]), ctypes.addressof(held[1]), held
+    for t, what in ((gate, "gate"), (up, "up")):
+        if t.shape != shape or t.dtype != like.dtype:
+            raise ValueError(f"{what} must be {list(shape)} of {like.dtype}")
+    return gate.data_ptr(), _rows(gate, "gate")[2], up.data_ptr(), _rows(up, "up")[2], 0, 0, None
 
 
 def _weights(w_gate: torch.Tensor, w_up: torch.Tensor, dtype: torch.dtype):
-    if w_gate.dim() != 2 or w_gate.shape != w_up.shape or w_gate.dtype != dtype or w_up.dtype != dtype:
+    shape = w_gate.shape
+    if len(shape) != 2 or shape != w_up.shape or w_gate.dtype != dtype or w_up.dtype != dtype:
         raise ValueError(f"w_gate and w_up must be [hidden, dim] of {dtype}")
-    hidden, dim, ld_g = _rows(w_gate, "w_gate")
-    return hidden, dim, ld_g, _rows(w_up, "w_up")[2]
+    return shape[0], shape[1], _rows(w_gate, "w_gate")[2], _rows(w_up, "w_up")[2]
 
 
 def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, act: str = "silu",
@@ -358,22 +368,14 @@ def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, act: str
             raise ValueError("keep must be 'tensors', 'packed' or a pair of either")
     elif keep is not None:
         gate, up = keep
-    kw = {}
-    if gate is not None:
-        if _is_packed(gate) != _is_packed(up):
-            raise ValueError("gate and up are kept in one form")
-        if _is_packed(gate):
-            held = _held(gate, n, hidden, shape, "gate"), _held(up, n, hidden, shape, "up")
-            kw = dict(g8=ctypes.addressof(held[0]), u8=ctypes.addressof(held[1]))
-        else:
-            kw = {k: (t.data_ptr(), _result(t, shape, x.dtype, x, w)[1]) for k, t, w in (("g", gate, "gate"), ("u", up, "up"))}
+    pg, ldg, pu, ldu, g8, u8, held = _kept(gate, up, n, hidden, shape, x)
     dev = _one_device(x, w_gate, w_up, a, gate, up)
     if n and hidden:
         if dim == 0:
             raise ValueError("the weights have no columns")
-        _call(_abi.lib().zero_gated, dev, _pack_gated(
-            n, dim, hidden, code, kind, (x.data_ptr(), ld_x), (w_gate.data_ptr(), ld_g), (w_up.data_ptr(), ld_u),
-            (a.data_ptr(), ld_a), **kw))
+        _call(_abi.lib().zero_gated, dev, _GATED.pack(
+            n, dim, hidden, code, kind, x.data_ptr(), ld_x, w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u,
+            a.data_ptr(), ld_a, pg, ldg, pu, ldu, g8, u8, *_ZEROS[16]))
     return Gated(a, gate, up)
 
 
@@ -388,23 +390,18 @@ def gated_grad(da: torch.Tensor, gate: Union[torch.Tensor, Packed8], up: Union[t
     """
     n, hidden, ld_da = _rows(da, "da")
     shape, kind, code = da.shape, _act(act), _code(da.dtype)
-    if _is_packed(gate) != _is_packed(up):
-        raise ValueError("gate and up are given in one form")
-    if _is_packed(gate):
-        held = _held(gate, n, hidden, shape, "gate"), _held(up, n, hidden, shape, "up")
-        kw = dict(g8=ctypes.addressof(held[0]), u8=ctypes.addressof(held[1]))
-    else:
-        kw = {k: (t.data_ptr(), _result(t, shape, da.dtype, da, w)[1]) for k, t, w in (("g", gate, "gate"), ("u", up, "up"))}
+    pg, ldg, pu, ldu, g8, u8, held = _kept(gate, up, n, hidden, shape, da)
     dg, ld_dg = _result(out_gate, shape, da.dtype, da, "out_gate")
     du, ld_du = _result(out_up, shape, da.dtype, da, "out_up")
-    a = None
+    a, ptr_a, ld_a = None, 0, 0
     if again is not False:
         a, ld_a = _result(None if again is True else again, shape, da.dtype, da, "again")
-        kw["a"] = (a.data_ptr(), ld_a)
+        ptr_a = a.data_ptr()
     dev = _one_device(da, gate, up, dg, du, a)
     if n and hidden:
-        _call(_abi.lib().zero_gated_grad, dev, _pack_gated(
-            n, 0, hidden, code, kind, da=(da.data_ptr(), ld_da), dg=(dg.data_ptr(), ld_dg), du=(du.data_ptr(), ld_du), **kw))
+        _call(_abi.lib().zero_gated_grad, dev, _GATED.pack(
+            n, 0, hidden, code, kind, *_ZEROS[6], ptr_a, ld_a, pg, ldg, pu, ldu, g8, u8, da.data_ptr(), ld_da,
+            dg.data_ptr(), ld_dg, du.data_ptr(), ld_du, *_ZEROS[10]))
     return GatedGrad(dg, du, a)
 
 
@@ -440,9 +437,9 @@ def gated_input_grad(dg: torch.Tensor, du: torch.Tensor, w_gate: torch.Tensor, w
         return dx.zero_()
     L = _abi.lib()
     workspace = _workspace(workspace, L.zero_gated_ws_bytes(n, dim, hidden), dg)
-    _call(L.zero_gated_input_grad, dev, _pack_gated(
-        n, dim, hidden, code, dg=(dg.data_ptr(), ld_dg), du=(du.data_ptr(), ld_du), w_gate=(w_gate.data_ptr(), ld_g),
-        w_up=(w_up.data_ptr(), ld_u), dx=(dx.data_ptr(), ld_dx), ws=(workspace.data_ptr(), workspace.numel())))
+    _call(L.zero_gated_input_grad, dev, _GATED.pack(
+        n, dim, hidden, code, 0, 0, 0, w_gate.data_ptr(), ld_g, w_up.data_ptr(), ld_u, *_ZEROS[10], dg.data_ptr(), ld_dg,
+        du.data_ptr(), ld_du, dx.data_ptr(), ld_dx, *_ZEROS[6], workspace.data_ptr(), workspace.numel()))
     return dx
 
 
@@ -465,8 +462,8 @@ def gated_weight_grad(dg: torch.Tensor, du: torch.Tensor, x: torch.Tensor, grad_
         return grad_gate, grad_up
     L = _abi.lib()
     workspace = _workspace(workspace, L.zero_gated_ws_bytes(n, dim, hidden), dg)
-    _call(L.zero_gated_weight_grad, dev, _pack_gated(
-        n, dim, hidden, code, dg=(dg.data_ptr(), ld_dg), du=(du.data_ptr(), ld_du), x=(x.data_ptr(), ld_x),
-        dw_gate=(grad_gate.data_ptr(), ld_g), dw_up=(grad_up.data_ptr(), ld_u), dw_dtype=wc,
-        accumulate=1 if accumulate else 0, ws=(workspace.data_ptr(), workspace.numel())))
+    _call(L.zero_gated_weight_grad, dev, _GATED.pack(
+        n, dim, hidden, code, 0, x.data_ptr(), ld_x, *_ZEROS[14], dg.data_ptr(), ld_dg, du.data_ptr(), ld_du, 0, 0,
+        grad_gate.data_ptr(), ld_g, grad_up.data_ptr(), ld_u, wc, 1 if accumulate else 0,
+        workspace.data_ptr(), workspace.numel()))
     return grad_gate, grad_up
