@@ -244,19 +244,21 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
       interleave<kMfma, (!kPByK || J % 2 ? kRP : 0) + (!kQByK || J % 2 == (kThree ? 0 : 1) ? kRQ : 0), kReads, kEach>();
     };
     constexpr int kSmall = (kPByK ? 0 : kRP) + (kQByK && !kThree ? 0 : kRQ);  // copies started by an even step
+    // When step J is done, what the next one reads has arrived: deep tiles started by the step before an even
+    // one; tiles of one step started two before.
+    constexpr auto later = [](int J) { return (kPByK || kQByK) && J % 2 == 0 ? kSmall : 8; };
     auto step = [&](auto j, const Fragments& f, Fragments& next) {
       constexpr int J = decltype(j)::value;
       copies(j, 0, std::true_type{});
       multiply_and_read(j, f, next);
-      // what the next step reads has arrived: deep tiles started by the step before an even one; tiles of
-      // one step started two before
-      turn<(kPByK || kQByK) && J % 2 == 0 ? kSmall : 8>();
+      turn<later(J)>();
     };
     auto last_steps = [&](auto j, u32 s, const Fragments& f, Fragments& next) {
       if (s >= steps) return;
       copies(j, s, std::false_type{});
       multiply_and_read(j, f, next);
-      turn<0>();
+      if (s + (kThree ? 6 : 5) <= whole) turn<later(decltype(j)::value)>();  // whole copies were started until now
+      else turn<0>();
     };
     using J0 = std::integral_constant<int, 0>;
     using J1 = std::integral_constant<int, 1>;
