@@ -26,8 +26,8 @@ namespace {
 // at its place.
 template <int TILE>
 constexpr int kTileThreads = TILE == 256 ? 512 : 256;
-template <int TILE, bool BY_K>
-constexpr int kTileBytes = TILE * kDeep<BY_K> * 2 + (TILE == 256 && !BY_K ? 512 : 0);
+template <int TILE, bool BY_K, bool DEEP>
+constexpr int kTileBytes = TILE * kDeep<DEEP> * 2 + (TILE == 256 && !BY_K ? 512 : 0);
 // This thread's place of round q in an operand's tile: byte offset from the tile's first element.
 // i0, ni: the tile's first row (column) and the matrix's number of them, beyond which the last
 // ones stand in (what they give is not stored).
@@ -77,10 +77,9 @@ __device__ __forceinline__ void copy_place(char* lds, __amdgpu_buffer_rsrc_t fro
 // All but the newest LATER copies have arrived, for every wave, and every wave's reads are done.
 template <int LATER>
 __device__ __forceinline__ void turn() {
-  static_assert(LATER < 16, "the field's low bits");
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x70 | LATER);  // vmcnt(LATER) lgkmcnt(0), known to the compiler, which adds no others
+  __builtin_amdgcn_s_waitcnt(0x70 | (LATER & 15) | (LATER >> 4) << 14);  // vmcnt(LATER) lgkmcnt(0), known to the compiler, which adds no others
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -105,7 +104,7 @@ __device__ __forceinline__ void each_step(F&& f) {
   if constexpr (J + 1 < N) each_step<N, J + 1>(f);
 }
 
-template <class T, Product KIND, int TILE>
+template <class T, Product KIND, int TILE, bool ALONE>
 __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const ProductLaunch a, u32 down, u32 across, u32 splits) {
   constexpr bool kQByK = KIND != kWeight, kPByK = KIND == kForward;
   constexpr int WC = 2, WR = TILE == 256 ? 4 : 2;
@@ -113,12 +112,14 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   constexpr u32 kCols = KIND == kForward ? TILE / 2 : TILE;  // columns of the results
   // Names of their own, so that the compiler sees that reads of one and copies to another do not
   // meet, and waits for none of them; it tells seven apart.  An operand has two deep tiles (of the forward
-  // pass's two the second has three), or four.
-  constexpr int kP = kTileBytes<TILE, kPByK>, kQ = kTileBytes<TILE, kQByK>;
-  constexpr bool kEight = !kPByK && !kQByK;
-  constexpr bool kThree = kPByK && kQByK;
-  __shared__ __attribute__((aligned(128))) char p1[kP], p2[kPByK ? 16 : kP], p3[kPByK ? 16 : kP];
-  __shared__ __attribute__((aligned(128))) char q1[kQ], q2[kThree || !kQByK ? kQ : 16], q3[kQByK ? 16 : kQ];
+  // pass's two the second has three), or four; where a tile is alone on its CU four deep ones.
+  static_assert(!ALONE || TILE == 128, "tiles of 256 have no room for more");
+  constexpr bool kPDeep = kPByK || ALONE, kQDeep = kQByK || ALONE, kThree = kPByK && kQByK && !ALONE;
+  constexpr int kPTiles = kPDeep && !ALONE ? 2 : 4, kQTiles = kThree ? 3 : kQDeep && !ALONE ? 2 : 4;
+  constexpr int kP = kTileBytes<TILE, kPByK, kPDeep>, kQ = kTileBytes<TILE, kQByK, kQDeep>;
+  constexpr bool kEight = kPTiles + kQTiles == 8;
+  __shared__ __attribute__((aligned(128))) char p1[kP], p2[kPTiles > 2 ? kP : 16], p3[kPTiles > 3 ? kP : 16];
+  __shared__ __attribute__((aligned(128))) char q1[kQ], q2[kQTiles > 2 ? kQ : 16], q3[kQTiles > 3 ? kQ : 16];
   __shared__ __attribute__((aligned(128))) char p0[kEight ? kP + kQ : kP], q0[kEight ? 16 : kQ];
   u32 tr, tc;
   const u32 halves = KIND == kWeight ? 2 : 1;
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
   const u32 wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const u32 wc = wave % WC, wr = wave / WC;
 
-  constexpr int kRP = kRounds<kPByK>, kRQ = kRounds<kQByK>;
+  constexpr int kRP = kRounds<kPDeep>, kRQ = kRounds<kQDeep>;
   u32 op[kRP], oq[kRQ];
 #pragma unroll
   for (int i = 0; i < kRP; ++i)  // in the forward pass gate's columns, then up's
@@ -165,7 +166,7 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
     const char* next_q = a.q[iq] + (kQByK ? r0 * a.ld_q[0] + k_lo * 2 : k_lo * a.ld_q[0] + r0 * 2);
     const char* next_p[2] = {a.p[ip] + (kPByK ? c0 * a.ld_p[0] + k_lo * 2 : k_lo * a.ld_p[0] + c0 * 2),
                              KIND == kForward ? a.p[1] + c0 * a.ld_p[0] : nullptr};
-    const int64_t far_q = kDeep<kQByK> * (kQByK ? 2 : a.ld_q[0]), far_p = kDeep<kPByK> * (kPByK ? 2 : a.ld_p[0]);
+    const int64_t far_q = kDeep<kQDeep> * (kQByK ? 2 : a.ld_q[0]), far_p = kDeep<kPDeep> * (kPByK ? 2 : a.ld_p[0]);
     int left_p = k, left_q = k;
     auto copy_p = [&](char* to, auto all_whole) {
       auto start = [&](auto is_part) {
@@ -174,59 +175,55 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
           copy_place<TILE, kPByK, decltype(is_part)::value>(to, buffer_at(next_p[KIND == kForward ? i / (kRP / 2) : 0]), op[i], i,
                                                             left_p);
       };
-      if (decltype(all_whole)::value || left_p >= kDeep<kPByK>) start(std::false_type{});
+      if (decltype(all_whole)::value || left_p >= kDeep<kPDeep>) start(std::false_type{});
       else start(std::true_type{});
       next_p[0] += far_p;
       if constexpr (KIND == kForward) next_p[1] += far_p;
-      left_p -= kDeep<kPByK>;
+      left_p -= kDeep<kPDeep>;
     };
     auto copy_q = [&](char* to, auto all_whole) {
       auto start = [&](auto is_part) {
 #pragma unroll
         for (int i = 0; i < kRQ; ++i) copy_place<TILE, kQByK, decltype(is_part)::value>(to, buffer_at(next_q), oq[i], i, left_q);
       };
-      if (decltype(all_whole)::value || left_q >= kDeep<kQByK>) start(std::false_type{});
+      if (decltype(all_whole)::value || left_q >= kDeep<kQDeep>) start(std::false_type{});
       else start(std::true_type{});
       next_q += far_q;
-      left_q -= kDeep<kQByK>;
+      left_q -= kDeep<kQDeep>;
     };
-    // Steps go round J = 0 .. kRound - 1.  The tile of step J, or of steps J and J + 1 (J even) where it is deep:
+    // Steps go round J = 0 .. kRound - 1.  The tile of step J, or of two steps where it is deep:
     auto tile_p = [&](auto j) -> char* {
-      constexpr int J = decltype(j)::value & 3;
-      if constexpr (kPByK) return J < 2 ? p0 : p1;
-      else return J == 0 ? p0 : J == 1 ? p1 : J == 2 ? p2 : p3;
+      constexpr int J = (kPDeep ? decltype(j)::value / 2 : decltype(j)::value) % kPTiles;
+      return J == 0 ? p0 : J == 1 ? p1 : J == 2 ? p2 : p3;
     };
     auto tile_q = [&](auto j) -> char* {
-      constexpr int J = kThree ? decltype(j)::value / 2 % 3 : decltype(j)::value & 3;
-      if constexpr (kThree) return J == 0 ? q0 : J == 1 ? q1 : q2;
-      else if constexpr (kQByK) return J < 2 ? q0 : q1;
-      else return J == 0 ? (kEight ? p0 + kP : q0) : J == 1 ? q1 : J == 2 ? q2 : q3;
+      constexpr int J = (kQDeep ? decltype(j)::value / 2 : decltype(j)::value) % kQTiles;
+      return J == 0 ? (kEight ? p0 + kP : q0) : J == 1 ? q1 : J == 2 ? q2 : q3;
     };
     auto read = [&](auto j, Fragments& f) {
-      constexpr u32 J = decltype(j)::value & 3;
+      constexpr u32 J = decltype(j)::value;
 #pragma unroll
       for (u32 s = 0; s < kStep / 16; ++s) {
 #pragma unroll
         for (int y = 0; y < YB; ++y)
-          f.q[s][y] = fragment<TILE, kQByK>(tile_q(j), at_q[y], s + (kQByK ? J % 2 * 2 : 0));
+          f.q[s][y] = fragment<TILE, kQByK>(tile_q(j), at_q[y], s + (kQDeep ? J % 2 * 2 : 0));
 #pragma unroll
         for (int x = 0; x < XB; ++x)
-          f.p[s][x] = fragment<TILE, kPByK>(tile_p(j), at_p[x], s + (kPByK ? J % 2 * 2 : 0));
+          f.p[s][x] = fragment<TILE, kPByK>(tile_p(j), at_p[x], s + (kPDeep ? J % 2 * 2 : 0));
       }
     };
     // A step multiplies fragments that are in registers, while those of the next one are read, and starts
-    // the copies that fit into what it was itself read from: a step's tile four steps ahead, or
-    // with its second step a deep tile three steps ahead; into the third deep tile four steps ahead.
+    // the copies that fit into what has been read: a step's tile four steps ahead, or with its
+    // second step a deep tile, kPFar (kQFar) steps ahead.  The second operand's third or fourth deep tile is
+    // started by the step after that.
+    constexpr bool kLater = kQTiles > 2 && kQDeep;
+    constexpr u32 kPFar = kPDeep ? 2 * kPTiles - 1 : 4, kQFar = !kQDeep ? 4 : kLater ? 2 * kQTiles - 2 : 2 * kQTiles - 1;
     auto copies = [&](auto j, u32 s, auto all_whole) {
       constexpr int J = decltype(j)::value;
-      const bool small = decltype(all_whole)::value || s + 4 < steps, deep = decltype(all_whole)::value || s + 3 < steps;
-      if constexpr (!kPByK || J % 2 == 1)
-        if (kPByK ? deep : small) copy_p(tile_p(j), all_whole);
-      if constexpr (kThree) {
-        if (J % 2 == 0 && small) copy_q(tile_q(std::integral_constant<int, J + 4>{}), all_whole);
-      } else if constexpr (!kQByK || J % 2 == 1) {
-        if (kQByK ? deep : small) copy_q(tile_q(j), all_whole);
-      }
+      if constexpr (!kPDeep || J % 2 == 1)
+        if (decltype(all_whole)::value || s + kPFar < steps) copy_p(tile_p(std::integral_constant<int, J + kPFar>{}), all_whole);
+      if constexpr (!kQDeep || J % 2 == (kLater ? 0 : 1))
+        if (decltype(all_whole)::value || s + kQFar < steps) copy_q(tile_q(std::integral_constant<int, J + kQFar>{}), all_whole);
     };
     auto multiply_and_read = [&](auto j, const Fragments& f, Fragments& next) {
       constexpr int J = decltype(j)::value;
@@ -241,12 +238,13 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
       constexpr int kReads = kStep / 16 * ((kPByK ? 1 : 2) * XB + (kQByK ? 1 : 2) * YB);
       constexpr int kMfma = kStep / 16 * XB * YB;
       constexpr int kEach = (kReads + kMfma - 3) / (kMfma - 2);
-      interleave<kMfma, (!kPByK || J % 2 ? kRP : 0) + (!kQByK || J % 2 == (kThree ? 0 : 1) ? kRQ : 0), kReads, kEach>();
+      interleave<kMfma, (!kPDeep || J % 2 ? kRP : 0) + (!kQDeep || J % 2 == (kLater ? 0 : 1) ? kRQ : 0), kReads, kEach>();
     };
-    constexpr int kSmall = (kPByK ? 0 : kRP) + (kQByK && !kThree ? 0 : kRQ);  // copies started by an even step
     // When step J is done, what the next one reads has arrived: deep tiles started by the step before an even
-    // one; tiles of one step started two before.
-    constexpr auto later = [](int J) { return (kPByK || kQByK) && J % 2 == 0 ? kSmall : 8; };
+    // one; tiles of one step started two before; with four deep tiles what was started more than four steps before.
+    constexpr int kEven = (kPDeep ? 0 : kRP) + (kQDeep && !kLater ? 0 : kRQ);  // copies started by an even step
+    constexpr auto later = [](int J) { return ALONE ? 16 : (kPDeep || kQDeep) && J % 2 == 0 ? kEven : 8; };
+    constexpr u32 kAhead = ALONE ? 9 : kThree ? 6 : 5;  // a step's copies lie within as many steps
     auto step = [&](auto j, const Fragments& f, Fragments& next) {
       constexpr int J = decltype(j)::value;
       copies(j, 0, std::true_type{});
@@ -257,31 +255,26 @@ __global__ __launch_bounds__(kTileThreads<TILE>) void tiled_kernel(const Product
       if (s >= steps) return;
       copies(j, s, std::false_type{});
       multiply_and_read(j, f, next);
-      if (s + (kThree ? 6 : 5) <= whole) turn<later(decltype(j)::value)>();  // whole copies were started until now
+      if (s + kAhead <= whole) turn<later(decltype(j)::value)>();  // whole copies were started until now
       else turn<0>();
     };
-    using J0 = std::integral_constant<int, 0>;
-    using J1 = std::integral_constant<int, 1>;
-    using J2 = std::integral_constant<int, 2>;
-    using J3 = std::integral_constant<int, 3>;
-    constexpr int kRound = kThree ? 12 : 4;
+    constexpr int kRound = ALONE ? 8 : kThree ? 12 : 4;
     Fragments f, g;
-    copy_p(tile_p(J0{}), std::false_type{});
-    copy_q(tile_q(J0{}), std::false_type{});
-    if (!kPByK && 1 < steps) copy_p(tile_p(J1{}), std::false_type{});
-    if (!kQByK && 1 < steps) copy_q(tile_q(J1{}), std::false_type{});
-    if (2 < steps) {
-      copy_p(tile_p(J2{}), std::false_type{});
-      copy_q(tile_q(J2{}), std::false_type{});
-    }
-    if (!kPByK && 3 < steps) copy_p(tile_p(J3{}), std::false_type{});
-    if (!kQByK && 3 < steps) copy_q(tile_q(J3{}), std::false_type{});
-    if (whole >= 4) turn<8>();  // the second four steps' copies may still be under way
+    // in the steps' order, but for what step 0 starts and later ones
+    constexpr u32 kFirst = kPDeep || kQDeep ? (ALONE ? 8 : 4) : 4;
+    each_step<kFirst>([&](auto j) {
+      constexpr u32 J = decltype(j)::value;
+      if (J > 0 && J >= steps) return;
+      if constexpr (!kPDeep || J % 2 == 0) copy_p(tile_p(j), std::false_type{});
+      if constexpr (!kQDeep || (J % 2 == 0 && (!kLater || J < kQFar))) copy_q(tile_q(j), std::false_type{});
+    });
+    constexpr int kBegun = ALONE ? 20 : 8;
+    if (whole >= kFirst) turn<kBegun>();  // the later steps' copies may still be under way
     else turn<0>();
-    read(J0{}, f);
-    turn<8>();
+    read(std::integral_constant<int, 0>{}, f);
+    turn<kBegun>();
     u32 s = 0;
-    for (; s + kRound + 4 <= whole; s += kRound)  // copies of whole steps only
+    for (; s + kRound - 1 + kAhead <= whole; s += kRound)  // copies of whole steps only
       each_step<kRound>([&](auto j) {
         if constexpr (decltype(j)::value % 2 == 0) step(j, f, g);
         else step(j, g, f);
@@ -439,15 +432,20 @@ bool tiles_fit(Product kind, const ProductLaunch& a) {
 // 128 0.4 alone on a CU and 0.95 where two share it (the 8192 x 4096 x 14336 forward pass 1498 us with
 // tiles of 256, 1873 with 128); a tile begins and ends in 8 and 5; partial results move at 5 TB/s,
 // and another launch takes 3.
+// Where no tile of 128 shares its CU, nothing covers its waits; four deep tiles an operand, in LDS that no other
+// workgroup needs, have copies under way for seven steps: 128 tokens, 4096 x 11008, forward 36.5 -> 32.3 us;
+// input gradient of 1024 tokens there 245 -> 164, of 4096 tokens, 768 x 2048, 38.2 -> 31.4. The weight gradient gains
+// nothing (173 and 173, 55.3 and 55.8), short sums lose (300 tokens, 512 x 1376: 6.6 and 7.1, 12.0 and 12.8).
 struct TilePlan {
   int tile;
   u32 splits;
+  bool alone;
 };
 
 TilePlan tile_plan(Product kind, const ProductLaunch& a) {
   const int64_t halves = kind == kWeight ? 2 : 1, units = (a.k + 63) / 64 * (kind == kInput ? 2 : 1);
   const int64_t bytes = halves * a.rows * a.cols * 4;
-  TilePlan best{128, 1};
+  TilePlan best{128, 1, false};
   double least = 1e300;
   for (int tile : {128, 256}) {
     const int64_t cols = kind == kForward ? tile / 2 : tile;
@@ -463,18 +461,18 @@ TilePlan tile_plan(Product kind, const ProductLaunch& a) {
       if (n > 1) t += 3.0 + 2.0 * n * (double)bytes / 5e6;
       if (t < least) {
         least = t;
-        best = TilePlan{tile, n};
+        best = TilePlan{tile, n, kind != kWeight && tile == 128 && groups <= 256 && units / n >= 32};
       }
     }
   }
   return best;
 }
 
-template <class T, Product KIND, int TILE>
+template <class T, Product KIND, int TILE, bool ALONE>
 int tiled_as(const ProductLaunch& a, u32 splits, hipStream_t s) {
   constexpr int cols = KIND == kForward ? TILE / 2 : TILE;
   const u32 down = (u32)((a.rows + TILE - 1) / TILE), across = (u32)((a.cols + cols - 1) / cols);
-  hipLaunchKernelGGL((tiled_kernel<T, KIND, TILE>), dim3(down * across * (KIND == kWeight ? 2 : 1) * splits),
+  hipLaunchKernelGGL((tiled_kernel<T, KIND, TILE, ALONE>), dim3(down * across * (KIND == kWeight ? 2 : 1) * splits),
                      dim3(kTileThreads<TILE>), 0, s, a, down, across, splits);
   return launched(KIND == kForward ? "gated projections" : KIND == kInput ? "gated input gradient" : "gated weight gradient");
 }
@@ -487,7 +485,10 @@ int tiled_of(const ProductLaunch& a, hipStream_t s) {
     if (a.rows <= 64) return few_as<T, 64>(a, s);
   }
   const TilePlan plan = tile_plan(KIND, a);
-  if (int rc = plan.tile == 256 ? tiled_as<T, KIND, 256>(a, plan.splits, s) : tiled_as<T, KIND, 128>(a, plan.splits, s)) return rc;
+  if (int rc = plan.tile == 256 ? tiled_as<T, KIND, 256, false>(a, plan.splits, s)
+               : plan.alone     ? tiled_as<T, KIND, 128, KIND != kWeight>(a, plan.splits, s)
+                                : tiled_as<T, KIND, 128, false>(a, plan.splits, s))
+    return rc;
   return plan.splits > 1 ? launch_join(KIND, a, std::is_same<T, BF16>::value ? ZERO_BF16 : ZERO_F16, plan.splits, s) : ZERO_OK;
 }
 

@@ -72,10 +72,10 @@ __device__ __forceinline__ void finish_gated4(const ProductLaunch& a, int64_t r,
 // takes, at j ^ 2 (k % 2), with 64 bytes left out before every odd pair of rows.  Either way
 // the 4 rows lie in different banks.
 constexpr int kStep = 32;
-template <bool BY_K>
-constexpr int kDeep = BY_K ? 2 * kStep : kStep;  // of k, copied at a time
-template <bool BY_K>
-constexpr int kRounds = BY_K ? 4 : 2;            // 16 bytes a thread and round
+template <bool DEEP>
+constexpr int kDeep = DEEP ? 2 * kStep : kStep;  // of k, copied at a time
+template <bool DEEP>
+constexpr int kRounds = DEEP ? 4 : 2;            // 16 bytes a thread and round
 
 // Where the 1024 bytes of chunk c of a tile begin.
 template <int TILE, bool BY_K>
