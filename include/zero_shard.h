@@ -727,8 +727,9 @@ typedef struct zero_rms_args {
 /*
  * h = x + residual, rounded to res_dtype (without a residual h = x);
  * rstd = 1 / sqrt(mean over the row of h^2 + eps); y = h * rstd * weight.
- * The row's sum is computed in fp64, y in pairs of fp32 (good to 2^-44); y is rounded to fp32, then
- * to out_dtype, and from fp32 to the codes of `held`.  A row of zeros with eps == 0 gives NaN.
+ * The row's sum is computed in fp64, y in pairs of fp32 (good to 2^-44 of its
+ * value, or 2^-149); y is rounded to fp32, then to out_dtype, and from fp32 to the codes of
+ * `held`.  A row of zeros with eps == 0 gives NaN.
  * total may be x (if the types are equal) or the residual, at the same address and
  * stride; any other overlap of what is written is refused.  Element alignment suffices.
  * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.

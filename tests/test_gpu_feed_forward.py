@@ -281,6 +281,39 @@ def test_rms_norm_in_place_and_batches():
     assert torch.equal(one.y, ref.y[2, 7:8]) and torch.equal(one.rstd, ref.rstd[2, 7:8])
 
 
+@pytest.mark.parametrize("cols", [40, 700, 1500, 4096, 8192])
+def test_rms_norm_far_magnitudes(cols):
+    """Rows whose rstd, or whose products with the weight, lie near the ends of fp32 or beyond: y is the value in
+    64 bits rounded once, whatever the factors' sizes; what does not fit is an infinity.  Of y below 2^-100 the
+    second part of the pair is a multiple of 2^-149, after two roundings of at most 2^-150 each, and so is
+    the result below 2^-126: 3 * 2^-150 beside E |y|."""
+    least = 3 * 2.0 ** -150
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    size = torch.tensor([1e-44, 1e-38, 1e-33, 1e-20, 1.0, 1e20, 1e33, 1e36], device="cuda")
+    x = torch.randn(len(size), cols, generator=g, device="cuda") * size[:, None]
+    x[:, 1] = 0
+    w = torch.randn(cols, generator=g, device="cuda") + 3
+    for k, factor in ((0, 1.0), (1, 1e-6), (2, 1e30), (3, 1e-38), (4, 2e38)):
+        v = w * factor
+        if k == 0:
+            v[3] = float("inf")
+            v[5] = float("nan")
+        with np.errstate(all="ignore"):
+            want, scale = OF.rms_norm(f64(x), f64(v), 0.0)
+            once = torch.from_numpy(want).float().double().numpy()
+        n = F.rms_norm(x, v, eps=0.0, packed=True)
+        got = f64(n.y)
+        assert np.array_equal(np.isnan(got), np.isnan(once))
+        assert np.array_equal(np.isinf(got) & ~np.isnan(once), np.isinf(once) & ~np.isnan(once)), factor
+        fits = np.isfinite(once)
+        assert (np.abs(got - want)[fits] <= 1.01 * E * np.abs(want[fits]) + least).all(), factor
+        same_codes(n.packed, OF.hold(got), "codes")
+        assert np.array_equal(f64(n.rstd), torch.from_numpy(scale).float().double().numpy())
+    alone = F.rms_norm(x, None, eps=0.0).y
+    want, _ = OF.rms_norm(f64(x), None, 0.0)
+    assert (np.abs(f64(alone) - want) <= 1.01 * E * np.abs(want) + least).all()
+
+
 def test_rms_norm_special_rows():
     """A row of zeros, one with an infinity, one with NaN, very large and very small
     ones: each on its own."""

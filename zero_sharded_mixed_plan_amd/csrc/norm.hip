@@ -45,6 +45,19 @@ __global__ __launch_bounds__(rms_threads(WAVES)) void rms_kernel(const RmsLaunch
     n[c] = col < a.cols ? min(a.cols - col, 8u) : 0;
     if (a.weight) load8_as(a.weight + (int64_t)col * one_bytes(a.weight_type), a.weight_end, a.weight_type, n[c], rw[c]);
   }
+  // |n| <= sqrt(8192): only weights from 2^121 on make an infinity of it
+  bool large = false;
+  if (a.weight) {
+    float top = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float w[8];
+      values8_as(rw[c], a.weight_type, n[c], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(w[j]));
+    }
+    large = __builtin_amdgcn_ballot_w64(top >= 0x1p121f);
+  }
   const int64_t stride = (int64_t)gridDim.x * kRows;
   struct Row {
     Raw8<XT> x[C];
@@ -105,24 +118,32 @@ __global__ __launch_bounds__(rms_threads(WAVES)) void rms_kernel(const RmsLaunch
     const double rstd = inverse_root(sum * b.per_col + b.eps);
     const float r_hi = (float)rstd, r_lo = (float)(rstd - (double)r_hi);
     if (b.rstd && t == 0) b.rstd[row] = r_hi;
+    // n = h * rstd is of size one whatever its factors are, but pairs of fp32 cannot hold an rstd near the
+    // ends of fp32
+    const bool far = large || !(rstd >= 0x1p-100 && rstd <= 0x1p100);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float y[8];
-      if (a.weight) {
-        float w[8];
-        values8_as(rw[c], a.weight_type, 8, w);
+      float y[8], w[8];
+      if (a.weight) values8_as(rw[c], a.weight_type, 8, w);
+      if (__builtin_amdgcn_ballot_w64(far)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float s = w[j] * r_hi;
-          const float s_lo = __builtin_fmaf(w[j], r_lo, __builtin_fmaf(w[j], r_hi, -s));
-          const float p = h[c][j] * s;
-          y[j] = p + __builtin_fmaf(h[c][j], s_lo, __builtin_fmaf(h[c][j], s, -p));
+          float one = h[c][j];
+          asm volatile("" : "+v"(one));  // not the squares' conversion, held in two registers until here
+          const double d = (double)one * rstd;
+          y[j] = (float)(a.weight ? d * (double)w[j] : d);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float p = h[c][j] * r_hi;
-          y[j] = p + __builtin_fmaf(h[c][j], r_lo, __builtin_fmaf(h[c][j], r_hi, -p));
+          const float p_lo = __builtin_fmaf(h[c][j], r_lo, __builtin_fmaf(h[c][j], r_hi, -p));
+          if (a.weight) {
+            const float q = w[j] * p;
+            y[j] = q + __builtin_fmaf(w[j], p_lo, __builtin_fmaf(w[j], p, -q));
+          } else {
+            y[j] = p + p_lo;
+          }
         }
       }
       clear_tail(y, n[c]);  // infinity times the zeros there
