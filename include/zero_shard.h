@@ -731,7 +731,8 @@ typedef struct zero_rms_args {
  * value, or 2^-149); y is rounded to fp32, then to out_dtype, and from fp32 to the codes of
  * `held`.  A row of zeros with eps == 0 gives NaN.
  * total may be x (if the types are equal) or the residual, at the same address and
- * stride; any other overlap of what is written is refused.  Element alignment suffices.
+ * stride; any other overlap of what is written is refused.  Matrices with one stride may be column
+ * ranges of one buffer, here and below.  Element alignment suffices.
  * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EHIP.
  */
 int zero_rms_norm(const zero_rms_args_t* args, void* stream);

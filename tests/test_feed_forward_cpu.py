@@ -260,6 +260,17 @@ def test_gated_weight_grad_refuses(kw, code):
     refused(lambda: Z.zero_gated_weight_grad(gated_args(**kw)), code, "zero_gated_weight_grad")
 
 
+@pytest.mark.parametrize("kw", [
+    dict(dg=at(11), ld_dg=79, du=at(11) + 80, ld_du=79),          # the second's last column wraps onto the first's
+    dict(dg=at(11), ld_dg=80, du=at(11) + 78, ld_du=80),          # begins in the first's last column
+    dict(dg=at(11), ld_dg=80, du=at(11) + 160 * 3 + 82, ld_du=80),  # the same rows further down, and past the row
+    dict(dg=at(11) + 160, ld_dg=80, du=at(11) + 82, ld_du=80),
+    dict(dg=at(11), ld_dg=80, du=at(11) + 80, ld_du=81),          # strides that differ
+    dict(dg=at(10) + 82, ld_dg=80, ld_da=80)])
+def test_column_ranges_that_meet_are_refused(kw):
+    refused(lambda: Z.zero_gated_grad(gated_args(**kw)), IN, "zero_gated_grad")
+
+
 def test_null_arguments():
     L = Z.lib()
     for fn in (L.zero_rms_norm, L.zero_rms_norm_grad, L.zero_gated, L.zero_gated_grad, L.zero_gated_input_grad,
@@ -341,6 +352,7 @@ X, W, WF = z(4, 8), z(8), z(6, 8)
     (lambda: F.pack8(X), ValueError, "GPU"),
     (lambda: F.pack8(z(4, 8, dtype=torch.float64)), TypeError, "dtype"),
     (lambda: F.pack8(z(8, 4).t()), ValueError, "adjacent"),
+    (lambda: F.rms_norm(z(4, 0), eps=1e-5), ValueError, "no columns"),
     (lambda: F.pack8(X, out=F.packed8_empty((4, 9), "cpu")), ValueError, "codes must be"),
     (lambda: F.pack8(X, out=F.Packed8(z(4, 8), z(4, 1))), TypeError, "float8"),
     (lambda: F.pack8(X, out=F.Packed8(z(4, 8, dtype=torch.uint8), z(4, 2, dtype=torch.uint8))), ValueError, "one for each"),

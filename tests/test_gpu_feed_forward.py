@@ -808,6 +808,69 @@ def test_products_keep_apart_what_is_not_finite(dt):
         assert torch.equal(two[0][:, :-1], one[0][:, :-1]) and torch.equal(two[1][:-1, :-1], one[1][:-1, :-1])
 
 
+@pytest.mark.parametrize("t,d,f,dt", [(5, 33, 40, "f32"), (37, 64, 136, "bf16"), (70, 65, 33, "f16"), (300, 128, 264, "bf16")])
+def test_column_ranges_of_one_buffer(t, d, f, dt):
+    """Matrices that lie side by side in the rows of one buffer, read and written: what a call gives is what
+    it gives apart, and the columns between are left as they were."""
+    gen = torch.Generator(device="cuda").manual_seed(t)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(T[dt])  # noqa: E731
+
+    def beside(rows, *cols):
+        m = Mat(rows, sum(cols) + 3 * len(cols), dt)
+        at, out = 0, []
+        for c in cols:
+            out.append(m.v[:, at:at + c])
+            at += c + 3
+        return m, out
+
+    x, res, w, wg, wu = r(t, d), r(t, d), r(d), r(f, d), r(f, d)
+    m, (xs, rs, ts, ys) = beside(t, d, d, d, d)
+    xs.copy_(x), rs.copy_(res)
+    a, b = F.rms_norm(x, w, eps=1e-5, residual=res), F.rms_norm(xs, w, eps=1e-5, residual=rs, total=ts, out=ys)
+    assert torch.equal(ys, a.y) and torch.equal(ts, a.total) and torch.equal(b.rstd, a.rstd)
+    assert torch.equal(xs, x) and torch.equal(rs, res)
+    assert torch.isnan(m.v[:, d:d + 3]).all() and torch.isnan(m.v[:, -3:]).all()
+    dn, dres = r(t, d), r(t, d)
+    gw, hw = (torch.empty(d, device="cuda") for _ in range(2))
+    want = F.rms_norm_grad(dn, a.total, a.rstd, w, residual_grad=dres, weight_grad=gw)
+    xs.copy_(dn), rs.copy_(dres)
+    F.rms_norm_grad(xs, ts, a.rstd, w, residual_grad=rs, out=ys, weight_grad=hw)
+    assert torch.equal(ys, want) and torch.equal(gw, hw)
+    # weights in one [f, 2 d] buffer, gate, up and a in one [t, 3 f]
+    m, (gs, us) = beside(f, d, d)
+    gs.copy_(wg), us.copy_(wu)
+    m2, (as_, gate, up) = beside(t, f, f, f)
+    one, two = F.gated(x, wg, wu, keep="tensors"), F.gated(x, gs, us, out=as_, keep=(gate, up))
+    for p, q in zip(one, two):
+        close(q, f64(p), np.maximum(np.abs(f64(p)), 1.0) * (d + 40) * 8 * E + (0 if dt == "f32" else 2.0 ** -7 * np.abs(f64(p))))
+    assert torch.isnan(m2.v[:, f:f + 3]).all() and torch.isnan(m2.v[:, 2 * f + 3:2 * f + 6]).all()
+    da = r(t, f)
+    m3, (dg, du) = beside(t, f, f)
+    ref = F.gated_grad(da, gate.contiguous(), up.contiguous())
+    F.gated_grad(da, gate, up, out_gate=dg, out_up=du, again=as_)
+    assert torch.equal(dg, ref.gate) and torch.equal(du, ref.up)
+    # whole numbers: exact on every path
+    for v in (dg, du):
+        v.copy_(torch.randint(-2, 3, v.shape, generator=gen, device="cuda"))
+    xi, gi, ui = (torch.randint(-2, 3, s, generator=gen, device="cuda").to(T[dt]) for s in ((t, d), (f, d), (f, d)))
+    gs.copy_(gi), us.copy_(ui)
+    m4, (dx, other) = beside(t, d, d)
+    F.gated_input_grad(dg, du, gs, us, out=dx)
+    assert torch.equal(dx, (dg.double() @ gi.double() + du.double() @ ui.double()).to(T[dt]))
+    assert torch.isnan(other).all()
+    m5, (wgrad, ugrad) = beside(f, d, d)
+    F.gated_weight_grad(dg, du, xi, wgrad, ugrad)
+    assert torch.equal(wgrad, (dg.double().t() @ xi.double()).to(T[dt]))
+    assert torch.equal(ugrad, (du.double().t() @ xi.double()).to(T[dt]))
+    assert torch.isnan(m5.v[:, d:d + 3]).all()
+    codes = torch.zeros(t, 2 * f, dtype=torch.float8_e4m3fn, device="cuda")
+    blocks = OF.blocks(f)
+    scales = torch.zeros(t, 2 * blocks, dtype=torch.uint8, device="cuda")
+    for k, v in enumerate((dg, du)):
+        p = F.pack8(v, out=F.Packed8(codes[:, k * f:(k + 1) * f], scales[:, k * blocks:(k + 1) * blocks]))
+        assert torch.equal(F.unpack8(p, T[dt]), F.unpack8(F.pack8(v), T[dt]))
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, and a run of them together
 # ---------------------------------------------------------------------------

@@ -54,26 +54,43 @@ void advance(zk::Held& k, int64_t rows) {
 }
 
 // What a call reads and writes: no written range may meet another one, but for the pairs
-// that `same` allows.
+// that allow() names.  Matrices with one stride may lie side by side, as column ranges of one buffer do.
 struct Ranges {
   static constexpr int kMost = 24;
   Span s[kMost];
+  uintptr_t ld[kMost], width[kMost];  // bytes; 0: not a matrix
   bool written[kMost];
   int n = 0;
-  int add(const Span& x, bool w) {
+  int add(const Span& x, bool w, int64_t ld_bytes = 0, int64_t row_bytes = 0) {
     s[n] = x;
+    ld[n] = (uintptr_t)ld_bytes;
+    width[n] = (uintptr_t)row_bytes;
     written[n] = w;
     return n++;
+  }
+  int add(const void* p, int64_t rows, int64_t cols, int64_t ld_elements, int eb, bool w) {
+    return add(span(p, rows, cols, ld_elements, eb), w, ld_elements * eb, cols * eb);
+  }
+  int add_codes(const zero_held_t* h, int64_t rows, int64_t cols, bool w) {
+    return add(codes_span(h, rows, cols), w, h->ld_codes, cols);
+  }
+  int add_scales(const zero_held_t* h, int64_t rows, int64_t cols, bool w) {
+    return add(scales_span(h, rows, cols), w, h->ld_scales, blocks_of(cols));
   }
   uint32_t allowed[kMost] = {};
   void allow(int i, int j) {
     allowed[i] |= 1u << j;
     allowed[j] |= 1u << i;
   }
+  bool beside(int i, int j) const {
+    if (ld[i] == 0 || ld[i] != ld[j]) return false;
+    const uintptr_t d = s[j].lo >= s[i].lo ? (s[j].lo - s[i].lo) % ld[i] : (ld[i] - (s[i].lo - s[j].lo) % ld[i]) % ld[i];
+    return d >= width[i] && d + width[j] <= ld[i];
+  }
   bool clash() const {
     for (int i = 0; i < n; ++i)
       for (int j = 0; j < i; ++j)
-        if ((written[i] || written[j]) && !(allowed[i] >> j & 1) && overlap(s[i], s[j])) return true;
+        if ((written[i] || written[j]) && !(allowed[i] >> j & 1) && overlap(s[i], s[j]) && !beside(i, j)) return true;
     return false;
   }
 };
@@ -104,9 +121,9 @@ int hold(const char* fn, bool pack, void* x, int64_t ld_x, zero_dtype_t t, const
   if ((rc = held_matrix(fn, "held", held, rows, cols))) return rc;
   if (rows == 0) return ZERO_OK;
   Ranges r;
-  r.add(span(x, rows, cols, ld_x, bytes_of(t)), !pack);
-  r.add(codes_span(held, rows, cols), pack);
-  r.add(scales_span(held, rows, cols), pack);
+  r.add(x, rows, cols, ld_x, bytes_of(t), !pack);
+  r.add_codes(held, rows, cols, pack);
+  r.add_scales(held, rows, cols, pack);
   if (r.clash()) return error(fn, "what is written overlaps something else");
   zk::HoldLaunch a = hold_launch(x, ld_x, t, held, rows, cols);
   const int64_t per_launch = std::max<int64_t>(1, zk::kMaxUnits / a.groups.d);
@@ -147,18 +164,18 @@ int rms(const zero_rms_args_t* args, void* stream) {
   if (!A.out && !A.held) return error(fn, "neither out nor held is given");
   const int xb = bytes_of(A.x_dtype), rb = res ? bytes_of(A.res_dtype) : 0;
   Ranges r;
-  const int x = r.add(span(A.x, A.rows, A.cols, A.ld_x, xb), false);
+  const int x = r.add(A.x, A.rows, A.cols, A.ld_x, xb, false);
   if (A.weight) r.add(vector_span(A.weight, A.cols, A.weight_dtype), false);
   if (res) {
-    const int d = r.add(span(A.residual, A.rows, A.cols, A.ld_res, rb), false);
-    const int h = r.add(span(A.total, A.rows, A.cols, A.ld_total, rb), true);
+    const int d = r.add(A.residual, A.rows, A.cols, A.ld_res, rb, false);
+    const int h = r.add(A.total, A.rows, A.cols, A.ld_total, rb, true);
     if (in_place(A.total, A.ld_total, A.res_dtype, A.x, A.ld_x, A.x_dtype, A.rows)) r.allow(h, x);
     if (in_place(A.total, A.ld_total, A.res_dtype, A.residual, A.ld_res, A.res_dtype, A.rows)) r.allow(h, d);
   }
-  if (A.out) r.add(span(A.out, A.rows, A.cols, A.ld_out, bytes_of(A.out_dtype)), true);
+  if (A.out) r.add(A.out, A.rows, A.cols, A.ld_out, bytes_of(A.out_dtype), true);
   if (A.held) {
-    r.add(codes_span(A.held, A.rows, A.cols), true);
-    r.add(scales_span(A.held, A.rows, A.cols), true);
+    r.add_codes(A.held, A.rows, A.cols, true);
+    r.add_scales(A.held, A.rows, A.cols, true);
   }
   if (A.rstd) r.add(span(A.rstd, A.rows * 4), true);
   if (r.clash()) return error(fn, "what is written overlaps something else");
@@ -224,20 +241,20 @@ int rms_grad(const zero_rms_grad_args_t* args, void* stream) {
   }
   const int yb = bytes_of(A.dy_dtype), hb = bytes_of(A.h_dtype);
   Ranges r;
-  const int dy = r.add(span(A.dy, A.rows, A.cols, A.ld_dy, yb), false);
-  const int dh = r.add(span(A.dh, A.rows, A.cols, A.ld_dh, hb), true);
+  const int dy = r.add(A.dy, A.rows, A.cols, A.ld_dy, yb, false);
+  const int dh = r.add(A.dh, A.rows, A.cols, A.ld_dh, hb, true);
   if (in_place(A.dh, A.ld_dh, A.h_dtype, A.dy, A.ld_dy, A.dy_dtype, A.rows)) r.allow(dh, dy);
   if (A.h) {
-    const int h = r.add(span(A.h, A.rows, A.cols, A.ld_h, hb), false);
+    const int h = r.add(A.h, A.rows, A.cols, A.ld_h, hb, false);
     if (in_place(A.dh, A.ld_dh, A.h_dtype, A.h, A.ld_h, A.h_dtype, A.rows)) r.allow(dh, h);
   }
   if (A.dres) {
-    const int d = r.add(span(A.dres, A.rows, A.cols, A.ld_dres, hb), false);
+    const int d = r.add(A.dres, A.rows, A.cols, A.ld_dres, hb, false);
     if (in_place(A.dh, A.ld_dh, A.h_dtype, A.dres, A.ld_dres, A.h_dtype, A.rows)) r.allow(dh, d);
   }
   if (A.held && A.rows > 0) {
-    r.add(codes_span(A.held, A.rows, A.cols), false);
-    r.add(scales_span(A.held, A.rows, A.cols), false);
+    r.add_codes(A.held, A.rows, A.cols, false);
+    r.add_scales(A.held, A.rows, A.cols, false);
   }
   if (A.rows > 0) r.add(vector_span(A.rstd, A.rows, ZERO_F32), false);
   if (A.weight) r.add(vector_span(A.weight, A.cols, A.weight_dtype), false);
@@ -314,18 +331,18 @@ int gated(const zero_gated_args_t* args, void* stream) {
   if (A.u8 && (rc = held_matrix(fn, "u8", A.u8, A.tokens, A.hidden))) return rc;
   if (A.tokens == 0) return ZERO_OK;
   Ranges r;
-  r.add(span(A.x, A.tokens, A.dim, A.ld_x, eb), false);
-  r.add(span(A.w_gate, A.hidden, A.dim, A.ld_w_gate, eb), false);
-  r.add(span(A.w_up, A.hidden, A.dim, A.ld_w_up, eb), false);
-  r.add(span(A.a, A.tokens, A.hidden, A.ld_a, eb), true);
+  r.add(A.x, A.tokens, A.dim, A.ld_x, eb, false);
+  r.add(A.w_gate, A.hidden, A.dim, A.ld_w_gate, eb, false);
+  r.add(A.w_up, A.hidden, A.dim, A.ld_w_up, eb, false);
+  r.add(A.a, A.tokens, A.hidden, A.ld_a, eb, true);
   if (A.g) {
-    r.add(span(A.g, A.tokens, A.hidden, A.ld_g, eb), true);
-    r.add(span(A.u, A.tokens, A.hidden, A.ld_u, eb), true);
+    r.add(A.g, A.tokens, A.hidden, A.ld_g, eb, true);
+    r.add(A.u, A.tokens, A.hidden, A.ld_u, eb, true);
   }
   if (A.g8)
     for (const zero_held_t* h : {A.g8, A.u8}) {
-      r.add(codes_span(h, A.tokens, A.hidden), true);
-      r.add(scales_span(h, A.tokens, A.hidden), true);
+      r.add_codes(h, A.tokens, A.hidden, true);
+      r.add_scales(h, A.tokens, A.hidden, true);
     }
   if (r.clash()) return error(fn, "what is written overlaps something else");
 
@@ -380,11 +397,11 @@ int gated_grad(const zero_gated_args_t* args, void* stream) {
     int64_t ld;
     int at;
   } in[3] = {{A.da, A.ld_da, 0}, {A.g, A.ld_g, 0}, {A.u, A.ld_u, 0}};
-  for (In& i : in) i.at = i.p ? r.add(span(i.p, n, h, i.ld, eb), false) : -1;
+  for (In& i : in) i.at = i.p ? r.add(i.p, n, h, i.ld, eb, false) : -1;
   if (A.g8)
     for (const zero_held_t* k : {A.g8, A.u8}) {
-      r.add(codes_span(k, n, h), false);
-      r.add(scales_span(k, n, h), false);
+      r.add_codes(k, n, h, false);
+      r.add_scales(k, n, h, false);
     }
   const struct {
     void* p;
@@ -392,7 +409,7 @@ int gated_grad(const zero_gated_args_t* args, void* stream) {
   } out[3] = {{A.dg, A.ld_dg}, {A.du, A.ld_du}, {A.a, A.ld_a}};
   for (const auto& o : out) {
     if (!o.p) continue;
-    const int at = r.add(span(o.p, n, h, o.ld, eb), true);
+    const int at = r.add(o.p, n, h, o.ld, eb, true);
     for (const In& i : in)
       if (i.p && in_place(o.p, o.ld, A.dtype, i.p, i.ld, A.dtype, n)) r.allow(at, i.at);
   }
@@ -465,11 +482,11 @@ int input_grad(const zero_gated_args_t* args, void* stream) {
   const int64_t need = zero_gated_ws_bytes(A.tokens, A.dim, A.hidden);
   if ((rc = workspace(fn, A, need))) return rc;
   Ranges r;
-  r.add(span(A.dg, A.tokens, A.hidden, A.ld_dg, eb), false);
-  r.add(span(A.du, A.tokens, A.hidden, A.ld_du, eb), false);
-  r.add(span(A.w_gate, A.hidden, A.dim, A.ld_w_gate, eb), false);
-  r.add(span(A.w_up, A.hidden, A.dim, A.ld_w_up, eb), false);
-  r.add(span(A.dx, A.tokens, A.dim, A.ld_dx, eb), true);
+  r.add(A.dg, A.tokens, A.hidden, A.ld_dg, eb, false);
+  r.add(A.du, A.tokens, A.hidden, A.ld_du, eb, false);
+  r.add(A.w_gate, A.hidden, A.dim, A.ld_w_gate, eb, false);
+  r.add(A.w_up, A.hidden, A.dim, A.ld_w_up, eb, false);
+  r.add(A.dx, A.tokens, A.dim, A.ld_dx, eb, true);
   r.add(span(A.ws, need), true);
   if (r.clash()) return error(fn, "what is written overlaps something else");
   zk::ProductLaunch a{};
@@ -509,11 +526,11 @@ int weight_grad(const zero_gated_args_t* args, void* stream) {
   if ((rc = workspace(fn, A, need))) return rc;
   const int wb = bytes_of(A.dw_dtype);
   Ranges r;
-  r.add(span(A.dg, A.tokens, A.hidden, A.ld_dg, eb), false);
-  r.add(span(A.du, A.tokens, A.hidden, A.ld_du, eb), false);
-  r.add(span(A.x, A.tokens, A.dim, A.ld_x, eb), false);
-  r.add(span(A.dw_gate, A.hidden, A.dim, A.ld_dw_gate, wb), true);
-  r.add(span(A.dw_up, A.hidden, A.dim, A.ld_dw_up, wb), true);
+  r.add(A.dg, A.tokens, A.hidden, A.ld_dg, eb, false);
+  r.add(A.du, A.tokens, A.hidden, A.ld_du, eb, false);
+  r.add(A.x, A.tokens, A.dim, A.ld_x, eb, false);
+  r.add(A.dw_gate, A.hidden, A.dim, A.ld_dw_gate, wb, true);
+  r.add(A.dw_up, A.hidden, A.dim, A.ld_dw_up, wb, true);
   r.add(span(A.ws, need), true);
   if (r.clash()) return error(fn, "what is written overlaps something else");
   zk::ProductLaunch a{};

@@ -17,7 +17,7 @@ stream of the tensors' device); every step of the computation runs in libzero_sh
     dh = rms_norm_grad(dn, n.total, n.rstd, w_norm, residual_grad=d, weight_grad=grad_norm)
 
 Matrices [..., cols] are rows of the last dimension; one that is not contiguous has to
-have two dimensions and adjacent columns.  The calls record no history for autograd: a loop
+have two dimensions and adjacent columns.  Inputs and results may be column ranges of one buffer.  The calls record no history for autograd: a loop
 calls the backward pass itself, or from a torch.autograd.Function.  With grad mode on, a
 tensor that requires grad is refused, since its gradient would be lost without a sign.
 """
@@ -193,6 +193,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
     bits too, or only.  rstd: fp32, [...]; False leaves it out.
     """
     n, cols, ld_x = _rows(x, "x")
+    if cols == 0:
+        raise ValueError("x has no columns")
     shape = x.shape
     xc = _code(x.dtype)
     ptr_r = ld_r = ptr_t = ld_t = 0
@@ -228,7 +230,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
         if scale.shape != shape[:-1] or scale.dtype != torch.float32 or not scale.is_contiguous():
             raise ValueError("rstd must be contiguous fp32 of x's shape without the columns")
     dev = _one_device(x, residual, total, weight, y, keep, scale)
-    if n and cols:
+    if n:
         _call(_abi.lib().zero_rms_norm, dev, _RMS.pack(
             x.data_ptr(), ld_x, xc, rc, ptr_r, ld_r, ptr_t, ld_t, ptr_w, wc, yc, ptr_y, ld_y,
             0 if held is None else ctypes.addressof(held), 0 if scale is None else scale.data_ptr(), n, cols, eps))
