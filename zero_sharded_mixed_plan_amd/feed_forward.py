@@ -94,7 +94,7 @@ def _packed8(shape, like: torch.Tensor) -> Packed8:
 
 def _held(p: Packed8, rows: int, cols: int, shape, what: str) -> _abi.zero_held_t:
     """The C struct of a Packed8 of this shape."""
-    codes, scales = p
+    codes, scales = p.codes, p.scales
     if codes.dtype not in _CODE_TYPES or scales.dtype not in _SCALE_TYPES:
         raise TypeError(f"{what}: codes must be float8_e4m3fn or uint8, scales float8_e8m0fnu or uint8")
     if codes.shape != shape or scales.shape != (*shape[:-1], (cols + BLOCK - 1) // BLOCK):
@@ -111,11 +111,11 @@ def _is_packed(t) -> bool:
 
 
 def _one_device(first: torch.Tensor, *others) -> int:
-    """The index of the one GPU of tensors, Packed8s and Nones."""
+    """The index of the one GPU of what a caller gave: tensors, Packed8s and Nones."""
     dev = first.get_device()
     history, stranger = first.requires_grad, None
     for t in others:
-        if t is None:
+        if t is None or t is True or t is False:
             continue
         if isinstance(t, Packed8):
             _one_device(first, *t)
@@ -158,7 +158,7 @@ def pack8(x: torch.Tensor, *, out: Optional[Packed8] = None) -> Packed8:
     code = _code(x.dtype)
     p = _packed8(x.shape, x) if out is None else out
     held = _held(p, n, cols, x.shape, "out")
-    dev = _one_device(x, p)
+    dev = _one_device(x, out)
     if n and cols:
         _call(_abi.lib().zero_pack8, dev, x.data_ptr(), ld, code, n, cols, ctypes.addressof(held))
     return p
@@ -170,8 +170,9 @@ def unpack8(p: Packed8, dtype: Optional[torch.dtype] = None, *, out: Optional[to
     code = _code(dtype)
     n, cols, _ = _rows(p.codes, "codes")
     held = _held(p, n, cols, p.codes.shape, "p")
+    given = out
     out, ld = _result(out, p.codes.shape, dtype, p.codes, "out")
-    dev = _one_device(out, p)
+    dev = _one_device(p.codes, p.scales, given)
     if n and cols:
         _call(_abi.lib().zero_unpack8, dev, ctypes.addressof(held), n, cols, out.data_ptr(), ld, code)
     return out
@@ -198,12 +199,14 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
     shape = x.shape
     xc = _code(x.dtype)
     ptr_r = ld_r = ptr_t = ld_t = 0
+    given_total = None
     rc = xc
     if residual is not None:
         if residual.shape != shape:
             raise ValueError("x and residual must have one shape")
         rc = _code(residual.dtype)
         ld_r = _rows(residual, "residual")[2]
+        given_total = total
         total, ld_t = _result(total, shape, residual.dtype, x, "total")
         ptr_r, ptr_t = residual.data_ptr(), total.data_ptr()
     elif total is not None:
@@ -225,11 +228,13 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
     if y is None and keep is None:
         raise ValueError("neither out nor packed is asked for")
     scale = None
-    if rstd is not False:
-        scale = x.new_empty(shape[:-1], dtype=torch.float32) if rstd is True else rstd
+    if rstd is True:
+        scale = x.new_empty(shape[:-1], dtype=torch.float32)
+    elif rstd is not False:
+        scale = rstd
         if scale.shape != shape[:-1] or scale.dtype != torch.float32 or not scale.is_contiguous():
             raise ValueError("rstd must be contiguous fp32 of x's shape without the columns")
-    dev = _one_device(x, residual, total, weight, y, keep, scale)
+    dev = _one_device(x, residual, weight, given_total, out, packed, rstd)
     if n:
         _call(_abi.lib().zero_rms_norm, dev, _RMS.pack(
             x.data_ptr(), ld_x, xc, rc, ptr_r, ld_r, ptr_t, ld_t, ptr_w, wc, yc, ptr_y, ld_y,
@@ -295,8 +300,9 @@ def rms_norm_grad(dy: torch.Tensor, h: Union[torch.Tensor, Packed8], rstd: torch
         ptr_dw, dwc = weight_grad.data_ptr(), _code(weight_grad.dtype)
     elif accumulate:
         raise ValueError("accumulate without a weight_grad")
+    given = out
     out, ld_out = _result(out, shape, dt, dy, "out")
-    dev = _one_device(dy, h, rstd, weight, residual_grad, out, weight_grad, workspace)
+    dev = _one_device(dy, h, rstd, weight, residual_grad, given, weight_grad, workspace)
     if cols == 0 or (n == 0 and weight_grad is None):
         return out
     L = _abi.lib()
@@ -371,7 +377,8 @@ def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, act: str
     elif keep is not None:
         gate, up = keep
     pg, ldg, pu, ldu, g8, u8, held = _kept(gate, up, n, hidden, shape, x)
-    dev = _one_device(x, w_gate, w_up, a, gate, up)
+    dev = _one_device(x, w_gate, w_up, out) if keep is None or isinstance(keep, str) else \
+        _one_device(x, w_gate, w_up, out, gate, up)
     if n and hidden:
         if dim == 0:
             raise ValueError("the weights have no columns")
@@ -399,7 +406,7 @@ def gated_grad(da: torch.Tensor, gate: Union[torch.Tensor, Packed8], up: Union[t
     if again is not False:
         a, ld_a = _result(None if again is True else again, shape, da.dtype, da, "again")
         ptr_a = a.data_ptr()
-    dev = _one_device(da, gate, up, dg, du, a)
+    dev = _one_device(da, gate, up, out_gate, out_up, again)
     if n and hidden:
         _call(_abi.lib().zero_gated_grad, dev, _GATED.pack(
             n, 0, hidden, code, kind, *_ZEROS[6], ptr_a, ld_a, pg, ldg, pu, ldu, g8, u8, da.data_ptr(), ld_da,
@@ -432,7 +439,7 @@ def gated_input_grad(dg: torch.Tensor, du: torch.Tensor, w_gate: torch.Tensor, w
         raise ValueError("the gradients and the weights must have one hidden size")
     code = _code(dg.dtype)
     dx, ld_dx = _result(out, (*dg.shape[:-1], dim), dg.dtype, dg, "out")
-    dev = _one_device(dg, du, w_gate, w_up, dx, workspace)
+    dev = _one_device(dg, du, w_gate, w_up, out, workspace)
     if n == 0 or dim == 0:
         return dx
     if hidden == 0:
