@@ -660,6 +660,32 @@ def test_products_random(t, d, f, dt):
     assert torch.equal(a, gg) and torch.equal(b, gu)
 
 
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("t,d,f", [(20, 48, 64), (130, 33, 77), (3, 260, 129)])
+def test_products_against_differences(t, d, f, kind):
+    """The gradients of x and both weights along a direction in all of them, from kept tensors, against central
+    differences of the forward pass; their third-order error is bounded by that of twice the step."""
+    g = torch.Generator(device="cuda").manual_seed(t)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, wg, wu, c = r(t, d), r(f, d) * d ** -0.5, r(f, d) * d ** -0.5, r(t, f)
+    v, vg, vu = r(t, d), r(f, d) * d ** -0.5, r(f, d) * d ** -0.5
+    k = F.gated(x, wg, wu, act=kind, keep="tensors")
+    b = F.gated_grad(c, k.gate, k.up, act=kind)
+    dx = F.gated_input_grad(b.gate, b.up, wg, wu)
+    gg, gu = torch.empty_like(wg), torch.empty_like(wu)
+    F.gated_weight_grad(b.gate, b.up, x, gg, gu)
+    terms = [(p.double() * q.double()) for p, q in ((dx, v), (gg, vg), (gu, vu))]
+    got = float(sum(p.sum() for p in terms))
+    loss = lambda s: float((F.gated(x + s * v, wg + s * vg, wu + s * vu, act=kind).a.double() * c.double()).sum())  # noqa: E731
+    s = 2.0 ** -8
+    num, num2 = ((loss(i * s) - loss(-i * s)) / (2 * i * s) for i in (1, 2))
+    # a is off by some (3 d + 20) e of the sums of magnitudes, here of size d^(1/2) at most 4 each, at random
+    size = float((k.a.double() * c.double()).abs().sum() + c.double().abs().sum())
+    noise = (3 * d + 20) * E * size / s + 3 * (d + f + t) * E * float(sum(p.abs().sum() for p in terms))
+    assert abs(got - num) <= abs(num2 - num) + noise
+    assert noise <= 0.1 * abs(got) + 0.02 * float(sum(p.abs().sum() for p in terms))  # it says something
+
+
 def test_products_empty_and_special():
     e = torch.empty(0, 24, device="cuda").bfloat16()
     w = torch.randn(24, 40, device="cuda").bfloat16()
@@ -975,6 +1001,69 @@ def test_graph_replays():
             for a, b in zip(got, want):
                 assert torch.equal(a, b), turn
             torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_graph_replays_of_other_forms(dt):
+    """Odd widths, few tokens, split sums and accumulated gradients, captured together on one workspace."""
+    sizes = [(33, 137, 201), (300, 64, 3000), (5, 96, 1040), (700, 130, 66)]
+    ws = F.gated_workspace(700, 137, 3000), F.rms_norm_grad_workspace(700, 137)
+
+    def run(p, grads, acc):
+        n = F.rms_norm(p["x"], p["w_norm"], eps=1e-5, residual=p["res"], packed=True)
+        f = F.gated(n.y, p["wg"], p["wu"], act="gelu", keep="packed")
+        b = F.gated_grad(f.a, f.gate, f.up, act="gelu", again=True)
+        dn = F.gated_input_grad(b.gate, b.up, p["wg"], p["wu"], workspace=ws[0])
+        F.gated_weight_grad(b.gate, b.up, n.y, grads["wg"], grads["wu"], accumulate=acc, workspace=ws[0])
+        dh = F.rms_norm_grad(dn, n.total, n.rstd, p["w_norm"], residual_grad=p["dout"], weight_grad=grads["norm"],
+                             accumulate=acc, workspace=ws[1])
+        return [f.a, b.a, dn, dh]
+
+    ps, gs = zip(*(make_block(*s, dt)[:2] for s in sizes))
+    for p, g in zip(ps, gs):
+        run(p, g, False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = []
+        for p, g in zip(ps, gs):
+            run(p, g, False)
+            outs.append(run(p, g, True))
+    for turn in range(4):
+        fresh = [make_block(*s, dt, seed=20 + turn)[0] for s in sizes]
+        for p, q in zip(ps, fresh):
+            for k in p:
+                p[k].copy_(q[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in o] + [g[k].clone() for k in ("wg", "wu", "norm")] for o, g in zip(outs, gs)]
+        for q, g, have in zip(fresh, gs, got):
+            other = {k: torch.empty_like(v) for k, v in g.items()}
+            run(q, other, False)
+            want = run(q, other, True) + [other[k] for k in ("wg", "wu", "norm")]
+            for a, b in zip(have, want):
+                assert torch.equal(a, b), turn
+
+
+def test_two_streams_at_once():
+    """Calls of two streams at the same time, each with a workspace of its own, give what they give alone."""
+    sizes = [(300, 512, 1376), (2000, 136, 264)]
+    jobs = [make_block(*s, "bf16", seed=i) for i, s in enumerate(sizes)]
+    want = []
+    for p, grads, ws in jobs:
+        out = [t.clone() for t in block(**p, grads=grads, ws=ws)]
+        want.append(out + [grads[k].clone() for k in sorted(grads)])
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for (p, grads, ws), s in zip(jobs, streams):
+            with torch.cuda.stream(s):
+                got.append(list(block(**p, grads=grads, ws=ws)))
+        torch.cuda.synchronize()
+        for (p, grads, ws), have, w in zip(jobs, got, want):
+            for a, b in zip(have + [grads[k] for k in sorted(grads)], w):
+                assert torch.equal(a, b)
 
 
 def test_training_with_the_sharded_step():
