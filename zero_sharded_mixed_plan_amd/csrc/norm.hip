@@ -8,8 +8,8 @@
 // registers for the row's sum.  In 8-bit codes a last bit decides which of two values 2^-4 apart is
 // stored, so rstd and y must not hang on how a row is split over lanes and waves: squares are summed in
 // fp64, and y is computed in pairs of fp32 numbers (good to 2^-44), rounded once to
-// fp32.  8192 x 4096 bf16: with a residual 56 us (4.8 TB/s), and codes 62, without 32; all in fp64,
-// whose conversions are slow, 62 and, without, 36.
+// fp32.  8192 x 4096 bf16, without a pause: with a residual 44 us, without 26 (55 and 30 one by one); all in
+// fp64, whose conversions are slow, 36 without.
 #include <algorithm>
 
 #include "held.h"
@@ -46,19 +46,6 @@ __global__ __launch_bounds__(rms_threads(WAVES), 4) void rms_kernel(const RmsLau
     const u32 col = (c * kRow + t) * 8;
     n[c] = col < a.cols ? min(a.cols - col, 8u) : 0;
     if (a.weight) load8_as(a.weight + (int64_t)col * one_bytes(a.weight_type), a.weight_end, a.weight_type, n[c], rw[c]);
-  }
-  // |n| <= sqrt(8192): only weights from 2^121 on make an infinity of it
-  bool large = false;
-  if (a.weight) {
-    float top = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float w[8];
-      values8_as(rw[c], a.weight_type, n[c], w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(w[j]));
-    }
-    large = __builtin_amdgcn_ballot_w64(top >= 0x1p121f);
   }
   const int64_t stride = (int64_t)gridDim.x * kRows;
   struct Row {
@@ -118,34 +105,32 @@ __global__ __launch_bounds__(rms_threads(WAVES), 4) void rms_kernel(const RmsLau
     if (!exists) continue;
     const RmsLaunch& b = argument<RmsLaunch>();
     const double rstd = inverse_root(sum * b.per_col + b.eps);
-    const float r_hi = (float)rstd, r_lo = (float)(rstd - (double)r_hi);
-    if (b.rstd && t == 0) b.rstd[row] = r_hi;
-    // n = h * rstd is of size one whatever its factors are, but pairs of fp32 cannot hold an rstd near the
-    // ends of fp32
-    const bool far = large || !(rstd >= 0x1p-100 && rstd <= 0x1p100);
+    if (b.rstd && t == 0) b.rstd[row] = (float)rstd;
+    // The row is scaled by rstd's power of two first, exactly, so that neither an rstd near the ends of
+    // fp32 nor its second part is lost: n = h * rstd is of size one.
+    const int e = __builtin_amdgcn_frexp_exp(rstd);
+    const double m = __builtin_amdgcn_frexp_mant(rstd);
+    const float m_hi = (float)m, m_lo = (float)(m - (double)m_hi);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float y[8], w[8];
-      if (a.weight) values8_as(rw[c], a.weight_type, 8, w);
-      if (__builtin_amdgcn_ballot_w64(far)) {
+      float y[8];
+      if (a.weight) {
+        float w[8];
+        values8_as(rw[c], a.weight_type, 8, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float one = h[c][j];
-          asm volatile("" : "+v"(one));  // not the squares' conversion, held in two registers until here
-          const double d = (double)one * rstd;
-          y[j] = (float)(a.weight ? d * (double)w[j] : d);
+          const float s = __builtin_amdgcn_ldexpf(h[c][j], e);
+          const float p = s * m_hi;
+          const float p_lo = __builtin_fmaf(s, m_lo, __builtin_fmaf(s, m_hi, -p));
+          // bounded, or an infinite weight times a second part of 0, or of the other sign, would not be a number
+          const float q_lo = __builtin_amdgcn_fmed3f(w[j] * p_lo, -0x1.fffffep127f, 0x1.fffffep127f);
+          y[j] = __builtin_fmaf(w[j], p, q_lo);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float p = h[c][j] * r_hi;
-          const float p_lo = __builtin_fmaf(h[c][j], r_lo, __builtin_fmaf(h[c][j], r_hi, -p));
-          if (a.weight) {
-            const float q = w[j] * p;
-            y[j] = q + __builtin_fmaf(w[j], p_lo, __builtin_fmaf(w[j], p, -q));
-          } else {
-            y[j] = p + p_lo;
-          }
+          const float s = __builtin_amdgcn_ldexpf(h[c][j], e);
+          y[j] = __builtin_fmaf(s, m_hi, s * m_lo);
         }
       }
       clear_tail(y, n[c]);  // infinity times the zeros there
@@ -164,7 +149,7 @@ void rms_as(const RmsLaunch& a, hipStream_t s) {
     hipLaunchKernelGGL((rms_kernel<XT, RT, W, C, HELD>), dim3(grid), dim3(rms_threads(W)), 0, s, a);
   };
   // 16 bytes of a row a lane and vector: two groups of 16-bit columns (8192 x 4096 bf16 without a residual 29 us,
-  // with one 33, before the rows that take fp64), one of fp32 (4096 x 4096 24 us, with two 30)
+  // with one 33), one of fp32 (4096 x 4096 24 us, with two 30)
   constexpr int C = XT::bytes == 4 ? 1 : 2;
   using Groups = std::integral_constant<int, C>;
   if (a.cols <= 512) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
