@@ -44,39 +44,40 @@ __device__ __forceinline__ vec4 unit_of(const char* p, const char* end, u32 n) {
 // tiles
 // ---------------------------------------------------------------------------
 
-// Tiles of 128 x 128 results (of gate and up in the forward pass 128 x 64 each), four waves
-// of 64 x 64.  The operands go through registers, which takes any address, two steps before they
+// Tiles of SIDE x SIDE results, 128 (of gate and up in the forward pass 128 x 64 each) or 64, four waves of a quarter
+// each.  The operands go through registers, which takes any address, two steps before they
 // are multiplied, into one of two tiles in LDS; a step has one barrier.  fp32 tiles lie as 16-bit
 // ones do where their rows are of k: a matrix instruction's k are one element of every unit that the
 // lanes read.  4096 tokens of bf16, 2049 x 5503: forward 290 us, input gradient 410, weight
 // gradient 306 (637, 451 and 603 TFLOP/s; two tiles share a CU, and its L1 takes two lines for every 128
 // bytes that begin inside one); tiles of 64 x 64, loaded one step ahead under masks, took 640, 1118
 // and 1510.  1024 tokens of fp32, 2048 x 5504: 385, 382 and 415 us, of a floor of 295 at the rate of fp32
-// matrix instructions.  Rows of the other index, [32 k][128] fp32, are read element by element; every
+// matrix instructions.  Rows of the other index, [32 k][SIDE] fp32, are read element by element; every
 // second four of them have their halves of 64 columns in turn exchanged by 32, so that the two halves
 // of a wave meet different banks.
-constexpr int kSide = 128, kOperand = kSide * 128;
+template <int SIDE>
+constexpr int kOperand = SIDE * 128;  // bytes
 
-template <class T, bool BY_K>
-constexpr u32 kLanes = BY_K ? 8 : kSide / kUnit<T>;  // of a row
-template <class T, bool BY_K>
-constexpr u32 kRowsEach = 256 / kLanes<T, BY_K>;     // rows of a round; four rounds are a tile
+template <class T, bool BY_K, int SIDE>
+constexpr u32 kLanes = BY_K ? 8 : SIDE / kUnit<T>;      // of a row
+template <class T, bool BY_K, int SIDE>
+constexpr u32 kRowsEach = 256 / kLanes<T, BY_K, SIDE>;  // rows of a round; SIDE / 32 rounds are a tile
 
 // This thread's place in LDS of the first round; each round is 4096 bytes further.
-template <class T, bool BY_K>
+template <class T, bool BY_K, int SIDE>
 __device__ __forceinline__ u32 put_at() {
-  const u32 t = threadIdx.x, row = t / kLanes<T, BY_K>, unit = t % kLanes<T, BY_K>;
+  const u32 t = threadIdx.x, row = t / kLanes<T, BY_K, SIDE>, unit = t % kLanes<T, BY_K, SIDE>;
   if constexpr (BY_K) return row * 128 + (unit ^ (row / 2 % 8)) * 16;
-  else if constexpr (T::bytes == 2) return row * 256 + (unit ^ swizzle<kSide>(row)) * 16;
-  else return row * 512 + (unit ^ (row / 4 % 2 * 8)) * 16;
+  else if constexpr (T::bytes == 2) return row * (SIDE * 2) + (unit ^ swizzle<SIDE>(row)) * 16;
+  else return row * (SIDE * 4) + (unit ^ (row / 4 % 2 * 8)) * 16;
 }
 
 // Whole steps are loaded with neither branches nor masks: rows (columns) beyond the matrix's ni are replaced by others
 // of it, and units that begin in a row of columns may read on into the next row; what comes of either is
 // not stored.  The byte offset of this thread's unit of round q of a tile that begins at i0:
-template <class T, bool BY_K>
+template <class T, bool BY_K, int SIDE>
 __device__ __forceinline__ int64_t offset_of(int q, int64_t ld, int64_t i0, int64_t ni) {
-  const u32 t = threadIdx.x, row = q * kRowsEach<T, BY_K> + t / kLanes<T, BY_K>, unit = t % kLanes<T, BY_K>;
+  const u32 t = threadIdx.x, row = q * kRowsEach<T, BY_K, SIDE> + t / kLanes<T, BY_K, SIDE>, unit = t % kLanes<T, BY_K, SIDE>;
   if constexpr (BY_K) return min((int64_t)row, ni - 1 - i0) * ld + unit * 16;
   else return (int64_t)row * ld + (i0 + unit * kUnit<T> < ni ? unit * 16 : 0);
 }
@@ -87,39 +88,39 @@ __device__ __forceinline__ int64_t whole_steps(int64_t ni, int64_t nk) {
 }
 
 // This thread's unit of round q of any step: from k0 on, of a matrix at p with ni rows (columns) and nk of k.
-template <class T, bool BY_K>
+template <class T, bool BY_K, int SIDE>
 __device__ __forceinline__ vec4 edge_unit(int q, const char* p, const char* end, int64_t ld, int64_t i0, int64_t ni, int64_t k0,
                                           int64_t nk) {
-  const u32 t = threadIdx.x, row = q * kRowsEach<T, BY_K> + t / kLanes<T, BY_K>, unit = t % kLanes<T, BY_K> * kUnit<T>;
+  const u32 t = threadIdx.x, row = q * kRowsEach<T, BY_K, SIDE> + t / kLanes<T, BY_K, SIDE>, unit = t % kLanes<T, BY_K, SIDE> * kUnit<T>;
   const int64_t i = i0 + (BY_K ? row : unit), k = k0 + (BY_K ? unit : row), left = BY_K ? nk - k : ni - i;
   const int64_t at = BY_K ? i * ld + k * T::bytes : k * ld + i * T::bytes;
   return unit_of<T>(p + at, end, i < ni && k < nk ? (u32)min(left, (int64_t)kUnit<T>) : 0);
 }
 
 // This lane's offset of the block of 32 rows (columns) from i0 on.
-template <class T, bool BY_K>
+template <class T, bool BY_K, int SIDE>
 __device__ __forceinline__ u32 any_offset(u32 i0) {
   const u32 lane = threadIdx.x & 63;
   if constexpr (BY_K || T::bytes == 2) {
     u32 at[1];
-    block_offsets<kSide, BY_K>(at, i0);
+    block_offsets<SIDE, BY_K>(at, i0);
     return at[0];
   } else {
-    return lane / 32 * 2048 + ((i0 + lane % 32) ^ (lane / 32 * 32)) * 4;
+    return lane / 32 * (SIDE * 16) + ((i0 + lane % 32) ^ (lane / 32 * 32)) * 4;
   }
 }
 
 // Part s of a step's four: lane l has row (column) l % 32 and a unit of k.
-template <class T, bool BY_K>
+template <class T, bool BY_K, int SIDE>
 __device__ __forceinline__ vec4 any_fragment(const char* lds, u32 at, u32 s) {
   if constexpr (BY_K) {
-    return __builtin_bit_cast(vec4, fragment<kSide, true>(lds, at, s));
+    return __builtin_bit_cast(vec4, fragment<SIDE, true>(lds, at, s));
   } else if constexpr (T::bytes == 2) {
-    return __builtin_bit_cast(vec4, fragment<kSide, false>(lds + s / 2 * 8192, at, s % 2));
+    return __builtin_bit_cast(vec4, fragment<SIDE, false>(lds, at, s));
   } else {
     vec4 v;
 #pragma unroll
-    for (u32 j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const u32*>(lds + at + s * 4096 + j * 512);
+    for (u32 j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const u32*>(lds + at + s * (SIDE * 32) + j * (SIDE * 4));
     return v;
   }
 }
@@ -136,42 +137,47 @@ __device__ __forceinline__ f32x16 any_mfma32(vec4 p, vec4 q, f32x16 acc) {
   }
 }
 
-template <class T, Product KIND>
-__global__ __launch_bounds__(256, 2) void any_kernel(const ProductLaunch a, u32 down, u32 across, u32 splits) {
+template <class T, Product KIND, int SIDE>
+__global__ __launch_bounds__(256, SIDE == 128 ? 2 : 4) void any_kernel(const ProductLaunch a, u32 down, u32 across, u32 splits) {
   constexpr bool kQByK = KIND != kWeight, kPByK = KIND == kForward;
-  __shared__ __attribute__((aligned(128))) char s0[2 * kOperand], s1[2 * kOperand];  // P, then Q
+  constexpr int B = SIDE / 64, R = SIDE / 32;  // blocks of a wave, rounds of an operand
+  static_assert(KIND != kForward || B == 2, "a wave has a block of gate and one of up");
+  __shared__ __attribute__((aligned(128))) char s0[2 * kOperand<SIDE>], s1[2 * kOperand<SIDE>];  // P, then Q
   const u32 halves = KIND == kWeight ? 2 : 1;
   const u32 split = KIND == kForward ? 0 : blockIdx.x / (down * halves * across);
   u32 tr, tc;
   tile_of(KIND == kForward ? blockIdx.x : blockIdx.x % (down * halves * across), down * halves, across, tr, tc);
   const int which = KIND == kWeight && tr >= down;
-  const int64_t r0 = (int64_t)(tr - which * down) * kSide, c0 = (int64_t)tc * (KIND == kForward ? kSide / 2 : kSide);
+  const int64_t r0 = (int64_t)(tr - which * down) * SIDE, c0 = (int64_t)tc * (KIND == kForward ? SIDE / 2 : SIDE);
   const u32 wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), wc = wave % 2, wr = wave / 2;
 
-  const u32 at_p[2] = {any_offset<T, kPByK>(KIND == kForward ? wc * 32 : wc * 64),
-                       any_offset<T, kPByK>(KIND == kForward ? 64 + wc * 32 : wc * 64 + 32)};
-  const u32 at_q[2] = {any_offset<T, kQByK>(wr * 64), any_offset<T, kQByK>(wr * 64 + 32)};
-  f32x16 acc[2][2] = {};
+  u32 at_p[B], at_q[B];
+#pragma unroll
+  for (int x = 0; x < B; ++x) {
+    at_p[x] = any_offset<T, kPByK, SIDE>(KIND == kForward ? x * 64 + wc * 32 : (wc * B + x) * 32);
+    at_q[x] = any_offset<T, kQByK, SIDE>((wr * B + x) * 32);
+  }
+  f32x16 acc[B][B] = {};
   auto multiply = [&](const char* lds) {
 #pragma unroll
     for (u32 s = 0; s < 4; ++s) {
-      vec4 p[2], q[2];
+      vec4 p[B], q[B];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) p[x] = any_fragment<T, kPByK>(lds, at_p[x], s);
+      for (int x = 0; x < B; ++x) p[x] = any_fragment<T, kPByK, SIDE>(lds, at_p[x], s);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) q[y] = any_fragment<T, kQByK>(lds + kOperand, at_q[y], s);
+      for (int y = 0; y < B; ++y) q[y] = any_fragment<T, kQByK, SIDE>(lds + kOperand<SIDE>, at_q[y], s);
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < B; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) acc[x][y] = any_mfma32<T>(p[x], q[y], acc[x][y]);
+        for (int y = 0; y < B; ++y) acc[x][y] = any_mfma32<T>(p[x], q[y], acc[x][y]);
     }
   };
-  const u32 put_p = put_at<T, kPByK>(), put_q = put_at<T, kQByK>();
-  auto put = [&](char* to, const vec4 (&r)[8]) {
+  const u32 put_p = put_at<T, kPByK, SIDE>(), put_q = put_at<T, kQByK, SIDE>();
+  auto put = [&](char* to, const vec4 (&r)[2 * R]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       *reinterpret_cast<vec4*>(to + put_p + i * 4096) = r[i];
-      *reinterpret_cast<vec4*>(to + kOperand + put_q + i * 4096) = r[4 + i];
+      *reinterpret_cast<vec4*>(to + kOperand<SIDE> + put_q + i * 4096) = r[R + i];
     }
   };
   // a split has a run of the steps, in the input gradient of gate's and then up's
@@ -189,28 +195,28 @@ __global__ __launch_bounds__(256, 2) void any_kernel(const ProductLaunch a, u32 
     const int64_t whole = min(hi, min(whole_steps<T, kPByK>(b.cols, b.k), whole_steps<T, kQByK>(b.rows, b.k)));
     int64_t s = lo;
     if (lo < whole) {
-      int64_t op[4], oq[4];
+      int64_t op[R], oq[R];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        op[i] = offset_of<T, kPByK>(KIND == kForward ? i % 2 : i, KIND == kForward && i >= 2 ? b.ld_p[1] : ld_p, c0, b.cols);
-        oq[i] = offset_of<T, kQByK>(i, ld_q, r0, b.rows);
+      for (int i = 0; i < R; ++i) {
+        op[i] = offset_of<T, kPByK, SIDE>(KIND == kForward ? i % 2 : i, KIND == kForward && i >= 2 ? b.ld_p[1] : ld_p, c0, b.cols);
+        oq[i] = offset_of<T, kQByK, SIDE>(i, ld_q, r0, b.rows);
       }
       const int64_t far_p = kPByK ? 128 : kAnyStep<T> * ld_p, far_q = kQByK ? 128 : kAnyStep<T> * ld_q;
       const char* next_p = p + (kPByK ? c0 * ld_p : c0 * T::bytes) + lo * far_p;
       const char* next_up = KIND == kForward ? b.p[1] + c0 * b.ld_p[1] + lo * far_p : nullptr;
       const char* next_q = q + (kQByK ? r0 * ld_q : r0 * T::bytes) + lo * far_q;
-      auto get = [&](vec4 (&r)[8]) {
+      auto get = [&](vec4 (&r)[2 * R]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
           r[i] = *reinterpret_cast<const vec4_any*>((KIND == kForward && i >= 2 ? next_up : next_p) + op[i]);
-          r[4 + i] = *reinterpret_cast<const vec4_any*>(next_q + oq[i]);
+          r[R + i] = *reinterpret_cast<const vec4_any*>(next_q + oq[i]);
         }
         next_p += far_p;
         next_up += far_p;
         next_q += far_q;
         __builtin_amdgcn_sched_barrier(0);  // the loads first: what follows waits for earlier ones only
       };
-      vec4 r[8], n[8];
+      vec4 r[2 * R], n[2 * R];
       get(r);
       if (lo + 1 < whole) get(n);
       put(s0, r);
@@ -245,13 +251,13 @@ __global__ __launch_bounds__(256, 2) void any_kernel(const ProductLaunch a, u32 
     }
 #pragma unroll 1
     for (; s < hi; ++s) {
-      vec4 r[8];
+      vec4 r[2 * R];
       const int64_t k0 = s * kAnyStep<T>;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < R; ++i) {
         const int ip2 = KIND == kForward && i >= 2 ? 1 : ip;
-        r[i] = edge_unit<T, kPByK>(KIND == kForward ? i % 2 : i, b.p[ip2], b.p_end[ip2], b.ld_p[ip2], c0, b.cols, k0, b.k);
-        r[4 + i] = edge_unit<T, kQByK>(i, q, b.q_end[iq], ld_q, r0, b.rows, k0, b.k);
+        r[i] = edge_unit<T, kPByK, SIDE>(KIND == kForward ? i % 2 : i, b.p[ip2], b.p_end[ip2], b.ld_p[ip2], c0, b.cols, k0, b.k);
+        r[R + i] = edge_unit<T, kQByK, SIDE>(i, q, b.q_end[iq], ld_q, r0, b.rows, k0, b.k);
       }
       put(s0, r);
       __syncthreads();
@@ -259,7 +265,8 @@ __global__ __launch_bounds__(256, 2) void any_kernel(const ProductLaunch a, u32 
       __syncthreads();
     }
   }
-  finish_tile<T, KIND, 2, 2>(acc, s0 + wave * kStageBytes, r0 + wr * 64, c0 + wc * (KIND == kForward ? 32 : 64), which, split, splits);
+  static_assert(2 * kStageBytes <= sizeof(s0), "two waves' results fit");
+  finish_tile<T, KIND, B, B>(acc, (wave < 2 ? s0 : s1) + wave % 2 * kStageBytes, r0 + wr * B * 32, c0 + wc * (KIND == kForward ? 32 : B * 32), which, split, splits);
 }
 
 // ---------------------------------------------------------------------------
@@ -391,25 +398,40 @@ int join_as(const ProductLaunch& a, u32 splits, hipStream_t s) {
   return launched("gated products (join)");
 }
 
-// The number of splits of k, by an estimate of microseconds: a step of a tile takes `each` (fp32 4096 clocks of matrix
-// instructions, 16 bits what the loads take), two tiles on a CU; partial results move at 5 TB/s, and
-// another launch takes 3.
-u32 any_splits(Product kind, const ProductLaunch& a, zero_dtype_t t) {
-  if (kind == kForward) return 1;
+// The side of the tiles and the number of splits of k, by an estimate of microseconds: what a step takes a tile alone on its
+// CU, or a CU full of them (2 of 128, 4 of 64); partial results move at 5 TB/s, and another launch takes 3.
+struct AnyPlan {
+  int side;
+  u32 splits;
+};
+AnyPlan any_plan(Product kind, const ProductLaunch& a, zero_dtype_t t) {
+  AnyPlan best{128, 1};
+  if (kind == kForward) return best;
   const int64_t halves = kind == kWeight ? 2 : 1, step = t == ZERO_F32 ? 32 : 64;
   const int64_t steps = (a.k + step - 1) / step * (kind == kInput ? 2 : 1), bytes = halves * a.rows * partial_cols(a.cols) * 4;
-  const int64_t tiles = (a.rows + kSide - 1) / kSide * ((a.cols + kSide - 1) / kSide) * halves;
-  const double alone = t == ZERO_F32 ? 2.2 : 1.0, both = t == ZERO_F32 ? 4.2 : 1.45;
   double least = 1e300;
-  u32 best = 1;
-  for (u32 n = 1; n <= kMaxSplits; ++n) {
-    if (n > 1 && (steps / n < 4 || bytes > kMaxPartialBytes / n)) break;
-    const int64_t groups = tiles * n;
-    double us = (groups <= 256 ? alone : both * (double)((groups + 511) / 512)) * (double)steps / n;
-    if (n > 1) us += 3.0 + 2.0 * n * (double)bytes / 5e6;
-    if (us < least) least = us, best = n;
+  for (int side : {128, 64}) {
+    const int64_t tiles = (a.rows + side - 1) / side * ((a.cols + side - 1) / side) * halves, full = side == 128 ? 512 : 1024;
+    const double alone = t == ZERO_F32 ? (side == 128 ? 2.2 : 0.8) : (side == 128 ? 1.0 : 0.7);
+    const double shared = t == ZERO_F32 ? (side == 128 ? 4.2 : 2.4) : (side == 128 ? 1.45 : 1.0);
+    for (u32 n = 1; n <= kMaxSplits; ++n) {
+      if (n > 1 && (steps / n < 4 || bytes > kMaxPartialBytes / n)) break;
+      const int64_t groups = tiles * n;
+      double us = (groups <= 256 ? alone : shared * (double)((groups + full - 1) / full)) * (double)steps / n;
+      if (n > 1) us += 3.0 + 2.0 * n * (double)bytes / 5e6;
+      if (us < least) least = us, best = AnyPlan{side, n};
+    }
   }
   return best;
+}
+
+template <class T, Product KIND, int SIDE>
+int any_tiles(const ProductLaunch& a, u32 splits, hipStream_t s) {
+  constexpr int cols = KIND == kForward ? SIDE / 2 : SIDE;
+  const u32 down = (u32)((a.rows + SIDE - 1) / SIDE), across = (u32)((a.cols + cols - 1) / cols);
+  hipLaunchKernelGGL((any_kernel<T, KIND, SIDE>), dim3(down * across * (KIND == kWeight ? 2 : 1) * splits), dim3(256), 0, s, a, down,
+                     across, splits);
+  return launched(KIND == kForward ? "gated projections" : KIND == kInput ? "gated input gradient" : "gated weight gradient");
 }
 
 template <class T, Product KIND>
@@ -419,13 +441,11 @@ int any_as(const ProductLaunch& a, zero_dtype_t t, hipStream_t s) {
     if (a.rows <= 32) return few_any_as<T, 32>(a, s);
     if (a.rows <= 64) return few_any_as<T, 64>(a, s);
   }
-  constexpr int cols = KIND == kForward ? kSide / 2 : kSide;
-  const u32 down = (u32)((a.rows + kSide - 1) / kSide), across = (u32)((a.cols + cols - 1) / cols), splits = any_splits(KIND, a, t);
-  hipLaunchKernelGGL((any_kernel<T, KIND>), dim3(down * across * (KIND == kWeight ? 2 : 1) * splits), dim3(256), 0, s, a, down, across,
-                     splits);
-  if (int rc = launched(KIND == kForward ? "gated projections" : KIND == kInput ? "gated input gradient" : "gated weight gradient"))
+  const AnyPlan plan = any_plan(KIND, a, t);
+  if (int rc = KIND != kForward && plan.side == 64 ? any_tiles<T, KIND, KIND == kForward ? 128 : 64>(a, plan.splits, s)
+                                                   : any_tiles<T, KIND, 128>(a, plan.splits, s))
     return rc;
-  return splits > 1 ? launch_join(KIND, a, t, splits, s) : ZERO_OK;
+  return plan.splits > 1 ? launch_join(KIND, a, t, plan.splits, s) : ZERO_OK;
 }
 
 template <Product KIND>

@@ -361,13 +361,13 @@ __device__ __forceinline__ void finish_tile(const f32x16 (&acc)[XB][YB], char* m
         flush_partial(mine, b.ws + at, r, b.rows, c0 + x * 32, wide);
       }
     } else if ((KIND == kInput && T::bytes == 2) || (KIND == kWeight && b.out_type != ZERO_F32 && !b.accumulate)) {  // rounded once, to 16 bits
-      constexpr int kWide = 64;
+      constexpr int kPair = XB < 2 ? 1 : 2, kWide = kPair * 32;
       auto store = [&](auto type) {
         using O = decltype(type);
 #pragma unroll
-        for (int x = 0; x < XB; x += 2) {
+        for (int x = 0; x < XB; x += kPair) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < kPair; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float v[4] = {acc[x + i][y][4 * j], acc[x + i][y][4 * j + 1], acc[x + i][y][4 * j + 2], acc[x + i][y][4 * j + 3]};
