@@ -450,7 +450,7 @@ TilePlan tile_plan(Product kind, const ProductLaunch& a) {
   for (int tile : {128, 256}) {
     const int64_t cols = kind == kForward ? tile / 2 : tile;
     const int64_t tiles = (a.rows + tile - 1) / tile * ((a.cols + cols - 1) / cols) * halves;
-    for (u32 n = 1; n <= kMaxSplits; ++n) {
+    for (u32 n = 1; n <= kMaxSplits / 2; ++n) {
       if (n > 1 && (kind == kForward || units / n < 4 || bytes > kMaxPartialBytes / n || a.cols % 8 != 0)) break;
       const int64_t groups = tiles * n;
       double each, begin, rounds;

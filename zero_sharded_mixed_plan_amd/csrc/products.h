@@ -14,7 +14,7 @@ int launch_join(Product kind, const ProductLaunch& a, zero_dtype_t t, uint32_t s
 
 namespace {
 
-constexpr u32 kMaxSplits = 16;
+constexpr u32 kMaxSplits = 32;  // of fp32 sums; 16 of 16-bit products, whose steps are short beside a partial result
 constexpr int64_t kMaxPartialBytes = int64_t(64) << 20;
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
