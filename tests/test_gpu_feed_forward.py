@@ -412,6 +412,42 @@ def test_rms_norm_grad_in_place_workspace_and_empty():
     assert (dw == 0).all()
 
 
+@pytest.mark.parametrize("cols", [300, 1000, 2000, 4000, 7001])
+@pytest.mark.parametrize("at,st", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+def test_norm_forms(at, st, cols):
+    """Every pair of types at every width of a row's share of a workgroup, with and without 8 bits, against
+    64 bits on the GPU; an odd number of rows."""
+    say(f"norm forms {at} {st} {cols}")
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    rows = 69
+    r = lambda *s, k=1.0, dt=at: (torch.randn(*s, generator=g, device="cuda") * k).to(T[dt])  # noqa: E731
+    x, res, w, dy, dres = r(rows, cols), r(rows, cols, k=2.0, dt=st), r(cols, dt="f32"), r(rows, cols), r(rows, cols, dt=st)
+    total = (x.float() + res.float()).to(T[st])
+    h = total.double()
+    rstd = 1 / (h.square().mean(1, keepdim=True) + 1e-5).sqrt()
+    y = h * rstd * w.double()
+    plain = F.rms_norm(x, w, eps=1e-5, residual=res, out_dtype=T[at])
+    both = F.rms_norm(x, w, eps=1e-5, residual=res, out_dtype=T[at], packed=True)
+    assert torch.equal(plain.total, total) and torch.equal(both.total, total) and torch.equal(plain.y, both.y)
+    close(plain.y, f64(y), E * np.abs(f64(y)), "y")
+    close(plain.rstd, f64(rstd)[:, 0], np.zeros(rows), "rstd")
+    want = F.pack8(F.rms_norm(x, w, eps=1e-5, residual=res, out_dtype=torch.float32).y)
+    assert torch.equal(both.packed.codes.view(torch.uint8), want.codes.view(torch.uint8))
+    assert torch.equal(both.packed.scales.view(torch.uint8), want.scales.view(torch.uint8))
+    kept = F.pack8(total)
+    for source, hs in ((total, h), (kept, F.unpack8(kept, torch.float32).double())):
+        n = hs * plain.rstd.double()[:, None]
+        s = dy.double() * w.double()
+        dh = plain.rstd.double()[:, None] * (s - n * (s * n).mean(1, keepdim=True)) + dres.double()
+        size = (s * n).abs().mean(1, keepdim=True) * n.abs()
+        err = E * plain.rstd.double()[:, None] * (3 * s.abs() + 40 * size) + E * dh.abs()
+        dw = torch.empty(cols, device="cuda")
+        got = F.rms_norm_grad(dy, source, plain.rstd, w, residual_grad=dres, out_dtype=T[st] if source is kept else None,
+                              weight_grad=dw)
+        close(got, f64(dh), f64(err), "dh")
+        close(dw, f64((dy.double() * n).sum(0)), (rows + 3) * E * f64((dy.double() * n).abs().sum(0)), "dw")
+
+
 def test_rms_norm_grad_against_differences():
     """The kernels' forward pass in fp32, differenced along a direction, against the
     kernels' gradient: y is off by at most 2^-24 |y|, which a step of 2^-6 turns into 2^-18 sum |y c|;
@@ -730,7 +766,9 @@ FORMS = [  # tokens, dim, hidden, type, offset, padding
     (1, 840, 8300, "bf16", 0, 0), (5, 64, 8200, "f16", 0, 0), (17, 136, 8300, "bf16", 0, 0), (32, 72, 200, "bf16", 0, 0),
     (33, 840, 300, "f16", 0, 0), (64, 200, 8300, "bf16", 0, 0), (64, 8, 31, "f16", 0, 0),
     (1, 841, 8301, "bf16", 0, 0), (2, 63, 33, "f16", 1, 0), (17, 137, 300, "bf16", 0, 1), (33, 300, 77, "f32", 1, 3),
-    (64, 129, 1000, "f16", 3, 0), (64, 7, 65, "bf16", 0, 0), (12, 1000, 500, "f32", 0, 0), (29, 260, 200, "f32", 0, 0),
+    (64, 129, 1000, "f16", 3, 0), (64, 7, 65, "bf16", 0, 0), (12, 1000, 500, "f32", 0, 0),
+    (200, 2200, 600, "f16", 0, 0), (130, 2304, 1000, "bf16", 0, 0), (20, 72, 8320, "f16", 0, 0), (20, 72, 8320, "bf16", 0, 0),
+    (40, 72, 8320, "f16", 0, 0), (20, 65, 40, "f16", 0, 0), (29, 260, 200, "f32", 0, 0),
     (65, 9, 31, "bf16", 0, 0), (300, 515, 190, "bf16", 0, 0), (1025, 191, 333, "f16", 5, 3), (257, 512, 640, "f32", 0, 0),
     (129, 31, 65, "f32", 1, 1), (130, 64, 66, "bf16", 4, 0),
     (3, 16, (1 << 18) + 40, "bf16", 0, 0), ((1 << 18) + 5, 8, 16, "f16", 0, 0), (3, 5, (1 << 18) + 33, "f32", 0, 0),
@@ -767,6 +805,7 @@ def test_gated_forms(t, d, f, dt, off, pad):
 
 PRODUCT_FORMS = [  # tokens, dim, hidden, type, offset, padding
     (4096, 4096, 72, "bf16", 0, 0), (4100, 2048, 200, "f16", 0, 8), (100, 4096, 2048, "bf16", 0, 0), (100, 4096, 2048, "f16", 0, 0),
+    (1024, 1024, 1024, "f32", 0, 0), (1000, 2040, 2304, "bf16", 0, 0), (1000, 2040, 2304, "f16", 0, 0),
     (300, 512, 5000, "bf16", 0, 0), (9000, 136, 72, "bf16", 0, 0), (9000, 136, 72, "f16", 0, 8), (1, 512, 5000, "bf16", 0, 0),
     (1, 513, 5001, "bf16", 0, 0), (1, 300, 700, "f32", 0, 0), (9001, 137, 71, "bf16", 0, 0), (9001, 66, 130, "f16", 1, 0),
     (2500, 100, 60, "f32", 0, 0), (2501, 130, 129, "f32", 3, 1), (700, 260, 390, "bf16", 4, 0), (3, 5, 4099, "f16", 0, 3),
