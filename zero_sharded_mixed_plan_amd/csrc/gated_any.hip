@@ -48,10 +48,10 @@ __device__ __forceinline__ vec4 unit_of(const char* p, const char* end, u32 n) {
 // each.  The operands go through registers, which takes any address, two steps before they
 // are multiplied, into one of two tiles in LDS; a step has one barrier.  fp32 tiles lie as 16-bit
 // ones do where their rows are of k: a matrix instruction's k are one element of every unit that the
-// lanes read.  4096 tokens of bf16, 2049 x 5503: forward 290 us, input gradient 410, weight
-// gradient 306 (637, 451 and 603 TFLOP/s; two tiles share a CU, and its L1 takes two lines for every 128
+// lanes read.  4096 tokens of bf16, 2049 x 5503: forward 288 us, input gradient 396, weight
+// gradient 292 (642, 466 and 632 TFLOP/s; two tiles share a CU, and its L1 takes two lines for every 128
 // bytes that begin inside one); tiles of 64 x 64, loaded one step ahead under masks, took 640, 1118
-// and 1510.  1024 tokens of fp32, 2048 x 5504: 385, 382 and 415 us, of a floor of 295 at the rate of fp32
+// and 1510.  1024 tokens of fp32, 2048 x 5504: 384 to 433, 370 and 400 us, of a floor of 295 at the rate of fp32
 // matrix instructions.  Rows of the other index, [32 k][SIDE] fp32, are read element by element; every
 // second four of them have their halves of 64 columns in turn exchanged by 32, so that the two halves
 // of a wave meet different banks.
