@@ -367,8 +367,10 @@ int few_any_as(const ProductLaunch& a, hipStream_t s) {
     constexpr int C = decltype(columns)::value;
     hipLaunchKernelGGL((few_any_kernel<T, TOKENS, C>), dim3((u32)((a.cols + C - 1) / C)), dim3(256), 0, s, a);
   };
-  if (TOKENS == 64 || a.held[0].codes) go(std::integral_constant<int, 32>{});
-  else if constexpr (TOKENS < 64) go(std::integral_constant<int, 16>{});
+  // 32 columns are a block of 8 bits; 16 give twice the workgroups (64 tokens of bf16, 4095 x 11007 65 us and 80,
+  // 2047 x 4001 19 and 25; of fp32 218 and 230, 40 and 63)
+  if (a.held[0].codes) go(std::integral_constant<int, 32>{});
+  else go(std::integral_constant<int, 16>{});
   return launched("gated projections");
 }
 
