@@ -402,11 +402,15 @@ int few_as(const ProductLaunch& a, hipStream_t s) {
   using Two = std::integral_constant<int, 2>;
   using Four = std::integral_constant<int, 4>;
   const bool many = a.cols > 16 * 512;  // more than two workgroups a CU
-  // With 64 tokens their rows are more than the weights' of 16 columns (64 tokens, 4096 x 14336
-  // 58 us with 32 columns, 69 with 16; 16 tokens 48 and 47, 4096 x 11008 45 and 37.5).
-  if (TOKENS == 64 || a.held[0].codes) {
+  // With 64 tokens their rows are more than the weights' of 16 columns, and a workgroup of four waves has a CU
+  // to itself (64 tokens, 4096 x 14336 58 us with 32 columns, 69 with 16, 40 tokens, 4096 x 8000 24 and 30; but
+  // 4096 x 5504 24.9 and 23.0, 2048 x 4000 11.6 and 9.1, 512 x 1376 6.5 and 4.0: few columns need the workgroups).
+  // 16 tokens, 4096 x 14336 48 and 47, 4096 x 11008 45 and 37.5.
+  if ((TOKENS == 64 && a.cols > 16 * 384) || a.held[0].codes) {
     a.cols > 32 * 256 ? go(std::integral_constant<int, 32>{}, Two{}) : go(std::integral_constant<int, 32>{}, Four{});
-  } else if constexpr (TOKENS < 64) {
+  } else if constexpr (TOKENS == 64) {
+    go(std::integral_constant<int, 16>{}, Four{});
+  } else {
     many ? go(std::integral_constant<int, 16>{}, Two{}) : go(std::integral_constant<int, 16>{}, Four{});
   }
   return launched("gated projections");
