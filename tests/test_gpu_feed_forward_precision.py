@@ -1,0 +1,65 @@
+"""Where digits of the feed-forward sub-layer's results could be lost without a sign: gates far out,
+sums rounded twice, far magnitudes, scales.
+
+Error bounds beside those of test_gpu_feed_forward.py (e = 2^-24):
+  gates of fp32   t = exp(-|z|) within an ulp, 2 e, or 2^-149 where t is a subnormal; 1 + t: t's error, at most
+              half of it relative to the sum, and e; the quotient e; t * (1 / (1 + t)): t's error once more, and
+              e.  p and 1 - p are off by at most P = 6 e of themselves, whatever z (GELU: z in fp64, whose
+              part beyond fp32 costs one more rounding, P = 7 e), and by 2^-148 where they are subnormals.
+              With r = P p + 2^-148:  a = g p u: |g u| r + e |a|,  du = da g p: |g da| r + e |du|,
+              act' = p + g p (1 - p) slope, slope off by 5 e: D = r + |g| slope ((2 P + 8 e) p (1 - p) + 2^-147)
+              + e |act'|, and dg = da u act': |da u| (D + e |act'|)
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import feed_forward as OF
+from test_gpu_feed_forward import E, close, codes_of, f64
+from zero_sharded_mixed_plan_amd import feed_forward as F
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+# ---------------------------------------------------------------------------
+# gates
+# ---------------------------------------------------------------------------
+
+def far_gates():
+    """Gates of both signs, to where silu's are subnormals and gelu's are 0."""
+    g = np.concatenate([np.linspace(-103, 103, 4001), np.linspace(-11, 11, 4001), np.exp2(np.linspace(-40, -1, 79)),
+                        -np.exp2(np.linspace(-40, -1, 79))])
+    return torch.from_numpy(g).float().cuda()
+
+
+def gate_errors(kind, g):
+    """act(g), act'(g), r and D of the bounds above, float64."""
+    v, d, p, z, dz = OF.act(kind, g)
+    with np.errstate(over="ignore"):
+        less = np.where(z >= 0, np.exp(-np.abs(z)) / (1 + np.exp(-np.abs(z))), 1 / (1 + np.exp(-np.abs(z))))
+    rel = (6 if kind == "silu" else 7) * E
+    r = rel * p + 2.0 ** -148
+    return v, d, r, r + np.abs(g) * dz * ((2 * rel + 8 * E) * p * less + 2.0 ** -147) + E * np.abs(d)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_fp32_gates_keep_their_digits(kind):
+    g = far_gates()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    da, u = (torch.rand(g.shape, generator=gen, device="cuda") + 0.5 for _ in range(2))
+    r = F.gated_grad(da[None], g[None], u[None], act=kind, again=True)
+    gs, ds, us = f64(g), f64(da), f64(u)
+    v, d, err, D = gate_errors(kind, gs)
+    close(r.a[0], v * us, np.abs(gs * us) * err + E * np.abs(v * us), "a")
+    close(r.up[0], v * ds, np.abs(gs * ds) * err + E * np.abs(v * ds), "du")
+    close(r.gate[0], ds * us * d, np.abs(ds * us) * (D + E * np.abs(d)), "dg")
+    # a product of one term gives the gates as they are; few tokens and tiles
+    for tokens in (1, 70):
+        f = F.gated(torch.ones(tokens, 1, device="cuda"), g[:, None], u[:, None], act=kind).a
+        close(f, np.broadcast_to(v * us, f.shape), np.abs(gs * us) * err + E * np.abs(v * us), f"a of {tokens} tokens")

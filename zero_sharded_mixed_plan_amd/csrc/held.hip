@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kThreads8) void unpack_kernel(const HoldLaunch a) {
   store8<T>(a.x + (int64_t)row * a.ld_x + (int64_t)grp * 8 * T::bytes, v, n);
 }
 
-// a = g p u, dg = da u (p + g p (1 - p) slope), du = da g p; see gate_of.
+// a = g p u, dg = da u (p + g p q slope), du = da g p; see Gate.
 template <class T, bool HELD, int ACT>
 __global__ __launch_bounds__(kThreads8) void gated_grad_kernel(const GatedGradLaunch a) {
   const u32 i = blockIdx.x * (u32)kThreads8 + threadIdx.x;
@@ -64,9 +64,9 @@ __global__ __launch_bounds__(kThreads8) void gated_grad_kernel(const GatedGradLa
   float dg[8], du[8], act[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const Gate e = gate_of<ACT>(g[j]);
+    const Gate e = gate_of<T, ACT>(g[j]);
     const float v = g[j] * e.p;
-    const float slope = __builtin_fmaf(v * (1.0f - e.p), e.slope, e.p);
+    const float slope = __builtin_fmaf(v * e.q, e.slope, e.p);
     dg[j] = d[j] * u[j] * slope;
     du[j] = d[j] * v;
     act[j] = v * u[j];

@@ -42,8 +42,9 @@ __device__ __forceinline__ void finish4(const ProductLaunch& a, int which, int64
   }
 }
 
+template <class T>
 __device__ __forceinline__ float gated_value(int32_t act, float g, float u) {
-  return g * (act == kSilu ? gate_of<kSilu>(g).p : gate_of<kGelu>(g).p) * u;
+  return g * (act == kSilu ? gate_of<T, kSilu>(g).p : gate_of<T, kGelu>(g).p) * u;
 }
 
 // The same of the forward pass: gate and up.
@@ -52,7 +53,7 @@ __device__ __forceinline__ void finish_gated4(const ProductLaunch& a, int64_t r,
                                               u32 n) {
   float v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = gated_value(a.act, g[j], u[j]);
+  for (int j = 0; j < 4; ++j) v[j] = gated_value<T>(a.act, g[j], u[j]);
   store4<T>(a.out[0] + r * a.ld_out[0] + c * T::bytes, v, n);
   if (a.kept[0]) {
     store4<T>(a.kept[0] + r * a.ld_kept[0] + c * T::bytes, g, n);
@@ -325,7 +326,7 @@ __device__ __forceinline__ void finish_tile(const f32x16 (&acc)[XB][YB], char* m
         for (int j = 0; j < 4; ++j) {
           float v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = gated_value(b.act, acc[x][y][4 * j + e], acc[x + XG][y][4 * j + e]);
+          for (int e = 0; e < 4; ++e) v[e] = gated_value<T>(b.act, acc[x][y][4 * j + e], acc[x + XG][y][4 * j + e]);
           if constexpr (T::bytes == 4) stage_floats(mine, 8 * j, f32x4{v[0], v[1], v[2], v[3]});
           else stage_bits<T, kWide>(mine, x * 32 + 8 * j, v);
         }
