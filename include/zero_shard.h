@@ -679,7 +679,8 @@ int zero_embed_grad(const zero_embed_grad_args_t* args, void* stream);
  * lie in its range; magnitudes from 1.9375 * 2^127 up are held as 2^128, which reads as
  * an infinity.
  * codes [rows, cols]: one byte each, rows ld_codes bytes apart.  scales [rows,
- * ceil(cols / 32)]: bytes e + 127 (OCP e8m0; never 255), rows ld_scales bytes apart.
+ * ceil(cols / 32)]: bytes e + 127 (OCP e8m0), rows ld_scales bytes apart; never 255, which
+ * reads as NaN for the whole block.
  */
 #define ZERO_HELD_BLOCK 32
 typedef struct zero_held {

@@ -63,3 +63,29 @@ def test_fp32_gates_keep_their_digits(kind):
     for tokens in (1, 70):
         f = F.gated(torch.ones(tokens, 1, device="cuda"), g[:, None], u[:, None], act=kind).a
         close(f, np.broadcast_to(v * us, f.shape), np.abs(gs * us) * err + E * np.abs(v * us), f"a of {tokens} tokens")
+
+
+# ---------------------------------------------------------------------------
+# scales
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16, torch.float32])
+def test_a_scale_of_255_is_not_a_number(dt):
+    """e8m0's NaN, which no call here writes but other programs may: its block reads as NaN, no other does."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(5, 100, generator=g, device="cuda").to(dt)
+    x[2, 40] = 0
+    p = F.pack8(x)
+    want = F.unpack8(p, dt)
+    bytes_ = p.scales.view(torch.uint8).clone()
+    bytes_[2, 1] = 255
+    bad = F.Packed8(p.codes.view(torch.uint8), bytes_)
+    got = F.unpack8(bad, dt)
+    nan = torch.zeros(5, 100, dtype=torch.bool, device="cuda")
+    nan[2, 32:64] = True
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], want[~nan])
+    one = torch.ones(5, 100, dtype=dt, device="cuda")
+    r = F.gated_grad(one, bad, p, again=True)
+    assert torch.equal(torch.isnan(r.a), nan) and torch.equal(torch.isnan(r.gate), nan)
+    dh = F.rms_norm_grad(one, bad, torch.ones(5, device="cuda"))
+    assert torch.equal(torch.isnan(dh).any(1), nan.any(1))

@@ -220,8 +220,10 @@ __device__ __forceinline__ u32 scale_of(u32 top) {
 }
 // 1 / scale, exact
 __device__ __forceinline__ float inverse_scale(u32 s) { return __uint_as_float((254 - s) << 23); }
-// the scale; 2^-127 is a subnormal
-__device__ __forceinline__ float scale_value(u32 s) { return __uint_as_float(s ? s << 23 : 0x400000u); }
+// the scale; 2^-127 (byte 0) is a subnormal, and 255 is e8m0's NaN: both have the fraction's first bit set
+__device__ __forceinline__ float scale_value(u32 s) {
+  return __uint_as_float(s << 23 | (((s + 1) & 254) == 0 ? 0x400000u : 0));
+}
 
 __device__ __forceinline__ bool finite_bits(u32 b) { return (b & 0x7fffffffu) < 0x7f800000u; }
 
