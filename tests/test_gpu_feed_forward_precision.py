@@ -89,3 +89,33 @@ def test_a_scale_of_255_is_not_a_number(dt):
     assert torch.equal(torch.isnan(r.a), nan) and torch.equal(torch.isnan(r.gate), nan)
     dh = F.rms_norm_grad(one, bad, torch.ones(5, device="cuda"))
     assert torch.equal(torch.isnan(dh).any(1), nan.any(1))
+
+
+# ---------------------------------------------------------------------------
+# the norm's gradient
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,half", [(torch.bfloat16, 2.0 ** -8), (torch.float16, 2.0 ** -11)])
+def test_weight_gradient_is_rounded_once(dt, half):
+    """Sums next to the middle of two 16-bit numbers: fp32 in between would put them on it.  Rows of 2500
+    columns are a workgroup each, whose sums are joined in fp64."""
+    tiny = 2.0 ** -40
+    one = torch.ones(2, 2500, device="cuda")
+
+    def grad(first, second, held=None):
+        dy = torch.tensor([[first], [second]], device="cuda").expand(2, 2500).contiguous()
+        dw = torch.full((2500,), held or 0.0, dtype=dt, device="cuda")
+        F.rms_norm_grad(dy, one, torch.ones(2, device="cuda"), weight_grad=dw, accumulate=held is not None)
+        return dw
+
+    for held in (None, 1.0):
+        base = 0.0 if held else 1.0  # written: all of it in the sum; added: 1 lies there
+        for sign in (1.0, -1.0):
+            h = None if held is None else sign
+            assert (grad(sign * (base + half), sign * tiny, h) == sign * (1 + 2 * half)).all()
+            assert (grad(sign * (base + half), 0.0, h) == sign).all()  # the middle: to even
+            assert (grad(sign * (base + 3 * half), -sign * tiny, h) == sign * (1 + 2 * half)).all()
+            assert (grad(sign * (base + 3 * half), 0.0, h) == sign * (1 + 4 * half)).all()
+    big = torch.finfo(dt).max
+    assert torch.isinf(grad(3e38, 3e38)).all() and (grad(big, 0.0) == big).all()
+    assert torch.isnan(grad(float("nan"), 1.0)).all() and (grad(0.0, 0.0) == 0).all()

@@ -140,6 +140,15 @@ __global__ __launch_bounds__(grad_threads(WAVES)) void rms_grad_kernel(const Rms
   }
 }
 
+// A sum in fp32 that a second rounding, to 16 bits, takes where one rounding of the sum itself would: what fp32
+// cuts off makes its last bit odd, so that no sum lands on the middle of two 16-bit numbers that was not there.
+__device__ __forceinline__ float to_odd(double v) {
+  const float f = (float)v;
+  const double d = (double)f;
+  if (d == v || v != v) return f;
+  return __uint_as_float((__float_as_uint(f) - (fabs(d) > fabs(v) ? 1 : 0)) | 1);
+}
+
 // 32 columns a workgroup, 32 slices of the partial rows
 constexpr int kJoinCols = 32, kJoinSlices = 32;
 __global__ __launch_bounds__(kJoinCols * kJoinSlices) void rms_grad_join_kernel(const RmsGradLaunch a) {
@@ -158,7 +167,7 @@ __global__ __launch_bounds__(kJoinCols * kJoinSlices) void rms_grad_join_kernel(
   for (int i = 0; i < kJoinSlices; ++i) sum += part[i][x];
   char* const p = a.dweight + (int64_t)col * one_bytes(a.dweight_type);
   if (a.accumulate) sum += (double)load_one(p, a.dweight_type);
-  store_one(p, a.dweight_type, (float)sum);
+  store_one(p, a.dweight_type, a.dweight_type == ZERO_F32 ? (float)sum : to_odd(sum));
 }
 
 // 8 columns a lane: with 16, 8192 x 4096 bf16 took 55 us from 8 bits, against 51.
