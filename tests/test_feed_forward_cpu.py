@@ -418,3 +418,15 @@ def test_torch_layer_refuses_to_lose_a_gradient():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
             call()
+
+
+@pytest.mark.parametrize("half", [z(4, 6), F.packed8_empty((4, 6), "cpu")])
+def test_gate_and_up_go_together(half):
+    """One of the two would be neither read nor written, without a sign."""
+    for keep in ((None, half), (half, None)):
+        with pytest.raises(ValueError, match="both or neither"):
+            F.gated(X, WF, WF, keep=keep)
+        with pytest.raises(ValueError, match="both or neither"):
+            F.gated_grad(z(4, 6), *keep)
+    with pytest.raises(ValueError, match="GPU"):
+        F.gated(X, WF, WF, keep=(None, None))

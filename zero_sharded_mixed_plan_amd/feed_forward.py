@@ -330,7 +330,9 @@ def _act(act: str) -> int:
 def _kept(gate, up, n: int, hidden: int, shape, like: torch.Tensor):
     """The arguments g, ld_g, u, ld_u, g8, u8 of a pair of tensors or Packed8s, or of none, and what
     holds the structs."""
-    if gate is None:
+    if gate is None or up is None:
+        if gate is not up:
+            raise ValueError("gate and up go together: both or neither")
         return 0, 0, 0, 0, 0, 0, None
     if isinstance(gate, Packed8) != isinstance(up, Packed8):
         raise ValueError("gate and up must be of one form")
