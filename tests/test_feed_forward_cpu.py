@@ -430,3 +430,36 @@ def test_gate_and_up_go_together(half):
             F.gated_grad(z(4, 6), *keep)
     with pytest.raises(ValueError, match="GPU"):
         F.gated(X, WF, WF, keep=(None, None))
+
+
+def test_torch_layer_refuses_to_lose_a_tangent():
+    """A dual tensor of forward-mode differentiation does not require grad; its primal, and a dual inside a
+    Function, get on to the next check (no GPU here)."""
+    p = F.packed8_empty((4, 8), "cpu")
+    calls = [lambda w, v, m: F.pack8(w), lambda w, v, m: F.unpack8(p, out=w), lambda w, v, m: F.rms_norm(w, W, eps=0.0),
+             lambda w, v, m: F.rms_norm(X, v, eps=0.0), lambda w, v, m: F.rms_norm(X, W, eps=0.0, residual=w),
+             lambda w, v, m: F.rms_norm_grad(w, X, z(4), W), lambda w, v, m: F.rms_norm_grad(X, w, z(4), W),
+             lambda w, v, m: F.rms_norm_grad(X, p, z(4), W, residual_grad=w),
+             lambda w, v, m: F.gated(w, WF, WF), lambda w, v, m: F.gated(X, m, WF), lambda w, v, m: F.gated_grad(w, X, X),
+             lambda w, v, m: F.gated_grad(X, w, X), lambda w, v, m: F.gated_grad(X, X, w),
+             lambda w, v, m: F.gated_input_grad(z(4, 6), z(4, 6), WF, m),
+             lambda w, v, m: F.gated_weight_grad(z(4, 6), z(4, 6), w, WF, WF.clone())]
+    for call in calls:
+        class Through(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, *duals):
+                call(*duals)
+
+            @staticmethod
+            def jvp(ctx, *tangents):
+                pass
+
+        with torch.autograd.forward_ad.dual_level():
+            duals = [torch.autograd.forward_ad.make_dual(torch.zeros_like(t), torch.ones_like(t)) for t in (X, W, WF)]
+            for mode in (torch.enable_grad, torch.no_grad):
+                with mode(), pytest.raises(ValueError, match="tangent"):
+                    call(*duals)
+            with pytest.raises(ValueError, match="GPU"):
+                call(*[torch.autograd.forward_ad.unpack_dual(d).primal for d in duals])
+            with pytest.raises(ValueError, match="GPU"):
+                Through.apply(*duals)

@@ -301,3 +301,21 @@ def test_a_dropouts_step_can_be_a_function():
         _dropout(drop=d.c)
     with pytest.raises(ValueError, match="out of range"):
         L.Dropout(0.5, step=lambda: -1)
+
+
+def test_torch_layer_refuses_to_lose_a_tangent():
+    """As of a tensor that requires grad, of a dual one of forward-mode differentiation; its primal gets on to the
+    next check (no GPU here)."""
+    x, ids = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    calls = [lambda w: L.dropout(w, None), lambda w: L.dropout(x, None, residual=w), lambda w: L.dropout(x, None, out=w),
+             lambda w: L.embedding(ids, w), lambda w: L.embedding(ids, x, pos_table=w, pos_period=4),
+             lambda w: L.embedding_grad(w, ids, x), lambda w: L.embedding_grad(x, ids, w)]
+    for call in calls:
+        with torch.autograd.forward_ad.dual_level():
+            w = torch.autograd.forward_ad.make_dual(torch.zeros(4, 8), torch.ones(4, 8))
+            with pytest.raises(ValueError, match="tangent"):
+                call(w)
+            with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+                call(w)
+            with pytest.raises(ValueError, match="GPU"):
+                call(torch.autograd.forward_ad.unpack_dual(w).primal)

@@ -19,7 +19,8 @@ stream of the tensors' device); every step of the computation runs in libzero_sh
 Matrices [..., cols] are rows of the last dimension; one that is not contiguous has to
 have two dimensions and adjacent columns.  Inputs and results may be column ranges of one buffer.  The calls record no history for autograd: a loop
 calls the backward pass itself, or from a torch.autograd.Function.  With grad mode on, a
-tensor that requires grad is refused, since its gradient would be lost without a sign.
+tensor that requires grad is refused, since its gradient would be lost without a sign, and so is
+one that carries a tangent of forward-mode differentiation.
 """
 from __future__ import annotations
 
@@ -30,7 +31,7 @@ from typing import NamedTuple, Optional, Tuple, Union
 import torch
 
 from . import _abi
-from .input_layer import _call, _code, _no_history, _rows
+from .input_layer import _call, _code, _forward_ad, _no_history, _no_tangents, _rows
 
 # as in input_layer: the calls' argument structs are packed in one go
 _RMS = struct.Struct("@PqiiPqPqPiiPqPPqqd")
@@ -112,6 +113,8 @@ def _is_packed(t) -> bool:
 
 def _one_device(first: torch.Tensor, *others) -> int:
     """The index of the one GPU of what a caller gave: tensors, Packed8s and Nones."""
+    if _forward_ad._current_level >= 0:
+        _no_tangents(first, *others)
     dev = first.get_device()
     history, stranger = first.requires_grad, None
     for t in others:

@@ -10,7 +10,9 @@ libzero_shard.so (zero_embed_lookup, zero_embed_grad, zero_dropout).
 The calls record no history for autograd: a loop calls the backward pass itself, or
 from a torch.autograd.Function.  With grad mode on, a tensor that requires grad is
 refused, since its gradient would be lost without a sign; detach it, or call under
-torch.no_grad() (inside a Function's forward and backward, grad mode is off).
+torch.no_grad() (inside a Function's forward and backward, grad mode is off).  A tensor
+that carries a tangent of forward-mode differentiation is refused in the same way (inside
+a Function's forward it carries none).
 """
 from __future__ import annotations
 
@@ -19,6 +21,7 @@ import struct
 from typing import Callable, Optional, Union
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import _abi
 from .optim import _CODES, dtype_code
@@ -71,8 +74,18 @@ class Dropout:
         return self.c.p
 
 
+def _no_tangents(*tensors) -> None:
+    """Called where forward-mode differentiation is under way."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("a tensor carries a tangent, and these calls compute none: take its primal, "
+                             "or call from a torch.autograd.Function with a jvp")
+
+
 def _device(first: torch.Tensor, *others) -> int:
     """The index of the tensors' one GPU."""
+    if _forward_ad._current_level >= 0:
+        _no_tangents(first, *others)
     dev = first.get_device()
     if dev < 0:
         raise ValueError("tensors must be on the GPU")
