@@ -771,6 +771,8 @@ typedef struct zero_rms_grad_args {
  *   holds and rounded once.
  * Sums are fp32 within a workgroup's rows and fp64 beyond, in an order that the sizes
  * alone give.  dh may be dy, h or dres of the same type at the same address and stride.
+ * rstd has to be finite: from a row whose sqrt(mean(h^2) + eps) lies below 2^-128 the forward
+ * pass gives an infinite one (none where eps >= 1e-77), and the row's dh and dweight are no numbers.
  * dweight may sit anywhere in a flat gradient (element alignment).
  * ws needs no initial content and must not be shared by calls that overlap in time.
  * zero_rms_grad_ws_bytes: 0 if an argument is out of range; never falls as one grows.

@@ -119,3 +119,33 @@ def test_weight_gradient_is_rounded_once(dt, half):
     big = torch.finfo(dt).max
     assert torch.isinf(grad(3e38, 3e38)).all() and (grad(big, 0.0) == big).all()
     assert torch.isnan(grad(float("nan"), 1.0)).all() and (grad(0.0, 0.0) == 0).all()
+
+
+@pytest.mark.parametrize("cols", [40, 1500, 8192])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_rms_norm_grad_far_magnitudes(dt, cols):
+    """Rows over the whole range in which rstd is a number of fp32: from 1e-38, whose rstd is 1e38, on."""
+    g = np.random.default_rng(cols)
+    size = np.array([1e-38, 1e-33, 1e-20, 1e-5, 1.0, 1e20, 1e36, 3e37])
+    sign = np.where(g.random((8, cols)) < 0.5, -1.0, 1.0)
+    h = torch.from_numpy(size[:, None] * sign * (0.5 + g.random((8, cols)))).to(dt).cuda()
+    dy = torch.from_numpy(0.25 * g.normal(size=(8, cols))).to(dt).cuda()
+    w = torch.from_numpy(1 + 0.1 * g.normal(size=cols)).to(dt).cuda()
+    rstd = F.rms_norm(h, w, eps=0.0).rstd
+    assert torch.isfinite(rstd).all()
+    dw = torch.empty(cols, device="cuda")
+    dh = F.rms_norm_grad(dy, h, rstd, w, weight_grad=dw)
+    hs, ds, ws, rs = f64(h), f64(dy), f64(w), f64(rstd)
+    want, want_dw = OF.rms_norm_grad(ds, hs, rs, ws)
+    n, s = hs * rs[:, None], ds * ws
+    A = np.abs(s * n).mean(1, keepdims=True)
+    close(dh, want, E * rs[:, None] * (3 * np.abs(s) + 40 * A * np.abs(n)) + E * np.abs(want), "dh")
+    close(dw, want_dw, (8 + 3) * E * np.abs(ds * n).sum(0), "dweight")
+    # a row whose rstd fp32 does not hold spoils no other row's gradient
+    tiny = h.clone()
+    tiny[3] = 0 if dt == torch.bfloat16 else 1e-44
+    rs2 = rstd.clone()
+    rs2[3] = float("inf")
+    other = F.rms_norm_grad(dy, tiny, rs2, w)
+    rest = [0, 1, 2, 4, 5, 6, 7]
+    assert torch.equal(other[rest], dh[rest]) and torch.isnan(other[3]).any()

@@ -191,7 +191,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
              packed: Union[Packed8, bool] = False, rstd: Union[torch.Tensor, bool] = True) -> Normed:
     """y = h * rstd * weight with h = x + residual and rstd = 1 / sqrt(mean(h^2) + eps).
 
-    x [..., cols]; residual of x's type or fp32; total receives h in the residual's
+    x [..., cols], 1 to 8192 columns; residual of x's type or fp32; total receives h in the residual's
     type (a new tensor, or one given, which may be the residual or x itself).  y has, in this
     order, the type of out, out_dtype, x; out=False leaves it out.  packed: y in 8
     bits too, or only.  rstd: fp32, [...]; False leaves it out.
@@ -269,9 +269,10 @@ def rms_norm_grad(dy: torch.Tensor, h: Union[torch.Tensor, Packed8], rstd: torch
     """The gradient of rms_norm in h, plus residual_grad (the gradient that reaches h past
     the norm), and in the weight, written to weight_grad or added to what it holds (accumulate).
 
-    h: what the norm was taken of (x, or total), as it was or from pack8.  rstd: the
-    forward pass's.  The result has the type of, in this order, h as a tensor, out, out_dtype,
-    residual_grad, dy: dy's type or fp32.  out may be dy, h or residual_grad.
+    dy [..., cols], 1 to 8192 columns.  h: what the norm was taken of (x, or total), as it
+    was or from pack8.  rstd: the forward pass's, finite (it is infinite for rows below
+    2^-128 without an eps).  The result has the type of, in this order, h as a tensor, out,
+    out_dtype, residual_grad, dy: dy's type or fp32.  out may be dy, h or residual_grad.
     """
     n, cols, ld_dy = _rows(dy, "dy")
     shape = dy.shape
