@@ -149,3 +149,25 @@ def test_rms_norm_grad_far_magnitudes(dt, cols):
     other = F.rms_norm_grad(dy, tiny, rs2, w)
     rest = [0, 1, 2, 4, 5, 6, 7]
     assert torch.equal(other[rest], dh[rest]) and torch.isnan(other[3]).any()
+
+
+@pytest.mark.parametrize("t,d,f,dt", [(70, 640, 100, torch.bfloat16), (3, 1600, 700, torch.bfloat16), (300, 512, 264, torch.float16),
+                                      (40, 333, 77, torch.float32), (130, 333, 77, torch.bfloat16), (2000, 256, 1376, torch.bfloat16)])
+def test_scales_of_sums_are_the_smallest_that_saturate_nothing(t, d, f, dt):
+    """Gate and up held in 8 bits: with the block's largest magnitude known within b, the bound of the sums' errors,
+    the scale 2^e lets it pass, top - b <= 448 * 2^e, and half of it would not, top + b > 448 * 2^(e - 1)."""
+    g = np.random.default_rng(t)
+    x = torch.from_numpy(g.normal(size=(t, d))).to(dt).cuda()
+    for weights in [[torch.from_numpy(g.normal(size=(f, d)) / d ** 0.5 * size).to(dt).cuda() for size in sizes]
+                    for sizes in ((1.0, 30.0), (2.0 ** -9, 0.1))]:
+        r = F.gated(x, *weights, keep="packed")
+        for p, w in zip((r.gate, r.up), weights):
+            s = f64(x) @ f64(w).T
+            err = 1.01 * 3 * d * E * (np.abs(f64(x)) @ np.abs(f64(w)).T)
+            _, e = codes_of(p)
+            for b in range(e.shape[1]):
+                part = slice(32 * b, 32 * b + 32)
+                top, off = np.abs(s[:, part]).max(1), err[:, part].max(1)
+                limit = 448 * np.exp2(e[:, b].astype(float))
+                assert (top - off <= limit).all()
+                assert ((top + off > limit / 2) | (e[:, b] == -127)).all()
