@@ -403,9 +403,10 @@ int few_as(const ProductLaunch& a, hipStream_t s) {
   using Four = std::integral_constant<int, 4>;
   const bool many = a.cols > 16 * 512;  // more than two workgroups a CU
   // With 64 tokens their rows are more than the weights' of 16 columns, and a workgroup of four waves has a CU
-  // to itself (64 tokens, 4096 x 14336 58 us with 32 columns, 69 with 16, 40 tokens, 4096 x 8000 24 and 30; but
-  // 4096 x 5504 24.9 and 23.0, 2048 x 4000 11.6 and 9.1, 512 x 1376 6.5 and 4.0: few columns need the workgroups).
-  // 16 tokens, 4096 x 14336 48 and 47, 4096 x 11008 45 and 37.5.
+  // to itself.  Several sets of weights in turn, so that they come from HBM: 64 tokens, 4096 x 14336 53 us with 32
+  // columns, 64 with 16, 4096 x 11008 48 and 50, 40 tokens, 4096 x 8000 30 and 33; but 2048 x 4000 15.5 and
+  // 11.8, 512 x 1376 6.7 and 4.1: few columns need the workgroups.  Between them 4096 x 5504 takes 27.5 and 32.0, or
+  // 27.4 and 24.9 from the last-level cache.  16 tokens, 4096 x 14336 45 and 45, 4096 x 11008 39.7 and 35.7.
   if ((TOKENS == 64 && a.cols > 16 * 384) || a.held[0].codes) {
     a.cols > 32 * 256 ? go(std::integral_constant<int, 32>{}, Two{}) : go(std::integral_constant<int, 32>{}, Four{});
   } else if constexpr (TOKENS == 64) {
@@ -437,9 +438,12 @@ bool tiles_fit(Product kind, const ProductLaunch& a) {
 // tiles of 256, 1873 with 128); a tile begins and ends in 8 and 5; partial results move at 5 TB/s,
 // and another launch takes 3.
 // Where no tile of 128 shares its CU, nothing covers its waits; four deep tiles an operand, in LDS that no other
-// workgroup needs, have copies under way for seven steps: 128 tokens, 4096 x 11008, forward 36.5 -> 32.3 us;
-// input gradient of 1024 tokens there 245 -> 164, of 4096 tokens, 768 x 2048, 38.2 -> 31.4. The weight gradient gains
-// nothing (173 and 173, 55.3 and 55.8), short sums lose (300 tokens, 512 x 1376: 6.6 and 7.1, 12.0 and 12.8).
+// workgroup needs, have copies under way for seven steps: 128 tokens, 4096 x 11008, forward 57.7 -> 51.2 us with
+// weights from HBM (35.5 -> 31.8 from the last-level cache); input gradient of 1024 tokens there 251 -> 203, of 4096
+// tokens, 768 x 2048, 49.6 -> 38.5. The weight gradient gains nothing (173 and 173, 55.3 and 55.8), short sums lose (300
+// tokens, 512 x 1376: 6.6 and 7.1, 12.0 and 12.8).
+// The estimate is low where sums are short: 8192 x 512 x 1376 it gives 23 us for the input gradient and 31 for the
+// weight gradient's products, which take 29 to 33 and 32 to 35.
 struct TilePlan {
   int tile;
   u32 splits;
@@ -484,6 +488,9 @@ int tiled_as(const ProductLaunch& a, u32 splits, hipStream_t s) {
 template <class T, Product KIND>
 int tiled_of(const ProductLaunch& a, hipStream_t s) {
   if constexpr (KIND == kForward) {
+    // With weights from HBM, tiles take longer but for the widest layers: one token, 4096 x 11008 35.7 us and 41.3; 64
+    // tokens 512 x 1376 4.1 and 8.3, 2048 x 4000 11.7 and 19.8, 4096 x 5504 32 and 36, 4096 x 11008 48 and 44, 4096 x 14336
+    // 53 and 50 (from the last-level cache 36 and 30, 42 and 37).
     if (a.rows <= 16) return few_as<T, 16>(a, s);
     if (a.rows <= 32) return few_as<T, 32>(a, s);
     if (a.rows <= 64) return few_as<T, 64>(a, s);

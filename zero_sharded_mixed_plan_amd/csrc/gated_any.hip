@@ -48,10 +48,10 @@ __device__ __forceinline__ vec4 unit_of(const char* p, const char* end, u32 n) {
 // each.  The operands go through registers, which takes any address, two steps before they
 // are multiplied, into one of two tiles in LDS; a step has one barrier.  fp32 tiles lie as 16-bit
 // ones do where their rows are of k: a matrix instruction's k are one element of every unit that the
-// lanes read.  4096 tokens of bf16, 2049 x 5503: forward 288 us, input gradient 396, weight
-// gradient 292 (642, 466 and 632 TFLOP/s; two tiles share a CU, and its L1 takes two lines for every 128
+// lanes read.  4096 tokens of bf16, 2049 x 5503: forward 283 us, input gradient 410, weight
+// gradient 292 (653, 451 and 633 TFLOP/s; two tiles share a CU, and its L1 takes two lines for every 128
 // bytes that begin inside one); tiles of 64 x 64, loaded one step ahead under masks, took 640, 1118
-// and 1510.  1024 tokens of fp32, 2048 x 5504: 384 to 433, 370 and 400 us, of a floor of 295 at the rate of fp32
+// and 1510.  1024 tokens of fp32, 2048 x 5504: 392, 358 and 402 us, of a floor of 295 at the rate of fp32
 // matrix instructions.  Rows of the other index, [32 k][SIDE] fp32, are read element by element; every
 // second four of them have their halves of 64 columns in turn exchanged by 32, so that the two halves
 // of a wave meet different banks.
@@ -274,8 +274,8 @@ __global__ __launch_bounds__(256, SIDE == 128 ? 2 : 4) void any_kernel(const Pro
 // ---------------------------------------------------------------------------
 
 // As few_kernel does, every weight is read once, by waves that work alone: a turn of 128 bytes of k of all rows
-// is in registers two turns ahead, and goes through LDS to the lanes that multiply it.  One token of bf16, 4095 x 11007:
-// 33 us (5.4 TB/s), 180 with the tiles above; of fp32, 4096 x 11008: 75 (4.8 TB/s) and 231.
+// is in registers two turns ahead, and goes through LDS to the lanes that multiply it.  One token of bf16, 4095 x 11007, with
+// weights from HBM: 40 us (4.5 TB/s), 59 with the tiles above; of fp32, 4096 x 11008: 74 (4.9 TB/s) and 279.
 template <class T>
 __device__ __forceinline__ f32x4 any_mfma16(vec4 p, vec4 q, f32x4 acc) {
   if constexpr (T::bytes == 2) {
@@ -367,8 +367,8 @@ int few_any_as(const ProductLaunch& a, hipStream_t s) {
     constexpr int C = decltype(columns)::value;
     hipLaunchKernelGGL((few_any_kernel<T, TOKENS, C>), dim3((u32)((a.cols + C - 1) / C)), dim3(256), 0, s, a);
   };
-  // 32 columns are a block of 8 bits; 16 give twice the workgroups (64 tokens of bf16, 4095 x 11007 65 us and 80,
-  // 2047 x 4001 19 and 25; of fp32 218 and 230, 40 and 63)
+  // 32 columns are a block of 8 bits; 16 give twice the workgroups (64 tokens of bf16, 4095 x 11007 83 us and 90,
+  // 2047 x 4001 21 and 29; of fp32 221 and 233, 42 and 66)
   if (a.held[0].codes) go(std::integral_constant<int, 32>{});
   else go(std::integral_constant<int, 16>{});
   return launched("gated projections");
@@ -402,8 +402,10 @@ int join_as(const ProductLaunch& a, u32 splits, hipStream_t s) {
 
 // The side of the tiles and the number of splits of k, by an estimate of microseconds: what a step takes a tile alone on its
 // CU, or a CU full of them (2 of 128, 4 of 64); partial results move at 5 TB/s, and another launch takes 3.  Both
-// products of the backward pass, fp32: 593 tokens, 64 x 5936, 95 us with tiles of 128 alone, 45 with 64, 42 with
-// up to 32 splits in place of 16; 151 tokens, 96 x 10912, 123, 59 and 49; bf16, 91 tokens, 512 x 4674, 26, 22 and 26.
+// products of the backward pass, fp32: 593 tokens, 64 x 5936, 95 us with tiles of 128 alone, 45 with 64, 39 with
+// up to 32 splits in place of 16; 151 tokens, 96 x 10912, 123, 59 and 46; bf16, 91 tokens, 512 x 4674, 26, 22 and 26.
+// The forward pass has neither: more than 64 tokens are tiles of 128 x 64, few of them where hidden is small, each with
+// all of k (65 tokens, 4096 x 256: fp32 274 us, bf16 at odd places 56; 64 tokens in few_any_kernel 69 and 29).
 struct AnyPlan {
   int side;
   u32 splits;

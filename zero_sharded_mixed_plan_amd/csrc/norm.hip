@@ -8,8 +8,8 @@
 // registers for the row's sum.  In 8-bit codes a last bit decides which of two values 2^-4 apart is
 // stored, so rstd and y must not hang on how a row is split over lanes and waves: squares are summed in
 // fp64, and y is computed in pairs of fp32 numbers (good to 2^-44), rounded once to
-// fp32.  8192 x 4096 bf16, without a pause: with a residual 44 us, without 26 (55 and 30 one by one); all in
-// fp64, whose conversions are slow, 36 without.
+// fp32.  8192 x 4096 bf16, three sets of matrices in turn without a pause: with a residual 51 us, without 26 (53 and
+// 28 call by call); all in fp64, whose conversions are slow, 36 without.
 #include <algorithm>
 
 #include "held.h"
@@ -18,8 +18,8 @@ namespace zk {
 namespace {
 
 // A row is WAVES waves of C times 8 columns a lane.  Short rows share a workgroup of four waves.  128 registers,
-// four waves a SIMD: with the 170 that the compiler takes else, 8192 x 8192 bf16 took 112 us with a residual in
-// place of 100, 85 without in place of 59.
+// four waves a SIMD: the compiler takes 129 to 134 else in wide forms with 8-bit results or an fp32 stream, which
+// leaves three (8192 x 8192 bf16 with a residual and 8-bit results 123 us in place of 111, 8192 x 6000 103 and 88).
 constexpr int rms_threads(int waves) { return waves < 4 ? 256 : waves * 64; }
 
 // 1 / sqrt(x): the hardware's estimate and two of Newton's steps, each of which squares its error;
@@ -148,8 +148,9 @@ void rms_as(const RmsLaunch& a, hipStream_t s) {
     const u32 grid = (u32)std::min<int64_t>((a.rows + rows - 1) / rows, 256 * 16 / std::max(W, 4));
     hipLaunchKernelGGL((rms_kernel<XT, RT, W, C, HELD>), dim3(grid), dim3(rms_threads(W)), 0, s, a);
   };
-  // 16 bytes of a row a lane and vector: two groups of 16-bit columns (8192 x 4096 bf16 without a residual 29 us,
-  // with one 33), one of fp32 (4096 x 4096 24 us, with two 30)
+  // 16 bytes of a row a lane and vector: two groups of 16-bit columns (8192 x 4096 bf16 without a residual 26 us,
+  // with one 30; 8192 x 8192 53 and 77; slower only onto an fp32 stream with 8-bit results, 8192 x 4096 94 and
+  // 83), one of fp32 (4096 x 4096 26 us; with two a form spills)
   constexpr int C = XT::bytes == 4 ? 1 : 2;
   using Groups = std::integral_constant<int, C>;
   if (a.cols <= 512) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});

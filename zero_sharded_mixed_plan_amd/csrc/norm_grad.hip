@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kJoinCols * kJoinSlices) void rms_grad_join_kernel(
   store_one(p, a.dweight_type, a.dweight_type == ZERO_F32 ? (float)sum : to_odd(sum));
 }
 
-// 8 columns a lane: with 16, 8192 x 4096 bf16 took 55 us from 8 bits, against 51.
+// 8 columns a lane: with 16, 8192 x 4096 bf16 took 40.5 us from 8 bits, against 37.6, and 45.1 from tensors, against 43.6.
 int waves_of(int64_t cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : cols <= 4096 ? 8 : 16; }
 
 template <class AT, class ST, bool HELD>

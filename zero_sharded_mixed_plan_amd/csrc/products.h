@@ -71,7 +71,9 @@ __device__ __forceinline__ void finish_gated4(const ProductLaunch& a, int64_t r,
 // transposed, 4 rows of 16 columns by 16 lanes: unit j of row k sits at j ^ 2 (k % 4) in
 // tiles of 128; in tiles of 256, whose kernels have no registers for the addresses that this
 // takes, at j ^ 2 (k % 2), with 64 bytes left out before every odd pair of rows.  Either way
-// the 4 rows lie in different banks.
+// the 4 rows that 16 lanes read lie in different banks; what the other lanes of a wave read at the same time is not
+// kept apart from them, and the kernels that read transposed count 1.4 to 2.0 conflict cycles an LDS
+// instruction (the forward pass, whose rows are of k, 0.2).
 constexpr int kStep = 32;
 template <bool DEEP>
 constexpr int kDeep = DEEP ? 2 * kStep : kStep;  // of k, copied at a time

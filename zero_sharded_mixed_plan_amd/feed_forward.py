@@ -168,7 +168,8 @@ def pack8(x: torch.Tensor, *, out: Optional[Packed8] = None) -> Packed8:
 
 
 def unpack8(p: Packed8, dtype: Optional[torch.dtype] = None, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The values that p stands for, exact in bf16 and fp32 (dtype: default out's, or bf16)."""
+    """The values that p stands for, exact in bf16 and fp32 down to their smallest numbers, in fp16 within its range
+    (dtype: default out's, or bf16)."""
     dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
     code = _code(dtype)
     n, cols, _ = _rows(p.codes, "codes")
