@@ -2,9 +2,9 @@
 sums rounded twice, far magnitudes, scales.
 
 Error bounds beside those of test_gpu_feed_forward.py (e = 2^-24):
-  gates of fp32   t = exp(-|z|) within an ulp, 2 e, or 2^-149 where t is a subnormal; 1 + t: t's error, at most
-              half of it relative to the sum, and e; the quotient e; t * (1 / (1 + t)): t's error once more, and
-              e.  p and 1 - p are off by at most P = 6 e of themselves, whatever z (GELU: z in fp64, whose
+  gates of fp32   t = exp(-|z|) = 2^n exp2(f): an ulp, 2 e, and what f, below 1/2, is off, e / 2; or 2^-149 where
+              t is a subnormal.  1 + t, its reciprocal and t times that: e each, and t's error divided by 1 + t.
+              p and 1 - p are off by at most P = 6 e of themselves, whatever z (GELU: z in fp64, whose
               part beyond fp32 costs one more rounding, P = 7 e), and by 2^-148 where they are subnormals.
               With r = P p + 2^-148:  a = g p u: |g u| r + e |a|,  du = da g p: |g da| r + e |du|,
               act' = p + g p (1 - p) slope, slope off by 5 e: D = r + |g| slope ((2 P + 8 e) p (1 - p) + 2^-147)

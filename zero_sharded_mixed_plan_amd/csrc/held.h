@@ -377,24 +377,31 @@ __device__ __forceinline__ Gate gate_16(float g) {
 }
 
 // For fp32 results: from t = exp(-|z|), so that both p and q keep their digits, down to the subnormals; GELU's z is
-// computed in fp64, since exp turns its absolute error into a relative one.  p and q are good to some 4e-7 of themselves;
-// gate_16's would be off by 3e-6 at z = -50, for 0 to 2% less time where the matrices are large (gradient of 2048 x 14336,
-// GELU from 8 bits, 138 us in place of 141; forward pass of 1024 tokens, 2048 x 5504, 382 in place of 389).
+// computed in fp64, since exp turns its absolute error into a relative one.  p and q are good to some 3e-7 of themselves;
+// gate_16's would be off by 3e-6 at z = -50, for up to 1% less time where matrices are large (gradient of 2048 x 14336,
+// GELU from 8 bits, 138 us and 139; forward pass of 1024 tokens, 2048 x 5504, 384 and 388), 2 to 5% where sums are short
+// (4096 tokens, 512 x 1376, 104 and 107, GELU 108; 8192, 256 x 1376, 106 and 110, GELU 114).
 template <int ACT>
 __device__ __forceinline__ Gate gate_32(float g) {
-  float z = g, t, slope = 1.0f;
-  if constexpr (ACT == kSilu) {
-    t = expf(-fabsf(z));
-  } else {
-    const double d = g, w = fmin(fmax(kGeluScale * d * __builtin_fma(kGeluCube * d, d, 1.0), -256.0), 256.0);  // exp(-256) is 0
+  float z = g, rest = 0.0f, slope = 1.0f;  // z + rest
+  if constexpr (ACT == kGelu) {
+    const double d = g, w = fmin(fmax(kGeluScale * d * __builtin_fma(kGeluCube * d, d, 1.0), -256.0), 256.0);
     z = (float)w;
-    const float rest = (float)(w - (double)z);
-    t = expf(-fabsf(z));
-    t = __builtin_fmaf(t, z < 0.0f ? rest : -rest, t);
+    rest = (float)(w - (double)z);
     const float g2 = fminf(g * g, 1e30f);  // beyond, p or q is 0 and the slope only has to stay finite
     slope = (float)kGeluScale * __builtin_fmaf(3.0f * (float)kGeluCube, g2, 1.0f);
   }
-  const float large = 1.0f / (1.0f + t), small = t * large;
+  // exp(-|z|) = 2^n 2^f with n whole and |f| <= 1/2; log2(e) in two parts, so that f is off by 2^-25 at most
+  constexpr double kLog2e = 1.44269504088896340736;
+  constexpr float kHigh = (float)kLog2e, kLow = (float)(kLog2e - (double)kHigh);
+  const float m = fminf(fabsf(z), 256.0f);  // exp(-256) is 0
+  const float n = __builtin_rintf(m * -kHigh);
+  float f = __builtin_fmaf(m, -kLow, __builtin_fmaf(m, -kHigh, -n));
+  if constexpr (ACT == kGelu) f = __builtin_fmaf(z < 0.0f ? rest : -rest, kHigh, f);
+  const float t = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+  // 1 / (1 + t): the hardware's estimate and one of Newton's steps
+  const float sum = 1.0f + t, near = __builtin_amdgcn_rcpf(sum);
+  const float large = __builtin_fmaf(__builtin_fmaf(-sum, near, 1.0f), near, near), small = t * large;
   return z < 0.0f ? Gate{small, large, slope} : Gate{large, small, slope};
 }
 
